@@ -25,7 +25,8 @@ PLSH_F32 = 1
 PLSH_TILE = 128
 PLSH_MAX_S = 64
 PLSH_VARLEN_STATIC_SCRATCH_BYTES = 4 << 20
-DEVERR_BITS = {1: "RANGE", 2: "TABLE", 4: "WINDOW", 8: "TIMEOUT", 16: "SIGMA", 32: "POSITION"}
+DEVERR_BITS = {1: "RANGE", 2: "TABLE", 4: "WINDOW", 8: "TIMEOUT", 16: "SIGMA", 32: "POSITION",
+               64: "SEQUENCE", 128: "PAGE"}
 
 
 class PlshError(RuntimeError):
@@ -85,6 +86,18 @@ def _load() -> ctypes.CDLL:
                                     ctypes.c_size_t, vp, vp, vp, vp]
     lib.plsh_decode_scratch_bytes.restype = ctypes.c_size_t
     lib.plsh_decode_scratch_bytes.argtypes = [i32, i32, i32, i32]
+    i64 = ctypes.c_int64
+    lib.plsh_packed_fwd.restype = i32
+    lib.plsh_packed_fwd.argtypes = [vp, i64, i64, vp, i64, i64, vp, i64, i64, i32, i32, i32, vp, i32, i32, i32, i32, i32, vp,
+                                    vp, vp, vp, vp, vp]
+    lib.plsh_cache_append.restype = i32
+    lib.plsh_cache_append.argtypes = [vp, i64, i64, vp, i64, i64, i32, i32, i32, vp, vp, i32, i32, vp, vp, vp, vp, vp, i32,
+                                      i32, i32, vp, vp]
+    lib.plsh_cache_read.restype = i32
+    lib.plsh_cache_read.argtypes = [vp, vp, vp, vp, vp, i32, i32, i32, i32, i32, vp, vp, i32, i32, i32, vp, vp, vp, vp]
+    lib.plsh_paged_fwd.restype = i32
+    lib.plsh_paged_fwd.argtypes = [vp, i64, i64, i32, i32, i32, vp, vp, i32, i32, i32, i32, vp, vp, vp, vp, vp, i32, i32,
+                                   i32, i32, i32, vp, vp, vp, vp, vp, vp]
     return lib
 
 
@@ -254,8 +267,67 @@ def plsh_attention_bwd_tc(Q, K, V, O, dO, row_sum, B: int, H: int, H_kv: int, n:
                                       _dev_ptr(dV, "dV"), _dev_ptr(err_dev, "err_dev"), _stream_ptr(stream)))
 
 
+def _rows_arg(t, name: str):
+    """(pointer, token stride, head stride) of a CUDA tensor [T][heads][d] whose rows of d elements are contiguous."""
+    if not t.is_cuda:
+        raise ValueError(f"{name} must be a CUDA tensor")
+    if t.dim() != 3 or (t.stride(2) != 1 and t.shape[2] != 1):
+        raise ValueError(f"{name} must be [T][heads][d] with contiguous rows")
+    T, heads, d = t.shape
+    # the stride of a dimension of one element says nothing: torch leaves any number there
+    head = t.stride(1) if heads > 1 else d
+    token = t.stride(0) if T > 1 else heads * max(head, d)
+    return ctypes.c_void_p(t.data_ptr()), token, head
+
+
+def plsh_packed_fwd(Q, K, V, dtype: int, cu_dev, H: int, H_kv: int, d: int, s: int, max_len: int, tile_span_dev, bmask_dev,
+                    O, row_sum, err_dev, stream=None) -> None:
+    """Q [T][H][d], K, V [T][H_kv][d], any strides with contiguous rows; cu_dev int32 [S + 1]."""
+    _check(_lib.plsh_packed_fwd(*_rows_arg(Q, "Q"), *_rows_arg(K, "K"), *_rows_arg(V, "V"), dtype, Q.shape[0],
+                                cu_dev.shape[0] - 1, _dev_ptr(cu_dev, "cu_dev"), H, H_kv, d, s, max_len,
+                                _dev_ptr(tile_span_dev, "tile_span_dev"), _dev_ptr(bmask_dev, "bmask_dev"),
+                                _dev_ptr(O, "O"), _dev_ptr(row_sum, "row_sum"), _dev_ptr(err_dev, "err_dev"),
+                                _stream_ptr(stream)))
+
+
+def plsh_cache_append(K, V, dtype: int, cu_dev, start_dev, H_kv: int, d: int, k_pages, v_pages, k_exp, v_exp,
+                      page_table_dev, err_dev, stream=None) -> None:
+    """K, V [T][H_kv][d] into pages [num_pages][H_kv][page_size][d]; page_table_dev int32 [S][width]."""
+    _check(_lib.plsh_cache_append(*_rows_arg(K, "K"), *_rows_arg(V, "V"), dtype, K.shape[0], cu_dev.shape[0] - 1,
+                                  _dev_ptr(cu_dev, "cu_dev"), _dev_ptr(start_dev, "start_dev"), H_kv, d,
+                                  _dev_ptr(k_pages, "k_pages"), _dev_ptr(v_pages, "v_pages"), _dev_ptr(k_exp, "k_exp"),
+                                  _dev_ptr(v_exp, "v_exp"), _dev_ptr(page_table_dev, "page_table_dev"),
+                                  page_table_dev.shape[1], k_pages.shape[0], k_pages.shape[2],
+                                  _dev_ptr(err_dev, "err_dev"), _stream_ptr(stream)))
+
+
+def plsh_cache_read(k_pages, v_pages, k_exp, v_exp, page_table_dev, cu_dev, start_dev, H_kv: int, d: int, dtype: int, K, V,
+                    err_dev, stream=None) -> None:
+    """Positions start .. of every sequence into packed K, V [T][H_kv][d]."""
+    _check(_lib.plsh_cache_read(_dev_ptr(k_pages, "k_pages"), _dev_ptr(v_pages, "v_pages"), _dev_ptr(k_exp, "k_exp"),
+                                _dev_ptr(v_exp, "v_exp"), _dev_ptr(page_table_dev, "page_table_dev"),
+                                page_table_dev.shape[1], k_pages.shape[0], k_pages.shape[2], K.shape[0],
+                                cu_dev.shape[0] - 1, _dev_ptr(cu_dev, "cu_dev"), _dev_ptr(start_dev, "start_dev"), H_kv,
+                                d, dtype, _dev_ptr(K, "K"), _dev_ptr(V, "V"), _dev_ptr(err_dev, "err_dev"),
+                                _stream_ptr(stream)))
+
+
+def plsh_paged_fwd(Q, dtype: int, cu_dev, start_dev, max_new: int, H: int, H_kv: int, d: int, k_pages, v_pages, k_exp,
+                   v_exp, page_table_dev, s: int, max_len: int, tile_span_dev, bmask_dev, O, row_sum, err_dev,
+                   stream=None) -> None:
+    """Q [T][H][d], any strides with contiguous rows, against pages [num_pages][H_kv][page_size][d]."""
+    _check(_lib.plsh_paged_fwd(*_rows_arg(Q, "Q"), dtype, Q.shape[0], cu_dev.shape[0] - 1, _dev_ptr(cu_dev, "cu_dev"),
+                               _dev_ptr(start_dev, "start_dev"), max_new, H, H_kv, d, _dev_ptr(k_pages, "k_pages"),
+                               _dev_ptr(v_pages, "v_pages"), _dev_ptr(k_exp, "k_exp"), _dev_ptr(v_exp, "v_exp"),
+                               _dev_ptr(page_table_dev, "page_table_dev"), page_table_dev.shape[1], k_pages.shape[0],
+                               k_pages.shape[2], s, max_len, _dev_ptr(tile_span_dev, "tile_span_dev"),
+                               _dev_ptr(bmask_dev, "bmask_dev"), _dev_ptr(O, "O"), _dev_ptr(row_sum, "row_sum"),
+                               _dev_ptr(err_dev, "err_dev"), _stream_ptr(stream)))
+
+
 def decode_device_error(word: int) -> list:
     return [name for bit, name in DEVERR_BITS.items() if word & bit]
 
 
 from .api import HostPipeline, PlshForward, fixed_blocks_table, forward, head_partition  # noqa: E402,F401
+from .serving import PagedCache, PlshServing  # noqa: E402,F401

@@ -31,6 +31,9 @@ SOURCES = [
     "plsh_decode.cu",
     "plsh_bwd.cu",
     "plsh_bwd_tc.cu",
+    "plsh_serve_abi.cu",
+    "plsh_cache.cu",
+    "plsh_serve_simt.cu",
 ]
 
 ARCH = ["-gencode", "arch=compute_100a,code=sm_100a"]

@@ -87,6 +87,42 @@ struct BwdTcArgs {
 int launch_bwd_tc(const BwdTcArgs& a, cudaStream_t st);
 int launch_varlen_spans(const int32_t* ids, int H, int s, int n, int causal, int32_t* spans, cudaStream_t st);
 int launch_attention_simt(const AttnArgs& a, cudaStream_t st);
+
+// ---- serving: packed sequences and the paged cache (plsh_serve.cuh)
+// Tokens [cu[s], cu[s + 1]) belong to sequence s and sit at positions start[s], start[s] + 1, ... of it
+// (start NULL: 0); every position is below max_len, and no sequence has more than max_new tokens.
+struct SeqArgs {
+  const int32_t* cu; const int32_t* start;
+  int S, T, max_len, max_new;
+};
+// Elements between a tensor's tokens and between its heads.
+struct RowStrides {
+  long long token, head;
+};
+// Pages [num_pages][H_kv][2^lg_page][d] of K and V and the page table [S][width]; k_exp, v_exp
+// [num_pages][H_kv][2^lg_page] where the pages hold e4m3 (else NULL).
+struct PageArgs {
+  void* k; void* v;
+  int8_t* k_exp; int8_t* v_exp;
+  const int32_t* table;
+  int width, num_pages, lg_page, H_kv;
+};
+int launch_cache_append(const void* K, const void* V, int dtype, int d, RowStrides ks, RowStrides vs, const SeqArgs& sq,
+                        const PageArgs& pg, uint32_t* err, cudaStream_t st);
+int launch_cache_read(void* K, void* V, int dtype, int d, const SeqArgs& sq, const PageArgs& pg, uint32_t* err,
+                      cudaStream_t st);
+// T~ of the new tokens against packed K, V (pages = false) or against the pages.
+struct ServeArgs {
+  const void* Q; RowStrides qs;
+  const void* K; const void* V; RowStrides ks, vs;
+  bool paged;
+  PageArgs pg;
+  SeqArgs sq;
+  int dtype, H, H_kv, d, s;
+  const int32_t* spans; const void* bmask;  // plsh_window's, causal, over max_len positions
+  void* O; float* row_sum; uint32_t* err;
+};
+int launch_serve_simt(const ServeArgs& a, cudaStream_t st);
 int launch_attention_tc(const AttnArgs& a, cudaStream_t st);
 
 }  // namespace plsh

@@ -1,0 +1,157 @@
+// Entry points of the serving operators (declared in include/plsh.h): argument checks, then the launch.
+#include <cstring>
+
+#include "plsh_internal.h"
+
+namespace plsh {
+namespace {
+
+bool aligned16(const void* p) { return (reinterpret_cast<uintptr_t>(p) & 15u) == 0; }
+
+int check_seqs(const char* fn, int T, int S, const int32_t* cu, int max_len) {
+  if (T < 1 || S < 1) return fail(PLSH_ERR_INVALID_ARG, "%s: need T >= 1 and S >= 1 (T=%d S=%d)", fn, T, S);
+  if (T > (1 << 30) || S > (1 << 20)) return fail(PLSH_ERR_RANGE, "%s: T=%d exceeds 2^30 or S=%d exceeds 2^20", fn, T, S);
+  if (max_len < 1 || max_len > (1 << 30))
+    return fail(PLSH_ERR_INVALID_ARG, "%s: need 1 <= max_len <= 2^30 (max_len=%d)", fn, max_len);
+  if (!cu) return fail(PLSH_ERR_INVALID_ARG, "%s: null pointer", fn);
+  return PLSH_OK;
+}
+
+int check_heads(const char* fn, int T, int H, int H_kv, int dtype, int d) {
+  if (H < 1 || H > 65535 || H_kv < 1 || H % H_kv != 0)
+    return fail(PLSH_ERR_INVALID_ARG, "%s: need 1 <= H <= 65535 and H_kv dividing H (H=%d H_kv=%d)", fn, H, H_kv);
+  if (dtype != PLSH_BF16 && dtype != PLSH_F32) return fail(PLSH_ERR_UNSUPPORTED, "%s: dtype %d", fn, dtype);
+  if (d != 64 && d != 128) return fail(PLSH_ERR_UNSUPPORTED, "%s: head dim %d (64 or 128 supported)", fn, d);
+  if (static_cast<long long>(T) * H > 0x7fffffffLL) return fail(PLSH_ERR_RANGE, "%s: T * H exceeds 2^31", fn);
+  return PLSH_OK;
+}
+
+// Rows of d elements, 16-byte aligned, `token` elements from one token to the next and `head` between heads.
+int check_rows(const char* fn, const char* what, const void* p, int dtype, int d, int heads, int T, long long token,
+               long long head) {
+  if (!p) return fail(PLSH_ERR_INVALID_ARG, "%s: null pointer (%s)", fn, what);
+  const long long es = dtype == PLSH_BF16 ? 2 : 4;
+  if (!aligned16(p) || token * es % 16 != 0 || head * es % 16 != 0)
+    return fail(PLSH_ERR_INVALID_ARG, "%s: %s must be 16-byte aligned, with strides of whole 16 bytes", fn, what);
+  if ((T > 1 && token < d) || (heads > 1 && head < d))
+    return fail(PLSH_ERR_INVALID_ARG, "%s: %s's rows overlap (strides %lld and %lld elements, rows of %d)", fn, what, token, head, d);
+  return PLSH_OK;
+}
+
+int check_pages(const char* fn, const void* k, const void* v, const int8_t* ke, const int8_t* ve, const int32_t* table, int width,
+                int num_pages, int page_size) {
+  if (!k || !v || !table) return fail(PLSH_ERR_INVALID_ARG, "%s: null pointer", fn);
+  if ((ke == nullptr) != (ve == nullptr))
+    return fail(PLSH_ERR_INVALID_ARG, "%s: k_exp and v_exp must both be given (e4m3 pages) or both be NULL", fn);
+  if (!aligned16(k) || !aligned16(v)) return fail(PLSH_ERR_INVALID_ARG, "%s: pages must be 16-byte aligned", fn);
+  if (width < 1 || num_pages < 1)
+    return fail(PLSH_ERR_INVALID_ARG, "%s: need num_pages >= 1 and a page table at least one page wide", fn);
+  if (page_size < 16 || page_size > 256 || (page_size & (page_size - 1)) != 0)
+    return fail(PLSH_ERR_UNSUPPORTED, "%s: page size %d (16, 32, 64, 128 or 256 supported)", fn, page_size);
+  return PLSH_OK;
+}
+
+int lg2(int x) {
+  int l = 0;
+  while ((1 << l) < x) ++l;
+  return l;
+}
+
+PageArgs pages(const void* k, const void* v, const int8_t* ke, const int8_t* ve, const int32_t* table, int width, int num_pages,
+               int page_size, int H_kv) {
+  return PageArgs{const_cast<void*>(k), const_cast<void*>(v), const_cast<int8_t*>(ke), const_cast<int8_t*>(ve),
+                  table, width, num_pages, lg2(page_size), H_kv};
+}
+
+int check_plan(const char* fn, int s, const int32_t* spans, const void* bmask, const void* O, const float* row_sum,
+               const uint32_t* err) {
+  if (s < 1 || s > PLSH_MAX_S) return fail(PLSH_ERR_INVALID_ARG, "%s: need 1 <= s <= %d (s=%d)", fn, PLSH_MAX_S, s);
+  if (!spans || !bmask || !O || !row_sum || !err) return fail(PLSH_ERR_INVALID_ARG, "%s: null pointer", fn);
+  if (!aligned16(O)) return fail(PLSH_ERR_INVALID_ARG, "%s: O must be 16-byte aligned", fn);
+  return PLSH_OK;
+}
+
+}  // namespace
+}  // namespace plsh
+
+using plsh::fail;
+
+extern "C" int plsh_packed_fwd(const void* Q, int64_t q_token, int64_t q_head, const void* K, int64_t k_token, int64_t k_head,
+                               const void* V, int64_t v_token, int64_t v_head, int dtype, int T, int S,
+                               const int32_t* cu_dev, int H, int H_kv, int d, int s, int max_len,
+                               const int32_t* tile_span_dev, const void* bmask_dev, void* O, float* row_sum,
+                               uint32_t* err_dev, void* stream) {
+  const char* fn = "plsh_packed_fwd";
+  if (int rc = plsh::check_seqs(fn, T, S, cu_dev, max_len)) return rc;
+  if (int rc = plsh::check_heads(fn, T, H, H_kv, dtype, d)) return rc;
+  if (int rc = plsh::check_rows(fn, "Q", Q, dtype, d, H, T, q_token, q_head)) return rc;
+  if (int rc = plsh::check_rows(fn, "K", K, dtype, d, H_kv, T, k_token, k_head)) return rc;
+  if (int rc = plsh::check_rows(fn, "V", V, dtype, d, H_kv, T, v_token, v_head)) return rc;
+  if (int rc = plsh::check_plan(fn, s, tile_span_dev, bmask_dev, O, row_sum, err_dev)) return rc;
+  plsh::ServeArgs a{};
+  a.Q = Q; a.qs = {q_token, q_head};
+  a.K = K; a.ks = {k_token, k_head};
+  a.V = V; a.vs = {v_token, v_head};
+  a.paged = false;
+  a.pg.H_kv = H_kv;
+  a.sq = {cu_dev, nullptr, S, T, max_len, T};
+  a.dtype = dtype; a.H = H; a.H_kv = H_kv; a.d = d; a.s = s;
+  a.spans = tile_span_dev; a.bmask = bmask_dev;
+  a.O = O; a.row_sum = row_sum; a.err = err_dev;
+  return plsh::launch_serve_simt(a, static_cast<cudaStream_t>(stream));
+}
+
+extern "C" int plsh_cache_append(const void* K, int64_t k_token, int64_t k_head, const void* V, int64_t v_token, int64_t v_head,
+                                 int dtype, int T, int S, const int32_t* cu_dev, const int32_t* start_dev, int H_kv, int d,
+                                 void* k_pages, void* v_pages, int8_t* k_exp, int8_t* v_exp, const int32_t* page_table_dev,
+                                 int table_width, int num_pages, int page_size, uint32_t* err_dev, void* stream) {
+  const char* fn = "plsh_cache_append";
+  if (int rc = plsh::check_seqs(fn, T, S, cu_dev, 1 << 30)) return rc;
+  if (int rc = plsh::check_heads(fn, T, H_kv, H_kv, dtype, d)) return rc;
+  if (int rc = plsh::check_rows(fn, "K", K, dtype, d, H_kv, T, k_token, k_head)) return rc;
+  if (int rc = plsh::check_rows(fn, "V", V, dtype, d, H_kv, T, v_token, v_head)) return rc;
+  if (int rc = plsh::check_pages(fn, k_pages, v_pages, k_exp, v_exp, page_table_dev, table_width, num_pages, page_size)) return rc;
+  if (!start_dev || !err_dev) return fail(PLSH_ERR_INVALID_ARG, "%s: null pointer", fn);
+  return plsh::launch_cache_append(K, V, dtype, d, {k_token, k_head}, {v_token, v_head}, {cu_dev, start_dev, S, T, 1 << 30, T},
+                                   plsh::pages(k_pages, v_pages, k_exp, v_exp, page_table_dev, table_width, num_pages, page_size, H_kv),
+                                   err_dev, static_cast<cudaStream_t>(stream));
+}
+
+extern "C" int plsh_cache_read(const void* k_pages, const void* v_pages, const int8_t* k_exp, const int8_t* v_exp,
+                               const int32_t* page_table_dev, int table_width, int num_pages, int page_size, int T, int S,
+                               const int32_t* cu_dev, const int32_t* start_dev, int H_kv, int d, int dtype, void* K, void* V,
+                               uint32_t* err_dev, void* stream) {
+  const char* fn = "plsh_cache_read";
+  if (int rc = plsh::check_seqs(fn, T, S, cu_dev, 1 << 30)) return rc;
+  if (int rc = plsh::check_heads(fn, T, H_kv, H_kv, dtype, d)) return rc;
+  if (int rc = plsh::check_pages(fn, k_pages, v_pages, k_exp, v_exp, page_table_dev, table_width, num_pages, page_size)) return rc;
+  if (!start_dev || !K || !V || !err_dev) return fail(PLSH_ERR_INVALID_ARG, "%s: null pointer", fn);
+  if (!plsh::aligned16(K) || !plsh::aligned16(V)) return fail(PLSH_ERR_INVALID_ARG, "%s: K and V must be 16-byte aligned", fn);
+  return plsh::launch_cache_read(K, V, dtype, d, {cu_dev, start_dev, S, T, 1 << 30, T},
+                                 plsh::pages(k_pages, v_pages, k_exp, v_exp, page_table_dev, table_width, num_pages, page_size, H_kv),
+                                 err_dev, static_cast<cudaStream_t>(stream));
+}
+
+extern "C" int plsh_paged_fwd(const void* Q, int64_t q_token, int64_t q_head, int dtype, int T, int S, const int32_t* cu_dev,
+                              const int32_t* start_dev, int max_new, int H, int H_kv, int d, const void* k_pages,
+                              const void* v_pages, const int8_t* k_exp, const int8_t* v_exp, const int32_t* page_table_dev,
+                              int table_width, int num_pages, int page_size, int s, int max_len, const int32_t* tile_span_dev,
+                              const void* bmask_dev, void* O, float* row_sum, uint32_t* err_dev, void* stream) {
+  const char* fn = "plsh_paged_fwd";
+  if (int rc = plsh::check_seqs(fn, T, S, cu_dev, max_len)) return rc;
+  if (int rc = plsh::check_heads(fn, T, H, H_kv, dtype, d)) return rc;
+  if (int rc = plsh::check_rows(fn, "Q", Q, dtype, d, H, T, q_token, q_head)) return rc;
+  if (int rc = plsh::check_pages(fn, k_pages, v_pages, k_exp, v_exp, page_table_dev, table_width, num_pages, page_size)) return rc;
+  if (int rc = plsh::check_plan(fn, s, tile_span_dev, bmask_dev, O, row_sum, err_dev)) return rc;
+  if (!start_dev) return fail(PLSH_ERR_INVALID_ARG, "%s: null pointer", fn);
+  if (max_new < 1) return fail(PLSH_ERR_INVALID_ARG, "%s: need max_new >= 1 (max_new=%d)", fn, max_new);
+  plsh::ServeArgs a{};
+  a.Q = Q; a.qs = {q_token, q_head};
+  a.paged = true;
+  a.pg = plsh::pages(k_pages, v_pages, k_exp, v_exp, page_table_dev, table_width, num_pages, page_size, H_kv);
+  a.sq = {cu_dev, start_dev, S, T, max_len, max_new};
+  a.dtype = dtype; a.H = H; a.H_kv = H_kv; a.d = d; a.s = s;
+  a.spans = tile_span_dev; a.bmask = bmask_dev;
+  a.O = O; a.row_sum = row_sum; a.err = err_dev;
+  return plsh::launch_serve_simt(a, static_cast<cudaStream_t>(stream));
+}

@@ -1,0 +1,251 @@
+"""Serving with Positional-LSH attention: packed prompts, a paged cache and attention against it.
+
+PlshServing keeps what all sequences share, the table's windows and masks for positions
+0 .. max_len - 1, and runs T~ (causal) over
+  attend_packed   whole prompts of different lengths, packed without padding  (plsh_packed_fwd)
+  attend_paged    new tokens of every sequence against a paged cache          (plsh_paged_fwd)
+PagedCache holds the pages and moves rows in and out of them
+  append          new tokens' K and V, quantised to e4m3 or copied            (plsh_cache_append)
+  read            a range of every sequence as packed tensors                 (plsh_cache_read)
+Every call is asynchronous on `stream` (default: the current stream of the tensors' device), makes no
+host copies and can be captured into a CUDA graph. Data errors (a malformed sequence, a page
+outside the pool) are reported by check().
+"""
+from __future__ import annotations
+
+from typing import Optional, Sequence, Tuple
+
+import numpy as np
+import torch
+
+from . import (PLSH_BF16, PLSH_F32, PLSH_MAX_S, PLSH_TILE, PlshError, decode_device_error, plsh_cache_append,
+               plsh_cache_read, plsh_draw_table_heads, plsh_packed_fwd, plsh_paged_fwd, plsh_window_from_table)
+
+_CODES = {torch.bfloat16: PLSH_BF16, torch.float32: PLSH_F32}
+
+
+def _rows(t: torch.Tensor, name: str, shape: Tuple[Optional[int], ...], dtypes, device) -> None:
+    """t is [tokens][heads][d] on `device`, with rows that the kernels can load 16 bytes at a time."""
+    if t.dim() != len(shape) or any(b is not None and a != b for a, b in zip(t.shape, shape)):
+        raise ValueError(f"{name} must have shape {tuple('T' if b is None else b for b in shape)}, got {tuple(t.shape)}")
+    if t.dtype not in dtypes or t.device != device:
+        raise ValueError(f"{name} must be {' or '.join(map(str, dtypes))} on {device}, got {t.dtype} on {t.device}")
+    if t.numel() == 0:
+        return
+    step = 16 // t.element_size()
+    if t.stride(-1) != 1 or t.data_ptr() % 16 or any(n > 1 and (s % step or s < t.shape[-1])
+                                                     for n, s in zip(t.shape[:-1], t.stride()[:-1])):
+        raise ValueError(f"{name} must have contiguous, 16-byte aligned rows that do not overlap")
+
+
+def _ints(t: torch.Tensor, name: str, dims: int, device) -> None:
+    if t.dim() != dims or t.dtype != torch.int32 or t.device != device or not t.is_contiguous():
+        raise ValueError(f"{name} must be a contiguous int32 tensor of {dims} dimension(s) on {device}")
+
+
+def _sequences(cu_seqlens: torch.Tensor, start: Optional[torch.Tensor], page_table: Optional[torch.Tensor], device) -> int:
+    _ints(cu_seqlens, "cu_seqlens", 1, device)
+    S = cu_seqlens.shape[0] - 1
+    if S < 0:
+        raise ValueError("cu_seqlens must hold one entry more than there are sequences")
+    if start is not None:
+        _ints(start, "start", 1, device)
+        if start.shape[0] != S:
+            raise ValueError(f"start must hold one entry per sequence ({S})")
+    if page_table is not None:
+        _ints(page_table, "page_table", 2, device)
+        if page_table.shape[0] != S or page_table.shape[1] < 1:
+            raise ValueError(f"page_table must be [{S}][pages] with at least one page per sequence")
+    return S
+
+
+class _Errors:
+    """The device error word of an object's calls."""
+
+    err: torch.Tensor
+
+    def reset_errors(self) -> None:
+        self.err.zero_()
+
+    def device_errors(self) -> list:
+        """Synchronises and decodes the device error word."""
+        torch.cuda.synchronize(self.err.device)
+        return decode_device_error(int(self.err[0].item()) & 0xFFFFFFFF)
+
+    def check(self) -> None:
+        errs = self.device_errors()
+        if errs:
+            raise PlshError(-1, "device reported " + ",".join(errs))
+
+
+class PagedCache(_Errors):
+    """K and V of many sequences in pages [num_pages][H_kv][page_size][d].
+
+    dtype torch.float8_e4m3fn: each row is held as e4m3 values times a power of two, whose exponent is in
+    k_exp, v_exp (int8 [num_pages][H_kv][page_size]); torch.bfloat16 or torch.float32: rows as they are.
+    Which page holds which positions is the caller's: every call takes a page table int32 [S][pages].
+    """
+
+    def __init__(self, k_pages: torch.Tensor, v_pages: torch.Tensor, k_exp: Optional[torch.Tensor] = None,
+                 v_exp: Optional[torch.Tensor] = None):
+        if k_pages.dim() != 4 or k_pages.shape != v_pages.shape or k_pages.dtype != v_pages.dtype:
+            raise ValueError("k_pages and v_pages must be alike: [num_pages][H_kv][page_size][d]")
+        self.num_pages, self.H_kv, self.page_size, self.d = k_pages.shape
+        self.dtype, self.device = k_pages.dtype, k_pages.device
+        if self.dtype not in (torch.float8_e4m3fn, torch.bfloat16, torch.float32):
+            raise ValueError("pages must be float8_e4m3fn, bfloat16 or float32")
+        if self.page_size not in (16, 32, 64, 128, 256) or self.d not in (64, 128) or self.num_pages < 1 or self.H_kv < 1:
+            raise ValueError("need pages of 16, 32, 64, 128 or 256 rows of 64 or 128 elements")
+        self.quantised = self.dtype == torch.float8_e4m3fn
+        if (k_exp is not None) != self.quantised or (v_exp is not None) != self.quantised:
+            raise ValueError("e4m3 pages need k_exp and v_exp, other pages take none")
+        for t, nm in ((k_pages, "k_pages"), (v_pages, "v_pages"), (k_exp, "k_exp"), (v_exp, "v_exp")):
+            if t is None:
+                continue
+            if not t.is_cuda or t.device != self.device or not t.is_contiguous():
+                raise ValueError(f"{nm} must be a contiguous CUDA tensor on {self.device}")
+            if nm.endswith("exp") and (t.dtype != torch.int8 or t.shape != k_pages.shape[:3]):
+                raise ValueError(f"{nm} must be int8 [num_pages][H_kv][page_size]")
+        self.k_pages, self.v_pages, self.k_exp, self.v_exp = k_pages, v_pages, k_exp, v_exp
+        self.err = torch.zeros((4,), dtype=torch.int32, device=self.device)
+
+    @classmethod
+    def empty(cls, num_pages: int, H_kv: int, page_size: int, d: int, dtype: torch.dtype = torch.float8_e4m3fn,
+              device: str = "cuda") -> "PagedCache":
+        """A cache with nothing in it (the pages' contents are not set)."""
+        shape = (num_pages, H_kv, page_size, d)
+        exps = [torch.empty(shape[:3], dtype=torch.int8, device=device) for _ in range(2)] if dtype == torch.float8_e4m3fn else [None] * 2
+        return cls(torch.empty(shape, dtype=dtype, device=device), torch.empty(shape, dtype=dtype, device=device), *exps)
+
+    def append(self, k: torch.Tensor, v: torch.Tensor, page_table: torch.Tensor, cu_seqlens: torch.Tensor,
+               start: torch.Tensor, stream: Optional[torch.cuda.Stream] = None) -> None:
+        """Writes rows [cu[s], cu[s + 1]) of k, v [T][H_kv][d] to positions start[s] .. of sequence s."""
+        dtypes = tuple(_CODES) if self.quantised else (self.dtype,)
+        _rows(k, "k", (None, self.H_kv, self.d), dtypes, self.device)
+        _rows(v, "v", (k.shape[0], self.H_kv, self.d), (k.dtype,), self.device)
+        if _sequences(cu_seqlens, start, page_table, self.device) == 0 or k.shape[0] == 0:
+            return
+        with torch.cuda.device(self.device):
+            plsh_cache_append(k, v, _CODES[k.dtype], cu_seqlens, start, self.H_kv, self.d, self.k_pages, self.v_pages,
+                              self.k_exp, self.v_exp, page_table, self.err, stream)
+
+    def read(self, page_table: torch.Tensor, cu_seqlens: torch.Tensor, start: torch.Tensor, total: int,
+             dtype: Optional[torch.dtype] = None, out: Optional[Tuple[torch.Tensor, torch.Tensor]] = None,
+             stream: Optional[torch.cuda.Stream] = None) -> Tuple[torch.Tensor, torch.Tensor]:
+        """Positions start[s] .. of every sequence as packed K, V [total][H_kv][d], sequence s in rows [cu[s], cu[s + 1]).
+
+        total is the rows of the result, at least cu[S] (cu_seqlens stays on the device); rows of no sequence are left as
+        they are. dtype: bfloat16 (default) or float32 for e4m3 pages, the pages' own else. out: tensors to fill."""
+        dtype = dtype if dtype is not None else (out[0].dtype if out is not None else torch.bfloat16 if self.quantised else self.dtype)
+        if dtype not in (tuple(_CODES) if self.quantised else (self.dtype,)):
+            raise ValueError(f"cannot read {self.dtype} pages as {dtype}")
+        S = _sequences(cu_seqlens, start, page_table, self.device)
+        if total < 0:
+            raise ValueError("total must be >= 0")
+        with torch.cuda.device(self.device):
+            st = torch.cuda.current_stream() if stream is None else stream
+            if out is None:
+                with torch.cuda.stream(st):
+                    out = tuple(torch.empty((total, self.H_kv, self.d), dtype=dtype, device=self.device) for _ in range(2))
+            for t, nm in zip(out, ("K", "V")):
+                _rows(t, nm, (total, self.H_kv, self.d), (dtype,), self.device)
+                if not t.is_contiguous():
+                    raise ValueError(f"{nm} must be contiguous")
+            if S and total:
+                plsh_cache_read(self.k_pages, self.v_pages, self.k_exp, self.v_exp, page_table, cu_seqlens, start, self.H_kv,
+                                self.d, _CODES[dtype], out[0], out[1], self.err, st)
+        return out
+
+
+class PlshServing(_Errors):
+    """T~ (causal) for sequences of up to max_len positions, all with one table."""
+
+    def __init__(self, H: int, H_kv: int, max_len: int, d: int, s: int, sigma: Sequence[float], seed: int = 0,
+                 dtype: torch.dtype = torch.bfloat16, device: str = "cuda", head_offset: int = 0,
+                 table: Optional[np.ndarray] = None):
+        """sigma, seed, head_offset, table: as PlshForward's (table: float64 [H][s][2] instead of a drawn one)."""
+        if dtype not in _CODES:
+            raise ValueError("dtype must be torch.bfloat16 or torch.float32")
+        if H < 1 or H_kv < 1 or H % H_kv or max_len < 1 or d not in (64, 128) or not 1 <= s <= PLSH_MAX_S:
+            raise ValueError(f"need H_kv dividing H, max_len >= 1, d 64 or 128 and 1 <= s <= {PLSH_MAX_S}")
+        self.H, self.H_kv, self.max_len, self.d, self.s = H, H_kv, max_len, d, s
+        self.dtype, self.device = dtype, torch.device(device)
+        if self.device.type != "cuda":
+            raise ValueError("device must be a CUDA device")
+        if self.device.index is None:
+            self.device = torch.device("cuda", torch.cuda.current_device())
+        self.sigma_host = np.ascontiguousarray(sigma, dtype=np.float64)
+        if self.sigma_host.shape != (H,):
+            raise ValueError("sigma must hold one value per query head")
+        self.table_host = np.empty((H, s, 2), dtype=np.float64)
+        if table is None:
+            plsh_draw_table_heads(int(seed), int(head_offset), H, s, self.sigma_host, self.table_host)
+        else:
+            t = np.ascontiguousarray(table, dtype=np.float64)
+            if t.shape != (H, s, 2):
+                raise ValueError("table must be float64 [H][s][2]")
+            self.table_host[...] = t
+        with torch.cuda.device(self.device):
+            self.err = torch.zeros((4,), dtype=torch.int32, device=self.device)
+            self.table_dev = torch.from_numpy(self.table_host).to(self.device)
+            self.bmax = torch.empty((H,), dtype=torch.int32, device=self.device)
+            self.spans = torch.empty((H, -(-max_len // PLSH_TILE), 2), dtype=torch.int32, device=self.device)
+            self.bmask = torch.empty((H, max_len), dtype=torch.int32 if s <= 32 else torch.int64, device=self.device)
+            plsh_window_from_table(self.table_dev, H, s, max_len, 1, self.bmax, self.spans, self.bmask, self.err)
+            self.check()  # waits for the plan, so that any stream may use it from here on
+
+    def _outputs(self, T: int, out, st) -> Tuple[torch.Tensor, torch.Tensor]:
+        if out is None:
+            with torch.cuda.stream(st):
+                return (torch.empty((T, self.H, self.d), dtype=self.dtype, device=self.device),
+                        torch.empty((T, self.H), dtype=torch.float32, device=self.device))
+        O, row_sum = out
+        _rows(O, "O", (T, self.H, self.d), (self.dtype,), self.device)
+        if row_sum.shape != (T, self.H) or row_sum.dtype != torch.float32 or row_sum.device != self.device \
+                or not row_sum.is_contiguous() or not O.is_contiguous():
+            raise ValueError(f"out must be contiguous {self.dtype} [T][H][d] and float32 [T][H] on {self.device}")
+        return O, row_sum
+
+    def attend_packed(self, q: torch.Tensor, k: torch.Tensor, v: torch.Tensor, cu_seqlens: torch.Tensor,
+                      out: Optional[Tuple[torch.Tensor, torch.Tensor]] = None,
+                      stream: Optional[torch.cuda.Stream] = None) -> Tuple[torch.Tensor, torch.Tensor]:
+        """T~ of whole prompts: q [T][H][d], k, v [T][H_kv][d], sequence s in tokens [cu[s], cu[s + 1]).
+
+        Returns new tensors O [T][H][d] and row_sum [T][H] (float32), or fills `out`; tokens of no sequence (behind the
+        last) are left as they are. Views with contiguous rows, as a fused QKV projection gives, need no copy."""
+        _rows(q, "q", (None, self.H, self.d), (self.dtype,), self.device)
+        _rows(k, "k", (q.shape[0], self.H_kv, self.d), (self.dtype,), self.device)
+        _rows(v, "v", (q.shape[0], self.H_kv, self.d), (self.dtype,), self.device)
+        S = _sequences(cu_seqlens, None, None, self.device)
+        with torch.cuda.device(self.device):
+            st = torch.cuda.current_stream() if stream is None else stream
+            O, row_sum = self._outputs(q.shape[0], out, st)
+            if S and q.shape[0]:
+                plsh_packed_fwd(q, k, v, _CODES[self.dtype], cu_seqlens, self.H, self.H_kv, self.d, self.s, self.max_len,
+                                self.spans, self.bmask, O, row_sum, self.err, st)
+        return O, row_sum
+
+    def attend_paged(self, q: torch.Tensor, cache: PagedCache, page_table: torch.Tensor, cu_seqlens: torch.Tensor,
+                     start: torch.Tensor, max_new: Optional[int] = None,
+                     out: Optional[Tuple[torch.Tensor, torch.Tensor]] = None,
+                     stream: Optional[torch.cuda.Stream] = None) -> Tuple[torch.Tensor, torch.Tensor]:
+        """T~ of new tokens against the cache: q [T][H][d], token t of sequence s at position start[s] + t - cu[s].
+
+        The cache holds the new tokens' own K and V already (append first). max_new: the most new tokens of a sequence
+        where the caller knows it (1 when decoding); it chooses the kernels. Returns as attend_packed."""
+        _rows(q, "q", (None, self.H, self.d), (self.dtype,), self.device)
+        if cache.device != self.device or cache.H_kv != self.H_kv or cache.d != self.d or \
+                (not cache.quantised and cache.dtype != self.dtype):
+            raise ValueError("the cache's device, heads, head dim or type do not match the plan")
+        S = _sequences(cu_seqlens, start, page_table, self.device)
+        T = q.shape[0]
+        if max_new is not None and max_new < 1:
+            raise ValueError("max_new must be >= 1")
+        with torch.cuda.device(self.device):
+            st = torch.cuda.current_stream() if stream is None else stream
+            O, row_sum = self._outputs(T, out, st)
+            if S and T:
+                plsh_paged_fwd(q, _CODES[self.dtype], cu_seqlens, start, T if max_new is None else min(max_new, T), self.H,
+                               self.H_kv, self.d, cache.k_pages, cache.v_pages, cache.k_exp, cache.v_exp, page_table, self.s,
+                               self.max_len, self.spans, self.bmask, O, row_sum, self.err, st)
+        return O, row_sum

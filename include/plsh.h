@@ -63,6 +63,8 @@ extern "C" {
 #define PLSH_DEVERR_TIMEOUT  8u  /* a bounded wait on a barrier gave up (the kernel returned early) */
 #define PLSH_DEVERR_SIGMA   16u  /* a per-head sigma not finite and > 0 */
 #define PLSH_DEVERR_POSITION 32u /* a decode query position outside [0, n) */
+#define PLSH_DEVERR_SEQUENCE 64u /* a packed sequence outside its tensor, or past max_len or max_new */
+#define PLSH_DEVERR_PAGE    128u /* a page that a call needs is outside the page table or the pool */
 
 #define PLSH_TILE   128   /* query/key tile height of the windows */
 #define PLSH_MAX_S  64    /* most hashes per head (one bit each in a 64-bit boundary mask) */
@@ -469,6 +471,99 @@ PLSH_API int plsh_attention_bwd_tc(const void* Q, const void* K, const void* V, 
                                    const void* bmask_dev, const int32_t* tile_span_dev,
                                    const int32_t* key_span_dev, int causal, float* delta_dev, void* dQ, void* dK,
                                    void* dV, uint32_t* err_dev, void* stream);
+
+/*
+ * Serving: packed prompts, a paged cache, and attention against it.
+ *
+ * The four entry points below run the same T~ as plsh_attention_fwd (causal)
+ * where a server has it: prompts of different lengths packed without padding,
+ * and new tokens against a cache kept in pages. Conventions they share:
+ *   - Packed tokens: tokens [cu[s], cu[s + 1]) of T belong to sequence s of S
+ *     (cu_dev: int32 [S + 1], non-decreasing, within [0, T]; a sequence may
+ *     be empty). Token t of sequence s sits at position start[s] + t - cu[s]
+ *     (start_dev: int32 [S], the tokens that s has before; plsh_packed_fwd:
+ *     0). Tokens outside every sequence are neither read for another's result
+ *     nor written.
+ *   - Strides: Q, K and V hold rows of d elements, X_token elements from one
+ *     token to the next and X_head from one head to the next, each a
+ *     multiple of 16 bytes and at least d (the views that a fused QKV
+ *     projection gives, or head-major storage, need no copy). Outputs are
+ *     dense [T][H][d] and [T][H].
+ *   - max_len: positions of the plan: bmask_dev [H][max_len] and
+ *     tile_span_dev [H][ceil(max_len/128)][2] come from plsh_window (or
+ *     plsh_window_from_table) with n = max_len and causal = 1, once for all
+ *     calls. A position's block depends on the position only, so one plan
+ *     serves every sequence.
+ *   - Pages: k_pages, v_pages [num_pages][H_kv][page_size][d], page_size a
+ *     power of two in 16..256; position p of sequence s lies in page
+ *     page_table[s][p / page_size] (page_table_dev: int32 [S][table_width]) at
+ *     place p % page_size. With k_exp and v_exp, int8
+ *     [num_pages][H_kv][page_size], the pages hold e4m3 bytes and a row's
+ *     values are byte * 2^exp; with both NULL they hold the call's dtype.
+ *     Entries of the table that no position of the call needs are not read.
+ *   - err_dev: PLSH_DEVERR_SEQUENCE for a malformed sequence (it is skipped),
+ *     PLSH_DEVERR_PAGE for a needed page outside the table or the pool (a
+ *     row is then not written, or read as zeros).
+ *   - K and V must be finite: a NaN or an infinity may reach any row of
+ *     its own sequence near it, weighted or not, but no other sequence.
+ *   - Two sequences that share pages may read them in one call; a call in
+ *     which two tokens are written to one place leaves either.
+ *
+ * plsh_packed_fwd -- T~ of whole prompts.
+ *
+ * Cites: as plsh_attention_fwd (Methodology 2 and 3). For token t of
+ * sequence s, with i its position:
+ *   O[t][h]       = sum_{j <= i} c_ij e^{S_ij} V_j / sum_{j <= i} c_ij e^{S_ij},
+ *   row_sum[t][h] = ln( sum_{j <= i} (c_ij / s) e^{S_ij} ),
+ * j over the sequence's own positions.
+ *   O        [T][H][d] out, row_sum [T][H] float32 out.
+ */
+PLSH_API int plsh_packed_fwd(const void* Q, int64_t q_token, int64_t q_head, const void* K, int64_t k_token,
+                             int64_t k_head, const void* V, int64_t v_token, int64_t v_head, int dtype, int T, int S,
+                             const int32_t* cu_dev, int H, int H_kv, int d, int s, int max_len,
+                             const int32_t* tile_span_dev, const void* bmask_dev, void* O, float* row_sum,
+                             uint32_t* err_dev, void* stream);
+
+/*
+ * plsh_cache_append -- new tokens' K and V rows into their pages.
+ *
+ * The pages (of the method's explainer) have no counterpart: this is how a
+ * server keeps what plsh_decode_fwd calls the cache. With k_exp and v_exp a
+ * row x becomes RN_e4m3(x 2^-e) and e, the least integer >= -126 with
+ * max|x| <= 448 * 2^e (over x's finite values; NaN and infinities are stored as
+ * NaN). Else the row is copied.
+ */
+PLSH_API int plsh_cache_append(const void* K, int64_t k_token, int64_t k_head, const void* V, int64_t v_token,
+                               int64_t v_head, int dtype, int T, int S, const int32_t* cu_dev,
+                               const int32_t* start_dev, int H_kv, int d, void* k_pages, void* v_pages, int8_t* k_exp,
+                               int8_t* v_exp, const int32_t* page_table_dev, int table_width, int num_pages,
+                               int page_size, uint32_t* err_dev, void* stream);
+
+/*
+ * plsh_cache_read -- positions start[s] .. start[s] + cu[s + 1] - cu[s] - 1 of
+ * every sequence as packed rows K, V [T][H_kv][d] (dense, out) of `dtype`:
+ * byte * 2^exp rounded once to dtype, or the pages' rows themselves.
+ */
+PLSH_API int plsh_cache_read(const void* k_pages, const void* v_pages, const int8_t* k_exp, const int8_t* v_exp,
+                             const int32_t* page_table_dev, int table_width, int num_pages, int page_size, int T, int S,
+                             const int32_t* cu_dev, const int32_t* start_dev, int H_kv, int d, int dtype, void* K, void* V,
+                             uint32_t* err_dev, void* stream);
+
+/*
+ * plsh_paged_fwd -- T~ of a chunk of new tokens of every sequence (one token
+ * when decoding) against the pages, which hold the sequence's positions up to
+ * and including the chunk's own (append first). Results as plsh_packed_fwd,
+ * with the pages' K and V.
+ *   max_new   no sequence has more new tokens than this (else
+ *             PLSH_DEVERR_SEQUENCE, and it is skipped). The call chooses its kernels by it,
+ *             so give the largest length where it is known, or T.
+ */
+PLSH_API int plsh_paged_fwd(const void* Q, int64_t q_token, int64_t q_head, int dtype, int T, int S,
+                            const int32_t* cu_dev, const int32_t* start_dev, int max_new, int H, int H_kv, int d,
+                            const void* k_pages, const void* v_pages, const int8_t* k_exp, const int8_t* v_exp,
+                            const int32_t* page_table_dev, int table_width, int num_pages, int page_size, int s, int max_len,
+                            const int32_t* tile_span_dev, const void* bmask_dev, void* O, float* row_sum,
+                            uint32_t* err_dev, void* stream);
 
 #ifdef __cplusplus
 }

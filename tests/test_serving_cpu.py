@@ -1,0 +1,85 @@
+"""The serving entry points without a GPU: the host-side checks refuse bad arguments before any device work, and the
+plain implementation that the GPU tests compare with agrees with the oracle."""
+import ctypes
+
+import numpy as np
+import pytest
+import torch
+
+import oracle
+from tests import serving_plain as plain
+
+FAKE = ctypes.c_void_p(1 << 20)  # never dereferenced: the checks fail first
+NULL = None
+
+
+@pytest.fixture(scope="module")
+def plsh():
+    import alibi_positional_lsh_b200 as m
+    return m
+
+
+def _packed(Q=FAKE, qt=512, qh=128, kt=256, dtype=0, T=10, S=2, cu=FAKE, H=4, H_kv=2, d=128, s=20, max_len=100, spans=FAKE, O=FAKE):
+    return (Q, qt, qh, FAKE, kt, 128, FAKE, 256, 128, dtype, T, S, cu, H, H_kv, d, s, max_len, spans, FAKE, O, FAKE, FAKE, NULL)
+
+
+def _append(K=FAKE, dtype=0, T=10, S=2, start=FAKE, d=128, kp=FAKE, ke=FAKE, ve=FAKE, width=3, pages=8, page=64):
+    return (K, 256, 128, FAKE, 256, 128, dtype, T, S, FAKE, start, 2, d, kp, FAKE, ke, ve, FAKE, width, pages, page, FAKE, NULL)
+
+
+def _read(kp=FAKE, ke=FAKE, ve=FAKE, width=3, pages=8, page=64, T=10, start=FAKE, d=128, dtype=0, K=FAKE):
+    return (kp, FAKE, ke, ve, FAKE, width, pages, page, T, 2, FAKE, start, 2, d, dtype, K, FAKE, FAKE, NULL)
+
+
+def _paged(Q=FAKE, qt=512, dtype=0, T=10, S=2, start=FAKE, max_new=10, H=4, H_kv=2, d=128, ke=FAKE, ve=FAKE, page=64, s=20,
+           max_len=100, O=FAKE):
+    return (Q, qt, 128, dtype, T, S, FAKE, start, max_new, H, H_kv, d, FAKE, FAKE, ke, ve, FAKE, 3, 8, page, s, max_len, FAKE, FAKE,
+            O, FAKE, FAKE, NULL)
+
+
+ODD = ctypes.c_void_p((1 << 20) + 8)
+REFUSED = [
+    ("plsh_packed_fwd", _packed, [(dict(Q=NULL), 1), (dict(Q=ODD), 1), (dict(qt=508), 1), (dict(qh=64), 1), (dict(kt=64), 1), (dict(dtype=7), 2),
+                                  (dict(T=0), 1), (dict(S=0), 1), (dict(cu=NULL), 1), (dict(H_kv=3), 1), (dict(H=0), 1), (dict(d=96), 2),
+                                  (dict(s=0), 1), (dict(s=65), 1), (dict(max_len=0), 1), (dict(spans=NULL), 1), (dict(O=ODD), 1),
+                                  (dict(T=1 << 30, qt=1 << 20), 3), (dict(S=1 << 21), 3)]),
+    ("plsh_cache_append", _append, [(dict(K=NULL), 1), (dict(dtype=2), 2), (dict(T=0), 1), (dict(S=0), 1), (dict(start=NULL), 1), (dict(d=32), 2),
+                                    (dict(kp=NULL), 1), (dict(ke=NULL), 1), (dict(ve=NULL), 1), (dict(width=0), 1), (dict(pages=0), 1),
+                                    (dict(page=48), 2), (dict(page=8), 2), (dict(page=512), 2)]),
+    ("plsh_cache_read", _read, [(dict(kp=ODD), 1), (dict(ke=NULL), 1), (dict(width=0), 1), (dict(page=100), 2), (dict(T=0), 1),
+                                (dict(start=NULL), 1), (dict(d=256), 2), (dict(dtype=5), 2), (dict(K=NULL), 1), (dict(K=ODD), 1)]),
+    ("plsh_paged_fwd", _paged, [(dict(Q=NULL), 1), (dict(qt=100), 1), (dict(dtype=3), 2), (dict(T=0), 1), (dict(start=NULL), 1), (dict(max_new=0), 1),
+                                (dict(H_kv=3), 1), (dict(d=80), 2), (dict(ve=NULL), 1), (dict(page=20), 2), (dict(s=99), 1), (dict(max_len=0), 1),
+                                (dict(O=NULL), 1)]),
+]
+
+
+@pytest.mark.parametrize("name,args,bad", REFUSED, ids=[r[0] for r in REFUSED])
+def test_bad_arguments_are_refused_before_any_launch(plsh, name, args, bad):
+    for change, code in bad:
+        assert getattr(plsh._lib, name)(*args(**change)) == code, change
+        assert plsh.plsh_last_error().startswith(name + ":")
+
+
+def test_plain_sequence_agrees_with_the_oracle():
+    H, H_kv, n, d, s = 2, 1, 90, 64, 12
+    g = torch.Generator().manual_seed(1)
+    q, k, v = (torch.randn((n, h, d), generator=g, dtype=torch.float64) for h in (H, H_kv, H_kv))
+    table = oracle.draw_table(5, [3.0, 40.0], s)
+    O, R, _, _ = plain.sequence(q, k, v, table, 0)
+    tail, rt, _, _ = plain.sequence(q[60:], k, v, table, 60)
+    for h in range(H):
+        wO, wR = oracle.approx_attention(q[:, h].numpy(), k[:, 0].numpy(), v[:, 0].numpy(), oracle.bin_ids(table, n)[h], True)
+        assert np.abs(O[:, h].numpy() - wO).max() <= 1e-12 and np.abs(R[:, h].numpy() - wR).max() <= 1e-12
+    assert (tail - O[60:]).abs().max() <= 1e-13 and (rt - R[60:]).abs().max() <= 1e-13
+
+
+def test_plain_quantiser_agrees_with_torch_and_keeps_its_definition():
+    g = torch.Generator().manual_seed(2)
+    x = torch.randn((40, 2, 64), generator=g) * torch.exp2(torch.randint(-20, 20, (40, 2, 1), generator=g).float())
+    byte, exp = plain.quantise(x.double().numpy())
+    top = x.abs().amax(-1).double().numpy()
+    assert (top <= 448.0 * 2.0 ** exp).all() and (top > 448.0 * 2.0 ** (exp - 1.0)).all()
+    scaled = x.double() * torch.exp2(-torch.tensor(exp).double())[..., None]
+    assert np.array_equal(scaled.float().to(torch.float8_e4m3fn).view(torch.uint8).numpy(), byte)
+    assert np.array_equal(plain.values(byte, exp), scaled.float().to(torch.float8_e4m3fn).double().numpy() * (2.0 ** exp.astype(float))[..., None])
