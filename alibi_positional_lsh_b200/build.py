@@ -34,6 +34,7 @@ SOURCES = [
     "plsh_serve_abi.cu",
     "plsh_cache.cu",
     "plsh_serve_simt.cu",
+    "plsh_serve_tc.cu",
 ]
 
 ARCH = ["-gencode", "arch=compute_100a,code=sm_100a"]

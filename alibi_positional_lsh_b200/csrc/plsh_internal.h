@@ -123,6 +123,7 @@ struct ServeArgs {
   void* O; float* row_sum; uint32_t* err;
 };
 int launch_serve_simt(const ServeArgs& a, cudaStream_t st);
+int launch_serve_tc(const ServeArgs& a, cudaStream_t st);  // bf16, packed K and V
 int launch_attention_tc(const AttnArgs& a, cudaStream_t st);
 
 }  // namespace plsh

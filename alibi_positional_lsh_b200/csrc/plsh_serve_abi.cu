@@ -98,7 +98,8 @@ extern "C" int plsh_packed_fwd(const void* Q, int64_t q_token, int64_t q_head, c
   a.dtype = dtype; a.H = H; a.H_kv = H_kv; a.d = d; a.s = s;
   a.spans = tile_span_dev; a.bmask = bmask_dev;
   a.O = O; a.row_sum = row_sum; a.err = err_dev;
-  return plsh::launch_serve_simt(a, static_cast<cudaStream_t>(stream));
+  return dtype == PLSH_BF16 ? plsh::launch_serve_tc(a, static_cast<cudaStream_t>(stream))
+                            : plsh::launch_serve_simt(a, static_cast<cudaStream_t>(stream));
 }
 
 extern "C" int plsh_cache_append(const void* K, int64_t k_token, int64_t k_head, const void* V, int64_t v_token, int64_t v_head,

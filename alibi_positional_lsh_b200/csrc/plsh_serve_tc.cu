@@ -1,0 +1,824 @@
+// T~ for packed prompts (and chunks against the paged cache) on the sm_100a tensor cores, bf16.
+//
+//   O_i = sum_{j <= i} c_ij e^{S_ij} V_j / sum_{j <= i} c_ij e^{S_ij},   S = Q K^T / sqrt(d),
+// c_ij counting the hashes that put positions i and j into one bin (Positional LSH technical summary,
+// Methodology 2; blocks are contiguous, Methodology 1).
+//
+// The counts are a matrix product. Take a key tile whose last key is e, and rows i > e. Hash k
+// puts i and j together exactly if it has no block boundary in (j, e] and none in (e, i], so
+//   c_ij = sum_k a_ik b_jk,   a_ik = [no boundary of k in (e, i]],   b_jk = [none in (j, e]],
+// a product of two 0/1 matrices with one column per hash. They are written as e4m3 bytes and
+// multiplied by the tensor cores beside S: one instruction per 32 hashes, instead of an OR, a
+// population count and a conversion for every score. Both are exact (each byte is 2.0 or 0, so the product is
+// 4 c; the 4 cancels in O and leaves row_sum as two in the logarithm). Only the scores within 32 or
+// 64 keys of the diagonal are counted by scanning the boundary masks from the row down.
+//
+// Work. One item is a pair of 128-row tiles (256 positions) of one head; the tiles' windows
+// overlap, so both read the same 64-key tiles of K and V from shared memory, from the diagonal down.
+// Each row tile is a stream of its own: a warpgroup of softmax threads (one row each), a warp that issues its MMAs
+// and a warp that writes its counts' operands; the streams run half a step apart, so that one's
+// products run under the other's exponentials. Persistent blocks walk the items, heads with the widest
+// windows first. Tensor Memory, per stream: S (64 columns), 4 c (64 columns, P over them as
+// bf16), O (D columns).
+//
+// Per tile g of a stream:
+//   MMA      S(g) = Q K^T  (as soon as the softmax has read S(g - 1)),  O += P(g - 1) V,  C(g) = A B^T
+//   softmax  m = max over weighted keys;  P = 4c 2^(S log2e/sqrt(d) - m);  l += sum P
+// The maximum runs over keys with c > 0 only, so no score of a key without weight can push a row's weights
+// out of range. O is rescaled only when m grows by more than 2^8 (P <= 2^16 then).
+//
+// Rows past a sequence's end hold another sequence's data: their V rows are cleared in shared memory before the product, so that
+// a NaN there cannot meet a zero weight.
+//
+// Every barrier wait is bounded in time (PLSH_DEVERR_TIMEOUT), as in the fused kernel.
+#include <cuda.h>
+#include <cudaTypedefs.h>
+
+#include "plsh_serve.cuh"
+#include "plsh_sm100.cuh"
+#include "plsh_tile_common.cuh"
+
+namespace plsh {
+namespace {
+
+using namespace sm100;
+using namespace serve;
+using tiles::regs_after_wait;
+
+constexpr int kThreads = 512;                 // 16 warps
+constexpr int kSoftmaxWarps = 8;              // warps 0-3 stream 0 (the lower row tile), 4-7 stream 1
+constexpr int kWarpLoad = 8, kWarpMma = 9, kWarpMask = 11;  // one MMA and one mask warp per stream
+constexpr int kRows = 128, kKeys = 64;
+constexpr int kItems = 4;                     // item descriptors in flight
+constexpr uint32_t kTmemCols = 512, kStreamCols = 256;
+constexpr uint32_t kColS = 0, kColC = 64, kColO = 128;
+constexpr float kRescaleThreshold = 8.0f;
+constexpr int kMaxSortedHeads = 256;
+constexpr uint64_t kDrainNs = 100000000ull;
+// Registers per thread: 512 x 128 at launch; the two softmax warpgroups take 192, the other two keep 64.
+constexpr uint32_t kRegsSoftmax = 192, kRegsRest = 64;
+
+// Two row tiles of one head: positions 256 tp .. 256 tp + 255 of sequence s.
+struct Item {
+  int valid, h, tp, c0, pos0, end, s;
+  int top;       // highest key tile
+  int low[2];    // lowest key tile of each stream
+  int first[2];  // highest key tile of each stream; first < low: the stream has no rows here
+  int n0;        // number of the first key tile in the block's sequence of loads
+};
+
+template <int D, typename MaskT, int kStages>
+struct __align__(1024) TcSmem {
+  static constexpr int kQBytes = kRows * D * 2, kKBytes = kKeys * D * 2;
+  static constexpr int kFeat = sizeof(MaskT) * 8;  // bytes of a row of a or b: one per hash
+  uint8_t q[2][kQBytes];
+  uint8_t k[kStages][kKBytes];
+  uint8_t v[kStages][kKBytes];
+  uint8_t a[2][2][kRows * kFeat];   // [stream][0: pivot inside the row tile (rows 64..127), 1: pivot before it]
+  uint8_t b[2][2][kKeys * kFeat];   // [stream][stage]
+  MaskT bm[2][2][kRows];            // boundary masks of the row tile [stream][item parity]
+  MaskT pre[2][2][kRows];           // OR of the masks from the row tile's first row to the row
+  MaskT gap[2][2], upper[2][2];     // [stream][stage]: OR between the key tile and the row tile; OR of the key tile's keys 32..63
+  Item item[kItems];
+  int16_t order[kMaxSortedHeads];
+  int32_t width[kMaxSortedHeads];
+  uint64_t item_full[kItems], item_empty[kItems];
+  uint64_t q_full[2], q_empty[2];
+  uint64_t kv_full[kStages], kv_empty[kStages];
+  uint64_t row_full[2][2], row_empty[2][2];
+  uint64_t feat_full[2][2], feat_empty[2][2];
+  uint64_t s_free[2], c_full[2], p_full[2], o_full[2];
+  uint64_t drain[2];
+  uint32_t tmem_base;
+  int abort_flag;
+};
+
+struct TcParams {
+  SeqArgs sq;
+  int H, H_kv, s, slots, items;
+  int q_swap, k_swap, v_swap;  // tensor map's second coordinate is the token (head-major storage) instead of the head
+  const int32_t* spans;
+  uint64_t wait_ns;
+  int withhold_mma;
+};
+
+// ---- counts as a product
+
+// D[tmem] (+)= A[smem] * B[smem]^T, e4m3 operands, fp32 accumulation, 32 columns of K
+__device__ __forceinline__ void mma_f8(uint32_t d_tmem, uint64_t a_desc, uint64_t b_desc, uint32_t idesc, uint32_t accumulate) {
+  asm volatile(
+      "{\n\t.reg .pred p;\n\t"
+      "setp.ne.b32 p, %4, 0;\n\t"
+      "tcgen05.mma.cta_group::1.kind::f8f6f4 [%0], %1, %2, %3, p;\n\t}" ::"r"(d_tmem),
+      "l"(a_desc), "l"(b_desc), "r"(idesc), "r"(accumulate));
+}
+
+// K-major operand without swizzle: blocks of 8 rows x 16 bytes, 128 bytes apart along K, `group`
+// bytes from one group of 8 rows to the next.
+__device__ __forceinline__ uint64_t smem_desc_plain(uint32_t saddr, uint32_t group) {
+  uint64_t d = 0;
+  d |= static_cast<uint64_t>((saddr >> 4) & 0x3FFFu);
+  d |= static_cast<uint64_t>((128u >> 4) & 0x3FFFu) << 16;
+  d |= static_cast<uint64_t>((group >> 4) & 0x3FFFu) << 32;
+  d |= 1ull << 46;
+  return d;
+}
+
+__host__ __device__ constexpr uint32_t idesc_e4m3_f32(int M, int N) {
+  return (1u << 4) | (static_cast<uint32_t>(N >> 3) << 17) | (static_cast<uint32_t>(M >> 4) << 24);
+}
+
+// Row r of a 0/1 operand: byte k is 0x40 (e4m3 2.0) where bit k is set. Four bits spread to four bytes by one multiply.
+__device__ __forceinline__ uint32_t spread4(uint32_t bits) { return ((bits & 0xFu) * (0x00204081u << 6)) & 0x40404040u; }
+
+template <typename MaskT>
+__device__ __forceinline__ void put_bits(uint8_t* base, int r, MaskT bits) {
+  constexpr int kChunks = sizeof(MaskT) / 2;  // 16 bytes (16 hashes) each
+  uint8_t* row = base + (r >> 3) * (128 * kChunks) + (r & 7) * 16;
+#pragma unroll
+  for (int c = 0; c < kChunks; ++c) {
+    const uint32_t w = static_cast<uint32_t>(bits >> (16 * c));
+    *reinterpret_cast<uint4*>(row + 128 * c) = make_uint4(spread4(w), spread4(w >> 4), spread4(w >> 8), spread4(w >> 12));
+  }
+}
+
+// mbar_wait (plsh_sm100.cuh) with the polling loop in place: a kernel that moves registers between its warpgroups cannot
+// call a function, whose own registers would be those of the launch.
+__device__ __forceinline__ bool wait_bounded(uint64_t* bar, uint32_t parity, volatile int* abort_flag, uint32_t* err,
+                                             uint64_t limit_ns) {
+  if (mbar_try_wait(bar, parity)) return true;
+  const uint64_t t0 = global_timer_ns();
+  while (!mbar_try_wait(bar, parity)) {
+    if (*abort_flag) return false;
+    if (global_timer_ns() - t0 > limit_ns) {
+      *abort_flag = 1;
+      atomicOr(err, PLSH_DEVERR_TIMEOUT);
+      return false;
+    }
+  }
+  return true;
+}
+
+// ---- the kernel
+
+template <int D, typename MaskT, int kStages>
+__global__ void __launch_bounds__(kThreads, 1)
+serve_tc_kernel(const __grid_constant__ CUtensorMap tmap_q, const __grid_constant__ CUtensorMap tmap_k,
+                const __grid_constant__ CUtensorMap tmap_v, const __grid_constant__ TcParams prm,
+                const MaskT* __restrict__ bmask, __nv_bfloat16* __restrict__ O, float* __restrict__ row_sum,
+                uint32_t* __restrict__ err) {
+  using Smem = TcSmem<D, MaskT, kStages>;
+  extern __shared__ __align__(1024) uint8_t smem_raw[];
+  const uint32_t smem_pad = (1024u - (smem_u32(smem_raw) & 1023u)) & 1023u;
+  auto& sm = *reinterpret_cast<Smem*>(smem_raw + smem_pad);
+  volatile int* abort_flag = &sm.abort_flag;
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  const int H = prm.H, s = prm.s, max_len = prm.sq.max_len;
+  const int T128 = (max_len + PLSH_TILE - 1) / PLSH_TILE;
+  const MaskT FULL = (s >= static_cast<int>(8 * sizeof(MaskT))) ? static_cast<MaskT>(~static_cast<MaskT>(0))
+                                                                : static_cast<MaskT>((static_cast<MaskT>(1) << s) - 1);
+  constexpr int kFeat = Smem::kFeat;
+  constexpr uint32_t kFeatGroup = 128 * (kFeat / 16);
+
+  if (blockIdx.x == 0) check_seqs(prm.sq, err);
+  // heads by decreasing window width of the middle row tile
+  if (H <= kMaxSortedHeads) {
+    for (int h = threadIdx.x; h < H; h += kThreads) {
+      const int t = T128 / 2;
+      sm.width[h] = min(max_len, t * PLSH_TILE + PLSH_TILE) - prm.spans[(static_cast<size_t>(h) * T128 + t) * 2];
+    }
+    __syncthreads();
+    for (int h = threadIdx.x; h < H; h += kThreads) {
+      const int wh = sm.width[h];
+      int rank = 0;
+      for (int o = 0; o < H; ++o) {
+        const int wo = sm.width[o];
+        rank += (wo > wh) || (wo == wh && o < h);
+      }
+      sm.order[rank] = static_cast<int16_t>(h);
+    }
+  }
+  if (threadIdx.x == 0) {
+    sm.abort_flag = 0;
+    for (int i = 0; i < kItems; ++i) {
+      mbar_init(&sm.item_full[i], 1);
+      mbar_init(&sm.item_empty[i], kSoftmaxWarps + 4);
+    }
+    for (int i = 0; i < kStages; ++i) {
+      mbar_init(&sm.kv_full[i], 1);
+      mbar_init(&sm.kv_empty[i], 2);
+    }
+    for (int w = 0; w < 2; ++w) {
+      mbar_init(&sm.q_full[w], 1);
+      mbar_init(&sm.q_empty[w], 1);
+      for (int i = 0; i < 2; ++i) {
+        mbar_init(&sm.row_full[w][i], 1);
+        mbar_init(&sm.row_empty[w][i], 4);
+        mbar_init(&sm.feat_full[w][i], 1);
+        mbar_init(&sm.feat_empty[w][i], 5);
+      }
+      mbar_init(&sm.s_free[w], 4);
+      mbar_init(&sm.c_full[w], 1);
+      mbar_init(&sm.p_full[w], 4);
+      mbar_init(&sm.o_full[w], 1);
+      mbar_init(&sm.drain[w], 1);
+    }
+    fence_mbarrier_init();
+  }
+  if (warp == kWarpMma) {
+    tmem_alloc(&sm.tmem_base, kTmemCols);
+    tmem_relinquish();
+  }
+  tc_fence_before();
+  __syncthreads();
+  tc_fence_after();
+  const uint32_t tmem = sm.tmem_base;
+  auto wait = [&](uint64_t* bar, uint32_t parity) { return wait_bounded(bar, parity & 1u, abort_flag, err, prm.wait_ns); };
+  // the same by a whole warp: false in every lane if any gave up
+  auto wait_all = [&](uint64_t* bar, uint32_t parity) { return __all_sync(0xffffffffu, wait(bar, parity)) != 0; };
+
+  if (warp < kSoftmaxWarps) {
+    regs_raise<kRegsSoftmax>();
+    // ------------------------------------------------------------ softmax: one row per thread
+    const int w = warp >> 2, rg = warp & 3;
+    const int r = 32 * rg + lane;
+    const uint32_t base = tmem + kStreamCols * w + (static_cast<uint32_t>(32 * rg) << 16);
+    const float sc = 1.4426950408889634f / sqrtf(static_cast<float>(D));
+    int g = 0, items = 0;
+    float m2 = -INFINITY, l = 0.0f;
+    int d_h = 0, d_i0 = 0, d_c0 = 0, d_pos0 = 0, d_end = 0;  // the finished item, until its epilogue
+    bool pending = false;
+    // O / l of the item just finished, once its last product has completed
+    auto epilogue = [&](int number) -> bool {
+      if (!wait_all(&sm.o_full[w], number)) return false;
+      tc_fence_after();
+      const float inv = 1.0f / l;
+      const int p4 = lane & 3;
+#pragma unroll 1
+      for (int blk = 0; blk < D / 32; ++blk) {
+        uint32_t raw[32];
+        tmem_ld32(base + kColO + 32u * blk, raw);
+        tmem_wait_ld();
+        regs_after_wait(raw);
+        uint32_t a[4][4];  // [16-byte chunk][word] of this row's 32 columns
+#pragma unroll
+        for (int c = 0; c < 4; ++c)
+#pragma unroll
+          for (int e = 0; e < 4; ++e)
+            a[c][e] = pack_bf16x2(__uint_as_float(raw[8 * c + 2 * e]) * inv, __uint_as_float(raw[8 * c + 2 * e + 1]) * inv);
+        // 4x4 transpose of 16-byte chunks inside each quad of lanes: lane p then holds chunk p of the quad's four rows
+#pragma unroll
+        for (int msk = 2; msk >= 1; msk >>= 1) {
+          const bool lo_lane = (p4 & msk) == 0;
+#pragma unroll
+          for (int c = 0; c < 4; ++c) {
+            if (c & msk) continue;
+#pragma unroll
+            for (int e = 0; e < 4; ++e) {
+              const uint32_t send = lo_lane ? a[c | msk][e] : a[c][e];
+              const uint32_t recv = __shfl_xor_sync(0xffffffffu, send, msk);
+              if (lo_lane) a[c | msk][e] = recv;
+              else a[c][e] = recv;
+            }
+          }
+        }
+#pragma unroll
+        for (int e = 0; e < 4; ++e) {
+          const int p = d_i0 + (r & ~3) + e;
+          if (p >= d_pos0 && p < d_end) {
+            const size_t t = static_cast<size_t>(d_c0 + p - d_pos0);
+            *reinterpret_cast<uint4*>(O + (t * H + d_h) * D + 32 * blk + 8 * p4) = make_uint4(a[e][0], a[e][1], a[e][2], a[e][3]);
+          }
+        }
+      }
+      tc_fence_before();
+      const int p = d_i0 + r;
+      if (p >= d_pos0 && p < d_end)
+        row_sum[static_cast<size_t>(d_c0 + p - d_pos0) * H + d_h] =
+            (log2f(l) + m2 - 2.0f) * 0.6931471805599453f - logf(static_cast<float>(s));
+      return true;
+    };
+    for (int k = 0;; ++k) {
+      if (!wait_all(&sm.item_full[k % kItems], k / kItems)) break;
+      const Item& item = sm.item[k % kItems];
+      const int valid = item.valid, first = item.first[w], low = item.low[w], h = item.h, i0 = 256 * item.tp + 128 * w;
+      const int c0 = item.c0, pos0 = item.pos0, end = item.end;
+      __syncwarp();
+      if (lane == 0) mbar_arrive(&sm.item_empty[k % kItems]);
+      if (valid && first < low) continue;
+      MaskT pre = 0, mid = 0;
+      uint32_t cnt[16];  // c of the scanned keys, one byte each, as the halves of the tile: the warp's own 32 keys and, in odd blocks, the 32 before
+#pragma unroll
+      for (int i = 0; i < 16; ++i) cnt[i] = 0;
+      if (valid) {
+        const int rb = items & 1;
+        if (!wait_all(&sm.row_full[w][rb], items >> 1)) break;
+        const MaskT* bm = sm.bm[w][rb];
+        pre = sm.pre[w][rb][r];
+        // from the row down, four keys a step: own block first, then (odd blocks) the block before it
+        const int steps = (rg & 1) ? 16 : 8;
+#pragma unroll 1
+        for (int j = 0; j < steps; ++j) {
+          const int at = steps - 1 - j;               // word of four keys, counted from the tile half's first scanned key
+          const MaskT* b4 = bm + 32 * (rg & ~1) + 4 * at;
+          uint32_t four = 0;
+#pragma unroll
+          for (int e = 3; e >= 0; --e) {
+            if (32 * (rg & 1) + lane >= 4 * at + e) {
+              four |= static_cast<uint32_t>(s - popc_mask<MaskT>(mid)) << (8 * e);
+              mid = static_cast<MaskT>(mid | b4[e]);
+            }
+          }
+#pragma unroll
+          for (int i = 0; i < 16; ++i)
+            if (i == at) cnt[i] = four;
+        }
+        // mid: OR from the row tile's half (row 0 or 64) to the row
+        __syncwarp();
+        if (lane == 0) mbar_arrive(&sm.row_empty[w][rb]);
+      }
+      if (pending) {
+        if (!epilogue(items - 1)) break;
+        pending = false;
+      }
+      if (!valid) break;
+      m2 = -INFINITY;
+      l = 0.0f;
+      bool ok = true;
+      for (int u = first; u >= low; --u, ++g) {
+        const int fs = g & 1, rel = u - (i0 >> 6);
+        if (!wait_all(&sm.feat_full[w][fs], g >> 1)) { ok = false; break; }
+        // which 32-key halves hold weight for some row of the warp, and where its counts come from
+        const bool scan = rel >= 0 && rel == (rg >> 1);
+        bool live[2];
+        if (rel > 0 && rg < 2) {
+          live[0] = live[1] = false;
+        } else if (scan) {
+          // own keys in the half of the warp's block; odd blocks have the half before it too
+          live[1] = (rg & 1) != 0;
+          live[0] = true;
+        } else {
+          const MaskT keep = static_cast<MaskT>(FULL & ~((rel == 0 ? mid : pre) | sm.gap[w][fs]));
+          live[1] = __any_sync(0xffffffffu, keep != 0);
+          live[0] = __any_sync(0xffffffffu, static_cast<MaskT>(keep & ~sm.upper[w][fs]) != 0);
+        }
+        __syncwarp();
+        if (lane == 0) mbar_arrive(&sm.feat_empty[w][fs]);
+        if (!wait_all(&sm.c_full[w], g)) { ok = false; break; }
+        tc_fence_after();
+        uint32_t sv[2][32];
+        float top = -INFINITY;
+#pragma unroll
+        for (int hf = 0; hf < 2; ++hf) {
+          if (!live[hf]) continue;
+          tmem_ld32(base + kColS + 32u * hf, sv[hf]);
+          if (scan) {
+            tmem_wait_ld();
+            regs_after_wait(sv[hf]);
+#pragma unroll
+            for (int i = 0; i < 32; ++i) {
+              const uint32_t c = (cnt[8 * hf + (i >> 2)] >> (8 * (i & 3))) & 0xFFu;
+              if (c) top = fmaxf(top, __uint_as_float(sv[hf][i]));
+            }
+          } else {
+            uint32_t cv[32];
+            tmem_ld32(base + kColC + 32u * hf, cv);
+            tmem_wait_ld();
+            regs_after_wait(sv[hf]);
+            regs_after_wait(cv);
+#pragma unroll
+            for (int i = 0; i < 32; ++i)
+              if (__uint_as_float(cv[i]) > 0.0f) top = fmaxf(top, __uint_as_float(sv[hf][i]));
+          }
+        }
+        // S has been read
+        tc_fence_before();
+        __syncwarp();
+        if (lane == 0) mbar_arrive(&sm.s_free[w]);
+        const float mt = top * sc;
+        float alpha = 1.0f;
+        bool rescale = false;
+        if (mt > m2 + kRescaleThreshold) {
+          if (m2 != -INFINITY) {
+            alpha = ex2_approx(m2 - mt);
+            rescale = true;
+          }
+          m2 = mt;
+        }
+        if (__any_sync(0xffffffffu, rescale)) {  // C(g) was issued after PV(g - 1), which has therefore completed
+#pragma unroll 1
+          for (int q4 = 0; q4 < D / 16; ++q4) {
+            uint32_t raw[16];
+            tmem_ld16(base + kColO + 16u * q4, raw);
+            tmem_wait_ld();
+            regs_after_wait(raw);
+#pragma unroll
+            for (int e = 0; e < 16; ++e) raw[e] = __float_as_uint(__uint_as_float(raw[e]) * alpha);
+            tmem_st16(base + kColO + 16u * q4, raw);
+          }
+        }
+        float lsum = 0.0f;
+#pragma unroll
+        for (int hf = 0; hf < 2; ++hf) {
+          uint32_t pk[16];
+          if (live[hf]) {
+            float cf[32];
+            if (scan) {
+#pragma unroll
+              for (int i = 0; i < 32; ++i) cf[i] = 4.0f * static_cast<float>((cnt[8 * hf + (i >> 2)] >> (8 * (i & 3))) & 0xFFu);
+            } else {
+              uint32_t cv[32];
+              tmem_ld32(base + kColC + 32u * hf, cv);
+              tmem_wait_ld();
+              regs_after_wait(cv);
+#pragma unroll
+              for (int i = 0; i < 32; ++i) cf[i] = __uint_as_float(cv[i]);
+            }
+#pragma unroll
+            for (int i = 0; i < 16; ++i) {
+              float p[2];
+#pragma unroll
+              for (int e = 0; e < 2; ++e) {
+                const float x = fmaf(__uint_as_float(sv[hf][2 * i + e]), sc, -m2);
+                p[e] = cf[2 * i + e] > 0.0f ? cf[2 * i + e] * ex2_approx(x) : 0.0f;
+                lsum += p[e];
+              }
+              pk[i] = pack_bf16x2(p[0], p[1]);
+            }
+          } else {
+#pragma unroll
+            for (int i = 0; i < 16; ++i) pk[i] = 0u;
+          }
+          tmem_st16(base + kColC + 16u * hf, pk);
+        }
+        l = l * alpha + lsum;
+        tmem_wait_st();
+        tc_fence_before();
+        __syncwarp();
+        if (lane == 0) mbar_arrive(&sm.p_full[w]);
+      }
+      if (!ok) break;
+      d_h = h;
+      d_i0 = i0;
+      d_c0 = c0;
+      d_pos0 = pos0;
+      d_end = end;
+      pending = true;
+      ++items;
+    }
+  } else {
+    regs_lower<kRegsRest>();
+  if (warp == kWarpLoad) {
+    // ------------------------------------------------------------ items, Q and the K/V tiles
+    if (lane == 0) {
+      tma_prefetch_desc(&tmap_q);
+      tma_prefetch_desc(&tmap_k);
+      tma_prefetch_desc(&tmap_v);
+    }
+    int n = 0, k = 0, loads[2] = {0, 0};  // key tiles, items and Q tiles per stream so far
+    bool ok = true;
+    for (int x = blockIdx.x; ok && x < prm.items; x += gridDim.x) {
+      const int hr = x / prm.slots, slot = x % prm.slots;
+      const int h = H <= kMaxSortedHeads ? static_cast<int>(sm.order[hr]) : hr;
+      const int mult = prm.sq.start ? 2 : 1;
+      const int si = warp_find(prm.sq.cu, prm.sq.S, 8, mult, slot);
+      const Seq sq = load_seq(prm.sq, si);
+      Item it;
+      it.valid = 1;
+      it.h = h;
+      it.s = si;
+      it.c0 = sq.c0;
+      it.pos0 = sq.pos0;
+      it.end = sq.pos0 + sq.len;
+      it.tp = (sq.pos0 >> 8) + slot - ((prm.sq.cu[si] >> 8) + mult * si);
+      if (it.tp < 0 || sq.len == 0 || 256 * it.tp >= it.end) continue;
+      it.top = min(4 * it.tp + 3, (it.end - 1) >> 6);
+      it.n0 = n;
+      int low = it.top;
+#pragma unroll
+      for (int w = 0; w < 2; ++w) {
+        const int i0 = 256 * it.tp + 128 * w;
+        const bool rows = i0 < it.end && i0 + 128 > it.pos0;
+        it.first[w] = rows ? min(4 * it.tp + 2 * w + 1, it.top) : -1;
+        it.low[w] = 0;
+        if (rows) {
+          int lo = prm.spans[(static_cast<size_t>(h) * T128 + (i0 >> 7)) * 2];
+          if (lo < 0 || lo > i0) {
+            if (lane == 0) atomicOr(err, PLSH_DEVERR_WINDOW);
+            lo = i0;
+          }
+          it.low[w] = lo >> 6;
+          low = min(low, it.low[w]);
+        }
+      }
+      const int top = max(it.first[0], it.first[1]);  // without rows above, the tiles above are not needed
+      it.top = top;
+      // the descriptor
+      const int slot_i = k % kItems;
+      if (k >= kItems && !wait_all(&sm.item_empty[slot_i], k / kItems + 1)) { ok = false; break; }
+      if (lane == 0) {
+        sm.item[slot_i] = it;
+        mbar_arrive(&sm.item_full[slot_i]);
+      }
+      ++k;
+      __syncwarp();
+      const int kvh = h / (H / prm.H_kv);
+      bool q_due[2] = {it.first[0] >= it.low[0], it.first[1] >= it.low[1]};
+      for (int u = top; u >= low; --u, ++n) {
+        // each stream's Q when its first key tile comes up (the upper tile's rows begin two key tiles earlier)
+#pragma unroll
+        for (int w = 1; w >= 0; --w) {
+          if (!q_due[w] || u > it.first[w]) continue;
+          q_due[w] = false;
+          if (loads[w] && !wait_all(&sm.q_empty[w], loads[w] + 1)) { ok = false; break; }
+          if (lane == 0) {
+            const int t = it.c0 + 256 * it.tp + 128 * w - it.pos0;
+            mbar_arrive_expect_tx(&sm.q_full[w], Smem::kQBytes);
+#pragma unroll
+            for (int c = 0; c < D / 64; ++c)
+              tma_load_3d(sm.q[w] + c * (kRows * 128), &tmap_q, 64 * c, prm.q_swap ? t : h, prm.q_swap ? h : t, &sm.q_full[w]);
+          }
+          ++loads[w];
+        }
+        if (!ok) break;
+        const int st = n % kStages;
+        if (n >= kStages && !wait_all(&sm.kv_empty[st], n / kStages + 1)) { ok = false; break; }
+        if (lane == 0) {
+          const int t = it.c0 + kKeys * u - it.pos0;
+          mbar_arrive_expect_tx(&sm.kv_full[st], 2 * Smem::kKBytes);
+#pragma unroll
+          for (int c = 0; c < D / 64; ++c)
+            tma_load_3d(sm.k[st] + c * (kKeys * 128), &tmap_k, 64 * c, prm.k_swap ? t : kvh, prm.k_swap ? kvh : t, &sm.kv_full[st]);
+#pragma unroll
+          for (int c = 0; c < D / 64; ++c)
+            tma_load_3d(sm.v[st] + c * (kKeys * 128), &tmap_v, 64 * c, prm.v_swap ? t : kvh, prm.v_swap ? kvh : t, &sm.kv_full[st]);
+          // a stream that has no use for the tile has released it already
+#pragma unroll
+          for (int w = 0; w < 2; ++w)
+            if (u > it.first[w] || u < it.low[w]) mbar_arrive(&sm.kv_empty[st]);
+        }
+        __syncwarp();
+      }
+    }
+    if (ok) {  // the end marker
+      const int slot_i = k % kItems;
+      if (k < kItems || wait_all(&sm.item_empty[slot_i], k / kItems + 1)) {
+        if (lane == 0) {
+          sm.item[slot_i].valid = 0;
+          mbar_arrive(&sm.item_full[slot_i]);
+        }
+      }
+    }
+    __syncwarp();
+    if (*abort_flag && lane == 0) {
+      // let every copy already issued land before the block can exit
+      for (int i = max(0, n - kStages); i < n; ++i) mbar_wait_drain(&sm.kv_full[i % kStages], (i / kStages) & 1, kDrainNs);
+      if (n > 0 || loads[0] || loads[1])
+        for (int w = 0; w < 2; ++w)
+          if (loads[w]) mbar_wait_drain(&sm.q_full[w], (loads[w] + 1) & 1, kDrainNs);
+    }
+  } else if (warp == kWarpMma || warp == kWarpMma + 1) {
+    // ------------------------------------------------------------ one stream's MMAs
+    const int w = warp - kWarpMma;
+    if (lane == 0) {
+      constexpr uint32_t idesc_qk = idesc_bf16_f32(kRows, kKeys, 0);
+      constexpr uint32_t idesc_pv = idesc_bf16_f32(kRows, D, 1);
+      constexpr uint32_t idesc_c = idesc_e4m3_f32(kRows, kKeys);
+      const uint32_t base = tmem + kStreamCols * w;
+      const uint64_t q_desc = smem_desc_sw128(smem_u32(sm.q[w]), 16, 1024);
+      const uint64_t k_desc = smem_desc_sw128(smem_u32(sm.k[0]), 16, 1024);
+      const uint64_t v_desc = smem_desc_sw128(smem_u32(sm.v[0]), kKeys * 128, 1024);
+      const uint64_t a_desc = smem_desc_plain(smem_u32(sm.a[w][0]), kFeatGroup);
+      const uint64_t b_desc = smem_desc_plain(smem_u32(sm.b[w][0]), kFeatGroup);
+      int g = 0, items = 0;      // tiles and items of this stream so far
+      int pend = -1;             // stage of the tile whose PV is still to be issued
+      bool pend_first = false, pend_last = false;
+      auto issue_pv = [&]() {
+        tc_fence_after();
+        const uint64_t vd = v_desc + static_cast<uint64_t>((pend * Smem::kKBytes) >> 4);
+#pragma unroll
+        for (int kk = 0; kk < kKeys / 16; ++kk)
+          mma_ts(base + kColO, base + kColC + 8u * kk, vd + static_cast<uint64_t>((kk * 2048) >> 4), idesc_pv,
+                 (!pend_first || kk > 0) ? 1u : 0u);
+        mma_commit(&sm.kv_empty[pend]);
+        if (pend_last) mma_commit(&sm.o_full[w]);
+        pend = -1;
+      };
+      auto flush = [&]() {
+        if (pend < 0) return true;
+        if (!wait(&sm.p_full[w], g - 1)) return false;
+        issue_pv();
+        return true;
+      };
+      bool ok = !prm.withhold_mma;
+      for (int k = 0; ok; ++k) {
+        // no item yet: the loads that come before it may need the pending tile's place
+        if (!mbar_test_wait(&sm.item_full[k % kItems], (k / kItems) & 1) && !flush()) break;
+        if (!wait(&sm.item_full[k % kItems], k / kItems)) break;
+        const Item& item = sm.item[k % kItems];
+        const int valid = item.valid, first = item.first[w], low = item.low[w], above = item.n0 + item.top, row_tile = 4 * item.tp + 2 * w;
+        mbar_arrive(&sm.item_empty[k % kItems]);
+        if (!valid) break;
+        for (int u = first; ok && u >= low; --u, ++g) {
+          const int n = above - u, st = n % kStages;
+          // S(g) before PV(g - 1), which waits for the softmax, if S(g)'s operands are there. Where they are not, PV(g - 1) goes
+          // first: the tile to come may need the very place that tile g - 1 still holds.
+          if (pend >= 0 && !(mbar_test_wait(&sm.kv_full[st], (n / kStages) & 1) && (u != first || mbar_test_wait(&sm.q_full[w], items & 1))) &&
+              !flush()) { ok = false; break; }
+          if (!wait(&sm.kv_full[st], n / kStages) || (u == first && !wait(&sm.q_full[w], items)) || (g > 0 && !wait(&sm.s_free[w], g - 1))) {
+            ok = false;
+            break;
+          }
+          tc_fence_after();
+          const uint64_t kd = k_desc + static_cast<uint64_t>((st * Smem::kKBytes) >> 4);
+#pragma unroll
+          for (int kk = 0; kk < D / 16; ++kk)
+            mma_ss(base + kColS, q_desc + static_cast<uint64_t>(((kk >> 2) * (kRows * 128) + (kk & 3) * 32) >> 4),
+                   kd + static_cast<uint64_t>(((kk >> 2) * (kKeys * 128) + (kk & 3) * 32) >> 4), idesc_qk, kk > 0 ? 1u : 0u);
+          if (u == low) mma_commit(&sm.q_empty[w]);
+          if (!flush()) { ok = false; break; }
+          // C(g), after PV(g - 1), whose P lies where C goes. The upper diagonal tile has none.
+          const int fs = g & 1;
+          if (!wait(&sm.feat_full[w][fs], g >> 1)) { ok = false; break; }
+          const int rel = u - row_tile;  // 1: keys 64..127 of the row tile, 0: keys 0..63, < 0: before it
+          if (rel <= 0) {
+            tc_fence_after();
+            const uint64_t ad = a_desc + static_cast<uint64_t>((rel == 0 ? 0 : kRows * kFeat) >> 4);
+            const uint64_t bd = b_desc + static_cast<uint64_t>((fs * (kKeys * kFeat)) >> 4);
+#pragma unroll
+            for (int c = 0; c < kFeat / 32; ++c) mma_f8(base + kColC, ad + 16u * c, bd + 16u * c, idesc_c, c > 0 ? 1u : 0u);
+          }
+          mma_commit(&sm.feat_empty[w][fs]);
+          mma_commit(&sm.c_full[w]);
+          pend = st;
+          pend_first = u == first;
+          pend_last = u == low;
+        }
+        if (first >= low) ++items;
+      }
+      if (ok) flush();
+      mma_commit(&sm.drain[w]);  // every MMA issued so far completes before it arrives
+      mbar_wait_drain(&sm.drain[w], 0, kDrainNs);
+    }
+  } else if (warp == kWarpMask || warp == kWarpMask + 1) {
+    // ------------------------------------------------------------ one stream's count operands
+    const int w = warp - kWarpMask;
+    int g = 0, items = 0;
+    bool ok = true;
+    for (int k = 0; ok; ++k) {
+      if (!wait_all(&sm.item_full[k % kItems], k / kItems)) break;
+      const Item& item = sm.item[k % kItems];
+      const int valid = item.valid, first = item.first[w], low = item.low[w], above = item.n0 + item.top, end = item.end;
+      const int i0 = 256 * item.tp + 128 * w;
+      const MaskT* bm = bmask + static_cast<size_t>(item.h) * max_len;
+      __syncwarp();
+      if (lane == 0) mbar_arrive(&sm.item_empty[k % kItems]);
+      if (!valid) break;
+      if (first < low) continue;
+      auto mask_at = [&](int p) { return p < max_len ? bm[p] : FULL; };
+      MaskT rv[4];  // rows 32 q + lane
+#pragma unroll
+      for (int q = 0; q < 4; ++q) rv[q] = mask_at(i0 + 32 * q + lane);
+      // the first tiles' masks
+      MaskT kv[2], nx[2];
+#pragma unroll
+      for (int q = 0; q < 2; ++q) nx[q] = mask_at(kKeys * first + 32 * q + lane);
+      // rows: OR inside the 32-row block, then from the tile's middle and from its first row
+      MaskT in[4], tot[4];
+#pragma unroll
+      for (int q = 0; q < 4; ++q) {
+        in[q] = tiles::warp_prefix_or<MaskT>(rv[q], lane);
+        tot[q] = __shfl_sync(0xffffffffu, in[q], 31);
+      }
+      const int rb = items & 1;
+      if (items >= 2 && !wait_all(&sm.row_empty[w][rb], (items >> 1) + 1)) { ok = false; break; }
+      MaskT before = 0;
+#pragma unroll
+      for (int q = 0; q < 4; ++q) {
+        sm.bm[w][rb][32 * q + lane] = rv[q];
+        sm.pre[w][rb][32 * q + lane] = static_cast<MaskT>(before | in[q]);
+        before = static_cast<MaskT>(before | tot[q]);
+      }
+      __syncwarp();
+      if (lane == 0) mbar_arrive(&sm.row_full[w][rb]);
+      // the last product of the previous item has read a
+      if (g >= 1 && !wait_all(&sm.feat_empty[w][(g - 1) & 1], (g - 1) >> 1)) { ok = false; break; }
+      put_bits<MaskT>(sm.a[w][0], 64 + lane, static_cast<MaskT>(FULL & ~in[2]));
+      put_bits<MaskT>(sm.a[w][0], 96 + lane, static_cast<MaskT>(FULL & ~(tot[2] | in[3])));
+      before = 0;
+#pragma unroll
+      for (int q = 0; q < 4; ++q) {
+        put_bits<MaskT>(sm.a[w][1], 32 * q + lane, static_cast<MaskT>(FULL & ~(before | in[q])));
+        before = static_cast<MaskT>(before | tot[q]);
+      }
+      MaskT gap = 0;
+      for (int u = first; ok && u >= low; --u, ++g) {
+        kv[0] = nx[0];
+        kv[1] = nx[1];
+        if (u > low) {
+#pragma unroll
+          for (int q = 0; q < 2; ++q) nx[q] = mask_at(kKeys * (u - 1) + 32 * q + lane);
+        }
+        const int rel = u - (i0 >> 6), fs = g & 1;
+        if (g >= 2 && !wait_all(&sm.feat_empty[w][fs], (g >> 1) + 1)) { ok = false; break; }
+        // keys: OR after the key, up to the tile's last
+        const MaskT s1 = tiles::warp_suffix_or<MaskT>(kv[1], lane), s0 = tiles::warp_suffix_or<MaskT>(kv[0], lane);
+        const MaskT t1 = __shfl_sync(0xffffffffu, s1, 0), t0 = __shfl_sync(0xffffffffu, s0, 0);
+        MaskT a1 = __shfl_down_sync(0xffffffffu, s1, 1), a0 = __shfl_down_sync(0xffffffffu, s0, 1);
+        if (lane == 31) a1 = a0 = 0;
+        if (rel <= 0) {
+          put_bits<MaskT>(sm.b[w][fs], lane, static_cast<MaskT>(FULL & ~(a0 | t1 | gap)));
+          put_bits<MaskT>(sm.b[w][fs], 32 + lane, static_cast<MaskT>(FULL & ~(a1 | gap)));
+        }
+        if (lane == 0) {
+          sm.gap[w][fs] = gap;
+          sm.upper[w][fs] = t1;
+        }
+        if (rel < 0) gap = static_cast<MaskT>(gap | t0 | t1);
+        // V rows past the end: another sequence's, or nothing at all
+        if (kKeys * (u + 1) > end) {
+          const int n = above - u, st = n % kStages;
+          if (!wait_all(&sm.kv_full[st], n / kStages)) { ok = false; break; }
+          const int r0 = end - kKeys * u;
+          for (int e = lane; e < (kKeys - r0) * (D / 8); e += 32) {
+            const int r = r0 + e / (D / 8), c = e % (D / 8);
+            *reinterpret_cast<uint4*>(sm.v[st] + (c >> 3) * (kKeys * 128) + r * 128 + (c & 7) * 16) = make_uint4(0, 0, 0, 0);
+          }
+        }
+        fence_proxy_async_smem();
+        __syncwarp();
+        if (lane == 0) mbar_arrive(&sm.feat_full[w][fs]);
+      }
+      ++items;
+    }
+  }
+  }
+
+  tc_fence_before();
+  __syncthreads();
+  if (warp == kWarpMma) {
+    __syncwarp();
+    tc_fence_after();
+    tmem_dealloc(tmem, kTmemCols);
+  }
+}
+
+// ---------------------------------------------------------------- host side
+
+// Rows of D bf16 of a packed tensor [T][heads][D]: boxes of 64 columns x `rows` tokens of one head, 128-byte swizzle.
+// Rows past T read as zero. `swap` says whether the token is the second coordinate (the smaller stride).
+int make_rows_map(CUtensorMap* map, const void* p, RowStrides st, int T, int heads, int D, int rows, int* swap) {
+  auto enc = tiles::get_encode_fn();
+  if (!enc) return fail(PLSH_ERR_CUDA, "cuTensorMapEncodeTiled is not available from the driver");
+  *swap = st.token < st.head ? 1 : 0;
+  const cuuint64_t tok = static_cast<cuuint64_t>(st.token) * 2, hd = static_cast<cuuint64_t>(st.head) * 2;
+  cuuint64_t dims[3] = {static_cast<cuuint64_t>(D), static_cast<cuuint64_t>(*swap ? T : heads),
+                        static_cast<cuuint64_t>(*swap ? heads : T)};
+  cuuint64_t strides[2] = {*swap ? tok : hd, *swap ? hd : tok};
+  cuuint32_t box[3] = {64, static_cast<cuuint32_t>(*swap ? rows : 1), static_cast<cuuint32_t>(*swap ? 1 : rows)};
+  cuuint32_t estr[3] = {1, 1, 1};
+  const CUresult r = enc(map, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 3, const_cast<void*>(p), dims, strides, box, estr,
+                         CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
+                         CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE);
+  if (r != CUDA_SUCCESS) return fail(PLSH_ERR_CUDA, "cuTensorMapEncodeTiled failed (%d)", static_cast<int>(r));
+  return PLSH_OK;
+}
+
+template <int D, typename MaskT, int kStages>
+int launch(const ServeArgs& a, cudaStream_t st) {
+  CUtensorMap mq, mk, mv;
+  TcParams prm{};
+  if (int rc = make_rows_map(&mq, a.Q, a.qs, a.sq.T, a.H, D, kRows, &prm.q_swap)) return rc;
+  if (int rc = make_rows_map(&mk, a.K, a.ks, a.sq.T, a.H_kv, D, kKeys, &prm.k_swap)) return rc;
+  if (int rc = make_rows_map(&mv, a.V, a.vs, a.sq.T, a.H_kv, D, kKeys, &prm.v_swap)) return rc;
+  prm.sq = a.sq;
+  prm.H = a.H;
+  prm.H_kv = a.H_kv;
+  prm.s = a.s;
+  prm.slots = (a.sq.T >> 8) + (a.sq.start ? 2 : 1) * a.sq.S;
+  if (static_cast<long long>(prm.slots) * a.H > 0x7fffffffLL) return fail(PLSH_ERR_RANGE, "too many row tiles");
+  prm.items = prm.slots * a.H;
+  prm.spans = a.spans;
+  prm.wait_ns = wait_limit_ns();
+  prm.withhold_mma = withhold_mma() ? 1 : 0;
+  auto kern = serve_tc_kernel<D, MaskT, kStages>;
+  constexpr size_t smem = sizeof(TcSmem<D, MaskT, kStages>) + 1024;
+  static_assert(smem <= 232448, "shared memory budget");
+  cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, static_cast<int>(smem));
+  if (e != cudaSuccess) return cuda_fail(e, "cudaFuncSetAttribute(serve_tc_kernel)");
+  const int grid = prm.items < tiles::sm_count() ? prm.items : tiles::sm_count();
+  kern<<<grid, kThreads, smem, st>>>(mq, mk, mv, prm, static_cast<const MaskT*>(a.bmask), static_cast<__nv_bfloat16*>(a.O),
+                                     a.row_sum, a.err);
+  e = cudaGetLastError();
+  return e == cudaSuccess ? PLSH_OK : cuda_fail(e, "serve_tc_kernel launch");
+}
+
+}  // namespace
+
+int launch_serve_tc(const ServeArgs& a, cudaStream_t st) {
+  if (a.d == 128)
+    return a.s <= 32 ? launch<128, uint32_t, 4>(a, st) : launch<128, unsigned long long, 3>(a, st);
+  return a.s <= 32 ? launch<64, uint32_t, 6>(a, st) : launch<64, unsigned long long, 6>(a, st);
+}
+
+}  // namespace plsh
