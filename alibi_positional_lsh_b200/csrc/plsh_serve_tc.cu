@@ -22,13 +22,15 @@
 // bf16), O (D columns).
 //
 // Per tile g of a stream:
-//   MMA      S(g) = Q K^T  (as soon as the softmax has read S(g - 1)),  O += P(g - 1) V,  C(g) = A B^T
-//   softmax  m = max over weighted keys;  P = 4c 2^(S log2e/sqrt(d) - m);  l += sum P
-// The maximum runs over keys with c > 0 only, so no score of a key without weight can push a row's weights
-// out of range. O is rescaled only when m grows by more than 2^8 (P <= 2^16 then).
+//   MMA      O += P(g - 1) V,  S(g) = Q K^T,  C(g) = A B^T
+//   softmax  P = 4c 2^(S log2e/sqrt(d) - m);  l += sum P
+// The reference m starts at 0 and changes only where a row leaves the range it is good for: a tile's sum above 2^64,
+// or a sum below 2^-30 in the tile of the row's own key (which has the largest weight). fp32 and bf16 hold such P with
+// full relative precision, so no maximum is taken otherwise; the tile is then done again
+// with m = the maximum over its keys with c > 0. No score of a key without weight can push a row's weights out of range.
 //
-// Rows past a sequence's end hold another sequence's data: their V rows are cleared in shared memory before the product, so that
-// a NaN there cannot meet a zero weight.
+// Rows past a sequence's end hold another sequence's data: their K and V rows are cleared in shared memory before the
+// products, so that nothing there, not even a NaN, meets a zero weight: a sequence's result has the same bits whatever it is packed with.
 //
 // Every barrier wait is bounded in time (PLSH_DEVERR_TIMEOUT), as in the fused kernel.
 #include <cuda.h>
@@ -52,7 +54,7 @@ constexpr int kRows = 128, kKeys = 64;
 constexpr int kItems = 4;                     // item descriptors in flight
 constexpr uint32_t kTmemCols = 512, kStreamCols = 256;
 constexpr uint32_t kColS = 0, kColC = 64, kColO = 128;
-constexpr float kRescaleThreshold = 8.0f;
+constexpr float kSumMax = 1.8446744e19f, kSumMin = 9.3132257e-10f;  // 2^64, 2^-30
 constexpr int kMaxSortedHeads = 256;
 constexpr uint64_t kDrainNs = 100000000ull;
 // Registers per thread: 512 x 128 at launch; the two softmax warpgroups take 192, the other two keep 64.
@@ -87,7 +89,7 @@ struct __align__(1024) TcSmem {
   uint64_t kv_full[kStages], kv_empty[kStages];
   uint64_t row_full[2][2], row_empty[2][2];
   uint64_t feat_full[2][2], feat_empty[2][2];
-  uint64_t s_free[2], c_full[2], p_full[2], o_full[2];
+  uint64_t c_full[2], p_full[2], o_full[2];
   uint64_t drain[2];
   uint32_t tmem_base;
   int abort_flag;
@@ -147,9 +149,11 @@ __device__ __forceinline__ void put_bits(uint8_t* base, int r, MaskT bits) {
 __device__ __forceinline__ bool wait_bounded(uint64_t* bar, uint32_t parity, volatile int* abort_flag, uint32_t* err,
                                              uint64_t limit_ns) {
   if (mbar_try_wait(bar, parity)) return true;
-  const uint64_t t0 = global_timer_ns();
-  while (!mbar_try_wait(bar, parity)) {
+  uint64_t t0 = 0;
+  for (uint32_t i = 1; !mbar_try_wait(bar, parity); ++i) {
+    if (i & 63u) continue;
     if (*abort_flag) return false;
+    if (!t0) t0 = global_timer_ns();
     if (global_timer_ns() - t0 > limit_ns) {
       *abort_flag = 1;
       atomicOr(err, PLSH_DEVERR_TIMEOUT);
@@ -217,7 +221,6 @@ serve_tc_kernel(const __grid_constant__ CUtensorMap tmap_q, const __grid_constan
         mbar_init(&sm.feat_full[w][i], 1);
         mbar_init(&sm.feat_empty[w][i], 5);
       }
-      mbar_init(&sm.s_free[w], 4);
       mbar_init(&sm.c_full[w], 1);
       mbar_init(&sm.p_full[w], 4);
       mbar_init(&sm.o_full[w], 1);
@@ -245,7 +248,7 @@ serve_tc_kernel(const __grid_constant__ CUtensorMap tmap_q, const __grid_constan
     const uint32_t base = tmem + kStreamCols * w + (static_cast<uint32_t>(32 * rg) << 16);
     const float sc = 1.4426950408889634f / sqrtf(static_cast<float>(D));
     int g = 0, items = 0;
-    float m2 = -INFINITY, l = 0.0f;
+    float m2 = 0.0f, l = 0.0f;
     int d_h = 0, d_i0 = 0, d_c0 = 0, d_pos0 = 0, d_end = 0;  // the finished item, until its epilogue
     bool pending = false;
     // O / l of the item just finished, once its last product has completed
@@ -321,12 +324,14 @@ serve_tc_kernel(const __grid_constant__ CUtensorMap tmap_q, const __grid_constan
         for (int j = 0; j < steps; ++j) {
           const int at = steps - 1 - j;               // word of four keys, counted from the tile half's first scanned key
           const MaskT* b4 = bm + 32 * (rg & ~1) + 4 * at;
+          MaskT bv[4];
+          tiles::load4(b4, bv);
           uint32_t four = 0;
 #pragma unroll
           for (int e = 3; e >= 0; --e) {
             if (32 * (rg & 1) + lane >= 4 * at + e) {
               four |= static_cast<uint32_t>(s - popc_mask<MaskT>(mid)) << (8 * e);
-              mid = static_cast<MaskT>(mid | b4[e]);
+              mid = static_cast<MaskT>(mid | bv[e]);
             }
           }
 #pragma unroll
@@ -342,7 +347,7 @@ serve_tc_kernel(const __grid_constant__ CUtensorMap tmap_q, const __grid_constan
         pending = false;
       }
       if (!valid) break;
-      m2 = -INFINITY;
+      m2 = 0.0f;
       l = 0.0f;
       bool ok = true;
       for (int u = first; u >= low; --u, ++g) {
@@ -366,92 +371,125 @@ serve_tc_kernel(const __grid_constant__ CUtensorMap tmap_q, const __grid_constan
         if (lane == 0) mbar_arrive(&sm.feat_empty[w][fs]);
         if (!wait_all(&sm.c_full[w], g)) { ok = false; break; }
         tc_fence_after();
-        uint32_t sv[2][32];
-        float top = -INFINITY;
+        if (scan) {  // the scanned counts join the others' place (C's columns, free until P goes there)
+#pragma unroll
+          for (int hf = 0; hf < 2; ++hf) {
+            if (!live[hf]) continue;
+            uint32_t cv[32];
+#pragma unroll
+            for (int i = 0; i < 32; ++i)
+              cv[i] = __float_as_uint(4.0f * static_cast<float>((cnt[8 * hf + (i >> 2)] >> (8 * (i & 3))) & 0xFFu));
+            tmem_st32(base + kColC + 32u * hf, cv);
+          }
+          tmem_wait_st();
+        }
+        // P = 4c 2^(S sc - m) against the reference m, whatever S's maximum is: fp32 and bf16 hold P far beyond what the
+        // softmax needs, so m has to be near the maximum only within some 2^60
+        uint32_t pk[2][16];
+        const uint64_t sc2 = f2_pack(sc, sc), negm2 = f2_pack(-m2, -m2);
+        uint64_t ls2[2] = {0ull, 0ull};
 #pragma unroll
         for (int hf = 0; hf < 2; ++hf) {
-          if (!live[hf]) continue;
-          tmem_ld32(base + kColS + 32u * hf, sv[hf]);
-          if (scan) {
-            tmem_wait_ld();
-            regs_after_wait(sv[hf]);
-#pragma unroll
-            for (int i = 0; i < 32; ++i) {
-              const uint32_t c = (cnt[8 * hf + (i >> 2)] >> (8 * (i & 3))) & 0xFFu;
-              if (c) top = fmaxf(top, __uint_as_float(sv[hf][i]));
-            }
-          } else {
-            uint32_t cv[32];
+          if (live[hf]) {
+            uint32_t sv[32], cv[32];
+            tmem_ld32(base + kColS + 32u * hf, sv);
             tmem_ld32(base + kColC + 32u * hf, cv);
             tmem_wait_ld();
-            regs_after_wait(sv[hf]);
+            regs_after_wait(sv);
+            regs_after_wait(cv);
+#pragma unroll
+            for (int i = 0; i < 16; ++i) {
+              float x0, x1;
+              f2_unpack(f2_fma(f2_pack(__uint_as_float(sv[2 * i]), __uint_as_float(sv[2 * i + 1])), sc2, negm2), x0, x1);
+              const uint64_t p2 = f2_mul(f2_pack(ex2_approx(x0), ex2_approx(x1)),
+                                         f2_pack(__uint_as_float(cv[2 * i]), __uint_as_float(cv[2 * i + 1])));
+              ls2[i & 1] = f2_add(ls2[i & 1], p2);
+              float p0, p1;
+              f2_unpack(p2, p0, p1);
+              pk[hf][i] = pack_bf16x2(p0, p1);
+            }
+          } else {
+#pragma unroll
+            for (int i = 0; i < 16; ++i) pk[hf][i] = 0u;
+          }
+        }
+        float lsum;
+        {
+          float a0, a1, b0, b1;
+          f2_unpack(ls2[0], a0, a1);
+          f2_unpack(ls2[1], b0, b1);
+          lsum = (a0 + a1) + (b0 + b1);
+        }
+        // out of range: a sum too large (or NaN: an infinite exponential of a key without weight), or, where the row's own key is, too small
+        const bool redo = i0 + r >= pos0 && i0 + r < end && (!(lsum <= kSumMax) || (scan && lsum < kSumMin));
+        if (!__any_sync(0xffffffffu, redo)) {
+          tmem_st16(base + kColC, pk[0]);
+          tmem_st16(base + kColC + 16u, pk[1]);
+        } else {
+          // the maximum of the keys with weight becomes those rows' reference; O and l follow (PV(g - 1) has completed: C(g) came after it)
+          float top = -INFINITY;
+#pragma unroll 1
+          for (int hf = 0; hf < 2; ++hf) {
+            if (!(hf ? live[1] : live[0])) continue;
+            uint32_t sv[32], cv[32];
+            tmem_ld32(base + kColS + 32u * hf, sv);
+            tmem_ld32(base + kColC + 32u * hf, cv);
+            tmem_wait_ld();
+            regs_after_wait(sv);
             regs_after_wait(cv);
 #pragma unroll
             for (int i = 0; i < 32; ++i)
-              if (__uint_as_float(cv[i]) > 0.0f) top = fmaxf(top, __uint_as_float(sv[hf][i]));
+              if (__uint_as_float(cv[i]) > 0.0f) top = fmaxf(top, __uint_as_float(sv[i]));
           }
-        }
-        // S has been read
-        tc_fence_before();
-        __syncwarp();
-        if (lane == 0) mbar_arrive(&sm.s_free[w]);
-        const float mt = top * sc;
-        float alpha = 1.0f;
-        bool rescale = false;
-        if (mt > m2 + kRescaleThreshold) {
-          if (m2 != -INFINITY) {
-            alpha = ex2_approx(m2 - mt);
-            rescale = true;
+          float alpha = 1.0f;
+          if (redo && top != -INFINITY) {  // a row that has a sum already keeps its reference or raises it
+            const float m_new = l > 0.0f ? fmaxf(m2, top * sc) : top * sc;
+            if (l > 0.0f) alpha = exp2f(m2 - m_new);
+            m2 = m_new;
           }
-          m2 = mt;
-        }
-        if (__any_sync(0xffffffffu, rescale)) {  // C(g) was issued after PV(g - 1), which has therefore completed
+          l *= alpha;
+          if (u != first) {  // the first tile finds no O
 #pragma unroll 1
-          for (int q4 = 0; q4 < D / 16; ++q4) {
-            uint32_t raw[16];
-            tmem_ld16(base + kColO + 16u * q4, raw);
-            tmem_wait_ld();
-            regs_after_wait(raw);
+            for (int q4 = 0; q4 < D / 16; ++q4) {
+              uint32_t raw[16];
+              tmem_ld16(base + kColO + 16u * q4, raw);
+              tmem_wait_ld();
+              regs_after_wait(raw);
 #pragma unroll
-            for (int e = 0; e < 16; ++e) raw[e] = __float_as_uint(__uint_as_float(raw[e]) * alpha);
-            tmem_st16(base + kColO + 16u * q4, raw);
+              for (int e = 0; e < 16; ++e) raw[e] = __float_as_uint(__uint_as_float(raw[e]) * alpha);
+              tmem_st16(base + kColO + 16u * q4, raw);
+            }
           }
-        }
-        float lsum = 0.0f;
+          float ls[4] = {0.0f, 0.0f, 0.0f, 0.0f};  // summed in the order of the path above: the warp's other rows keep their bits
+#pragma unroll 1
+          for (int hf = 0; hf < 2; ++hf) {
+            uint32_t pr[16];
 #pragma unroll
-        for (int hf = 0; hf < 2; ++hf) {
-          uint32_t pk[16];
-          if (live[hf]) {
-            float cf[32];
-            if (scan) {
-#pragma unroll
-              for (int i = 0; i < 32; ++i) cf[i] = 4.0f * static_cast<float>((cnt[8 * hf + (i >> 2)] >> (8 * (i & 3))) & 0xFFu);
-            } else {
-              uint32_t cv[32];
+            for (int i = 0; i < 16; ++i) pr[i] = 0u;
+            if (hf ? live[1] : live[0]) {
+              uint32_t sv[32], cv[32];
+              tmem_ld32(base + kColS + 32u * hf, sv);
               tmem_ld32(base + kColC + 32u * hf, cv);
               tmem_wait_ld();
+              regs_after_wait(sv);
               regs_after_wait(cv);
 #pragma unroll
-              for (int i = 0; i < 32; ++i) cf[i] = __uint_as_float(cv[i]);
-            }
+              for (int i = 0; i < 16; ++i) {
+                float p[2];
 #pragma unroll
-            for (int i = 0; i < 16; ++i) {
-              float p[2];
-#pragma unroll
-              for (int e = 0; e < 2; ++e) {
-                const float x = fmaf(__uint_as_float(sv[hf][2 * i + e]), sc, -m2);
-                p[e] = cf[2 * i + e] > 0.0f ? cf[2 * i + e] * ex2_approx(x) : 0.0f;
-                lsum += p[e];
+                for (int e = 0; e < 2; ++e) {
+                  const float c = __uint_as_float(cv[2 * i + e]);
+                  p[e] = c > 0.0f ? c * ex2_approx(fmaf(__uint_as_float(sv[2 * i + e]), sc, -m2)) : 0.0f;
+                  ls[2 * (i & 1) + e] += p[e];
+                }
+                pr[i] = pack_bf16x2(p[0], p[1]);
               }
-              pk[i] = pack_bf16x2(p[0], p[1]);
             }
-          } else {
-#pragma unroll
-            for (int i = 0; i < 16; ++i) pk[i] = 0u;
+            tmem_st16(base + kColC + 16u * hf, pr);  // over C of the half before, which has been read
           }
-          tmem_st16(base + kColC + 16u * hf, pk);
+          lsum = (ls[0] + ls[1]) + (ls[2] + ls[3]);
         }
-        l = l * alpha + lsum;
+        l += lsum;
         tmem_wait_st();
         tc_fence_before();
         __syncwarp();
@@ -477,7 +515,12 @@ serve_tc_kernel(const __grid_constant__ CUtensorMap tmap_q, const __grid_constan
     }
     int n = 0, k = 0, loads[2] = {0, 0};  // key tiles, items and Q tiles per stream so far
     bool ok = true;
-    for (int x = blockIdx.x; ok && x < prm.items; x += gridDim.x) {
+    // every other round backwards: the items' costs fall along the list, so each block's early ones weigh against its late ones
+    for (int round = 0; ok; ++round) {
+      const long long x_ = static_cast<long long>(round) * gridDim.x + ((round & 1) ? gridDim.x - 1 - blockIdx.x : blockIdx.x);
+      if (static_cast<long long>(round) * gridDim.x >= prm.items) break;
+      if (x_ >= prm.items) continue;
+      const int x = static_cast<int>(x_);
       const int hr = x / prm.slots, slot = x % prm.slots;
       const int h = H <= kMaxSortedHeads ? static_cast<int>(sm.order[hr]) : hr;
       const int mult = prm.sq.start ? 2 : 1;
@@ -612,8 +655,8 @@ serve_tc_kernel(const __grid_constant__ CUtensorMap tmap_q, const __grid_constan
       };
       bool ok = !prm.withhold_mma;
       for (int k = 0; ok; ++k) {
-        // no item yet: the loads that come before it may need the pending tile's place
-        if (!mbar_test_wait(&sm.item_full[k % kItems], (k / kItems) & 1) && !flush()) break;
+        // the pending product first: the loads that come before the next item may need its tile's place
+        if (!flush()) break;
         if (!wait(&sm.item_full[k % kItems], k / kItems)) break;
         const Item& item = sm.item[k % kItems];
         const int valid = item.valid, first = item.first[w], low = item.low[w], above = item.n0 + item.top, row_tile = 4 * item.tp + 2 * w;
@@ -621,11 +664,10 @@ serve_tc_kernel(const __grid_constant__ CUtensorMap tmap_q, const __grid_constan
         if (!valid) break;
         for (int u = first; ok && u >= low; --u, ++g) {
           const int n = above - u, st = n % kStages;
-          // S(g) before PV(g - 1), which waits for the softmax, if S(g)'s operands are there. Where they are not, PV(g - 1) goes
-          // first: the tile to come may need the very place that tile g - 1 still holds.
-          if (pend >= 0 && !(mbar_test_wait(&sm.kv_full[st], (n / kStages) & 1) && (u != first || mbar_test_wait(&sm.q_full[w], items & 1))) &&
-              !flush()) { ok = false; break; }
-          if (!wait(&sm.kv_full[st], n / kStages) || (u == first && !wait(&sm.q_full[w], items)) || (g > 0 && !wait(&sm.s_free[w], g - 1))) {
+          // P(g - 1) is there: S(g - 1) has been read too
+          const int fs = g & 1;
+          if (!flush() || !wait(&sm.kv_full[st], n / kStages) || !wait(&sm.feat_full[w][fs], g >> 1) ||
+              (u == first && !wait(&sm.q_full[w], items))) {
             ok = false;
             break;
           }
@@ -636,13 +678,9 @@ serve_tc_kernel(const __grid_constant__ CUtensorMap tmap_q, const __grid_constan
             mma_ss(base + kColS, q_desc + static_cast<uint64_t>(((kk >> 2) * (kRows * 128) + (kk & 3) * 32) >> 4),
                    kd + static_cast<uint64_t>(((kk >> 2) * (kKeys * 128) + (kk & 3) * 32) >> 4), idesc_qk, kk > 0 ? 1u : 0u);
           if (u == low) mma_commit(&sm.q_empty[w]);
-          if (!flush()) { ok = false; break; }
           // C(g), after PV(g - 1), whose P lies where C goes. The upper diagonal tile has none.
-          const int fs = g & 1;
-          if (!wait(&sm.feat_full[w][fs], g >> 1)) { ok = false; break; }
           const int rel = u - row_tile;  // 1: keys 64..127 of the row tile, 0: keys 0..63, < 0: before it
           if (rel <= 0) {
-            tc_fence_after();
             const uint64_t ad = a_desc + static_cast<uint64_t>((rel == 0 ? 0 : kRows * kFeat) >> 4);
             const uint64_t bd = b_desc + static_cast<uint64_t>((fs * (kKeys * kFeat)) >> 4);
 #pragma unroll
@@ -705,12 +743,8 @@ serve_tc_kernel(const __grid_constant__ CUtensorMap tmap_q, const __grid_constan
       if (g >= 1 && !wait_all(&sm.feat_empty[w][(g - 1) & 1], (g - 1) >> 1)) { ok = false; break; }
       put_bits<MaskT>(sm.a[w][0], 64 + lane, static_cast<MaskT>(FULL & ~in[2]));
       put_bits<MaskT>(sm.a[w][0], 96 + lane, static_cast<MaskT>(FULL & ~(tot[2] | in[3])));
-      before = 0;
-#pragma unroll
-      for (int q = 0; q < 4; ++q) {
-        put_bits<MaskT>(sm.a[w][1], 32 * q + lane, static_cast<MaskT>(FULL & ~(before | in[q])));
-        before = static_cast<MaskT>(before | tot[q]);
-      }
+#pragma unroll 1
+      for (int r = lane; r < kRows; r += 32) put_bits<MaskT>(sm.a[w][1], r, static_cast<MaskT>(FULL & ~sm.pre[w][rb][r]));
       MaskT gap = 0;
       for (int u = first; ok && u >= low; --u, ++g) {
         kv[0] = nx[0];
@@ -735,14 +769,16 @@ serve_tc_kernel(const __grid_constant__ CUtensorMap tmap_q, const __grid_constan
           sm.upper[w][fs] = t1;
         }
         if (rel < 0) gap = static_cast<MaskT>(gap | t0 | t1);
-        // V rows past the end: another sequence's, or nothing at all
+        // rows past the end: another sequence's, or nothing at all
         if (kKeys * (u + 1) > end) {
           const int n = above - u, st = n % kStages;
           if (!wait_all(&sm.kv_full[st], n / kStages)) { ok = false; break; }
           const int r0 = end - kKeys * u;
           for (int e = lane; e < (kKeys - r0) * (D / 8); e += 32) {
             const int r = r0 + e / (D / 8), c = e % (D / 8);
-            *reinterpret_cast<uint4*>(sm.v[st] + (c >> 3) * (kKeys * 128) + r * 128 + (c & 7) * 16) = make_uint4(0, 0, 0, 0);
+            const int at = (c >> 3) * (kKeys * 128) + r * 128 + (c & 7) * 16;
+            *reinterpret_cast<uint4*>(sm.k[st] + at) = make_uint4(0, 0, 0, 0);
+            *reinterpret_cast<uint4*>(sm.v[st] + at) = make_uint4(0, 0, 0, 0);
           }
         }
         fence_proxy_async_smem();
