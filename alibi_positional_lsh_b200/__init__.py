@@ -89,7 +89,9 @@ def _load() -> ctypes.CDLL:
     i64 = ctypes.c_int64
     lib.plsh_packed_fwd.restype = i32
     lib.plsh_packed_fwd.argtypes = [vp, i64, i64, vp, i64, i64, vp, i64, i64, i32, i32, i32, vp, i32, i32, i32, i32, i32, vp,
-                                    vp, vp, vp, vp, vp]
+                                    vp, vp, vp, vp, vp, vp]
+    lib.plsh_near_counts.restype = i32
+    lib.plsh_near_counts.argtypes = [vp, i32, i32, i32, vp, vp]
     lib.plsh_cache_append.restype = i32
     lib.plsh_cache_append.argtypes = [vp, i64, i64, vp, i64, i64, i32, i32, i32, vp, vp, i32, i32, vp, vp, vp, vp, vp, i32,
                                       i32, i32, vp, vp]
@@ -281,13 +283,18 @@ def _rows_arg(t, name: str):
 
 
 def plsh_packed_fwd(Q, K, V, dtype: int, cu_dev, H: int, H_kv: int, d: int, s: int, max_len: int, tile_span_dev, bmask_dev,
-                    O, row_sum, err_dev, stream=None) -> None:
+                    near_dev, O, row_sum, err_dev, stream=None) -> None:
     """Q [T][H][d], K, V [T][H_kv][d], any strides with contiguous rows; cu_dev int32 [S + 1]."""
     _check(_lib.plsh_packed_fwd(*_rows_arg(Q, "Q"), *_rows_arg(K, "K"), *_rows_arg(V, "V"), dtype, Q.shape[0],
                                 cu_dev.shape[0] - 1, _dev_ptr(cu_dev, "cu_dev"), H, H_kv, d, s, max_len,
                                 _dev_ptr(tile_span_dev, "tile_span_dev"), _dev_ptr(bmask_dev, "bmask_dev"),
-                                _dev_ptr(O, "O"), _dev_ptr(row_sum, "row_sum"), _dev_ptr(err_dev, "err_dev"),
-                                _stream_ptr(stream)))
+                                _dev_ptr(near_dev, "near_dev"), _dev_ptr(O, "O"), _dev_ptr(row_sum, "row_sum"),
+                                _dev_ptr(err_dev, "err_dev"), _stream_ptr(stream)))
+
+
+def plsh_near_counts(bmask_dev, H: int, s: int, n: int, near_dev, stream=None) -> None:
+    _check(_lib.plsh_near_counts(_dev_ptr(bmask_dev, "bmask_dev"), H, s, n, _dev_ptr(near_dev, "near_dev"),
+                                 _stream_ptr(stream)))
 
 
 def plsh_cache_append(K, V, dtype: int, cu_dev, start_dev, H_kv: int, d: int, k_pages, v_pages, k_exp, v_exp,

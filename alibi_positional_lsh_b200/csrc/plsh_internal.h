@@ -120,9 +120,11 @@ struct ServeArgs {
   SeqArgs sq;
   int dtype, H, H_kv, d, s;
   const int32_t* spans; const void* bmask;  // plsh_window's, causal, over max_len positions
+  const uint8_t* near;                      // launch_near's; the bf16 kernel's
   void* O; float* row_sum; uint32_t* err;
 };
 int launch_serve_simt(const ServeArgs& a, cudaStream_t st);
+int launch_near(const void* bmask, int H, int s, int n, uint8_t* near, cudaStream_t st);
 int launch_serve_tc(const ServeArgs& a, cudaStream_t st);  // bf16, packed K and V
 int launch_attention_tc(const AttnArgs& a, cudaStream_t st);
 

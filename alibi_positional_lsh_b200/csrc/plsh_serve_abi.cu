@@ -76,10 +76,19 @@ int check_plan(const char* fn, int s, const int32_t* spans, const void* bmask, c
 
 using plsh::fail;
 
+extern "C" int plsh_near_counts(const void* bmask_dev, int H, int s, int n, uint8_t* near_dev, void* stream) {
+  const char* fn = "plsh_near_counts";
+  if (H < 1 || H > 65535 || n < 1 || n > (1 << 30) || s < 1 || s > PLSH_MAX_S)
+    return fail(PLSH_ERR_INVALID_ARG, "%s: need 1 <= H <= 65535, 1 <= n <= 2^30 and 1 <= s <= %d (H=%d n=%d s=%d)", fn, PLSH_MAX_S, H, n, s);
+  if (!bmask_dev || !near_dev) return fail(PLSH_ERR_INVALID_ARG, "%s: null pointer", fn);
+  if (!plsh::aligned16(near_dev)) return fail(PLSH_ERR_INVALID_ARG, "%s: near must be 16-byte aligned", fn);
+  return plsh::launch_near(bmask_dev, H, s, n, near_dev, static_cast<cudaStream_t>(stream));
+}
+
 extern "C" int plsh_packed_fwd(const void* Q, int64_t q_token, int64_t q_head, const void* K, int64_t k_token, int64_t k_head,
                                const void* V, int64_t v_token, int64_t v_head, int dtype, int T, int S,
                                const int32_t* cu_dev, int H, int H_kv, int d, int s, int max_len,
-                               const int32_t* tile_span_dev, const void* bmask_dev, void* O, float* row_sum,
+                               const int32_t* tile_span_dev, const void* bmask_dev, const uint8_t* near_dev, void* O, float* row_sum,
                                uint32_t* err_dev, void* stream) {
   const char* fn = "plsh_packed_fwd";
   if (int rc = plsh::check_seqs(fn, T, S, cu_dev, max_len)) return rc;
@@ -88,7 +97,10 @@ extern "C" int plsh_packed_fwd(const void* Q, int64_t q_token, int64_t q_head, c
   if (int rc = plsh::check_rows(fn, "K", K, dtype, d, H_kv, T, k_token, k_head)) return rc;
   if (int rc = plsh::check_rows(fn, "V", V, dtype, d, H_kv, T, v_token, v_head)) return rc;
   if (int rc = plsh::check_plan(fn, s, tile_span_dev, bmask_dev, O, row_sum, err_dev)) return rc;
+  if (dtype == PLSH_BF16 && (!near_dev || !plsh::aligned16(near_dev)))
+    return fail(PLSH_ERR_INVALID_ARG, "%s: bf16 needs near_dev, 16-byte aligned", fn);
   plsh::ServeArgs a{};
+  a.near = near_dev;
   a.Q = Q; a.qs = {q_token, q_head};
   a.K = K; a.ks = {k_token, k_head};
   a.V = V; a.vs = {v_token, v_head};

@@ -10,8 +10,9 @@
 // a product of two 0/1 matrices with one column per hash. They are written as e4m3 bytes and
 // multiplied by the tensor cores beside S: one instruction per 32 hashes, instead of an OR, a
 // population count and a conversion for every score. Both are exact (each byte is 2.0 or 0, so the product is
-// 4 c; the 4 cancels in O and leaves row_sum as two in the logarithm). Only the scores within 32 or
-// 64 keys of the diagonal are counted by scanning the boundary masks from the row down.
+// 4 c; the 4 cancels in O and leaves row_sum as two in the logarithm). Only the counts of a row's own
+// 64-key tile, where no key lies behind all rows, are read: they depend on the position and the head alone, and the plan
+// holds them as bytes (near_kernel).
 //
 // Work. One item is a pair of 128-row tiles (256 positions) of one head; the tiles' windows
 // overlap, so both read the same 64-key tiles of K and V from shared memory, from the diagonal down.
@@ -49,7 +50,7 @@ using tiles::regs_after_wait;
 
 constexpr int kThreads = 512;                 // 16 warps
 constexpr int kSoftmaxWarps = 8;              // warps 0-3 stream 0 (the lower row tile), 4-7 stream 1
-constexpr int kWarpLoad = 8, kWarpMma = 9, kWarpMask = 11;  // one MMA and one mask warp per stream
+constexpr int kWarpLoad = 8, kWarpMma = 9, kWarpMask = 11, kWarpItems = 13;  // one MMA and one mask warp per stream
 constexpr int kRows = 128, kKeys = 64;
 constexpr int kItems = 4;                     // item descriptors in flight
 constexpr uint32_t kTmemCols = 512, kStreamCols = 256;
@@ -63,7 +64,7 @@ constexpr uint32_t kRegsSoftmax = 192, kRegsRest = 64;
 // Two row tiles of one head: positions 256 tp .. 256 tp + 255 of sequence s.
 struct Item {
   int valid, h, tp, c0, pos0, end, s;
-  int top;       // highest key tile
+  int top, bottom;  // highest and lowest key tile
   int low[2];    // lowest key tile of each stream
   int first[2];  // highest key tile of each stream; first < low: the stream has no rows here
   int n0;        // number of the first key tile in the block's sequence of loads
@@ -78,8 +79,8 @@ struct __align__(1024) TcSmem {
   uint8_t v[kStages][kKBytes];
   uint8_t a[2][2][kRows * kFeat];   // [stream][0: pivot inside the row tile (rows 64..127), 1: pivot before it]
   uint8_t b[2][2][kKeys * kFeat];   // [stream][stage]
-  MaskT bm[2][2][kRows];            // boundary masks of the row tile [stream][item parity]
-  MaskT pre[2][2][kRows];           // OR of the masks from the row tile's first row to the row
+  MaskT pre[2][2][kRows];           // [stream][item parity]: OR of the boundary masks from the row tile's first row to the row
+  MaskT mid[2][2][kRows / 2];       // for rows 64..127: OR from row 64 to the row
   MaskT gap[2][2], upper[2][2];     // [stream][stage]: OR between the key tile and the row tile; OR of the key tile's keys 32..63
   Item item[kItems];
   int16_t order[kMaxSortedHeads];
@@ -87,7 +88,6 @@ struct __align__(1024) TcSmem {
   uint64_t item_full[kItems], item_empty[kItems];
   uint64_t q_full[2], q_empty[2];
   uint64_t kv_full[kStages], kv_empty[kStages];
-  uint64_t row_full[2][2], row_empty[2][2];
   uint64_t feat_full[2][2], feat_empty[2][2];
   uint64_t c_full[2], p_full[2], o_full[2];
   uint64_t drain[2];
@@ -100,6 +100,7 @@ struct TcParams {
   int H, H_kv, s, slots, items;
   int q_swap, k_swap, v_swap;  // tensor map's second coordinate is the token (head-major storage) instead of the head
   const int32_t* spans;
+  const uint8_t* near;  // [H][max_len][64]: c of the keys of each position's own 64-key tile
   uint64_t wait_ns;
   int withhold_mma;
 };
@@ -129,6 +130,15 @@ __device__ __forceinline__ uint64_t smem_desc_plain(uint32_t saddr, uint32_t gro
 __host__ __device__ constexpr uint32_t idesc_e4m3_f32(int M, int N) {
   return (1u << 4) | (static_cast<uint32_t>(N >> 3) << 17) | (static_cast<uint32_t>(M >> 4) << 24);
 }
+
+__device__ __forceinline__ bool elect_one() {
+  uint32_t p;
+  asm volatile("{\n\t.reg .pred q;\n\telect.sync _|q, 0xffffffff;\n\tselp.u32 %0, 1, 0, q;\n\t}" : "=r"(p));
+  return p != 0;
+}
+
+// A value that all lanes hold alike, known as such to the compiler.
+__device__ __forceinline__ int uniform(int x) { return __shfl_sync(0xffffffffu, x, 0); }
 
 // Row r of a 0/1 operand: byte k is 0x40 (e4m3 2.0) where bit k is set. Four bits spread to four bytes by one multiply.
 __device__ __forceinline__ uint32_t spread4(uint32_t bits) { return ((bits & 0xFu) * (0x00204081u << 6)) & 0x40404040u; }
@@ -163,6 +173,27 @@ __device__ __forceinline__ bool wait_bounded(uint64_t* bar, uint32_t parity, vol
   return true;
 }
 
+// near[h][p][k]: c of position p and key k of its own 64-key tile (0 past p). One thread per position scans from it down.
+template <typename MaskT>
+__global__ void __launch_bounds__(256) near_kernel(const MaskT* __restrict__ bmask, int s, int n, uint8_t* __restrict__ near) {
+  const int p = blockIdx.x * 256 + threadIdx.x;
+  if (p >= n) return;
+  const MaskT* bm = bmask + static_cast<size_t>(blockIdx.y) * n;
+  uint32_t* out = reinterpret_cast<uint32_t*>(near + (static_cast<size_t>(blockIdx.y) * n + p) * kKeys);
+  const int j0 = p & ~(kKeys - 1);
+  MaskT R = 0;
+  for (int w = kKeys / 4 - 1; w >= 0; --w) {
+    uint32_t four = 0;
+    for (int e = 3; e >= 0; --e) {
+      const int j = j0 + 4 * w + e;
+      if (j > p) continue;
+      four |= static_cast<uint32_t>(s - popc_mask<MaskT>(R)) << (8 * e);
+      R = static_cast<MaskT>(R | bm[j]);
+    }
+    out[w] = four;
+  }
+}
+
 // ---- the kernel
 
 template <int D, typename MaskT, int kStages>
@@ -176,7 +207,7 @@ serve_tc_kernel(const __grid_constant__ CUtensorMap tmap_q, const __grid_constan
   const uint32_t smem_pad = (1024u - (smem_u32(smem_raw) & 1023u)) & 1023u;
   auto& sm = *reinterpret_cast<Smem*>(smem_raw + smem_pad);
   volatile int* abort_flag = &sm.abort_flag;
-  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  const int warp = uniform(threadIdx.x >> 5), lane = threadIdx.x & 31;
   const int H = prm.H, s = prm.s, max_len = prm.sq.max_len;
   const int T128 = (max_len + PLSH_TILE - 1) / PLSH_TILE;
   const MaskT FULL = (s >= static_cast<int>(8 * sizeof(MaskT))) ? static_cast<MaskT>(~static_cast<MaskT>(0))
@@ -206,7 +237,7 @@ serve_tc_kernel(const __grid_constant__ CUtensorMap tmap_q, const __grid_constan
     sm.abort_flag = 0;
     for (int i = 0; i < kItems; ++i) {
       mbar_init(&sm.item_full[i], 1);
-      mbar_init(&sm.item_empty[i], kSoftmaxWarps + 4);
+      mbar_init(&sm.item_empty[i], kSoftmaxWarps + 5);
     }
     for (int i = 0; i < kStages; ++i) {
       mbar_init(&sm.kv_full[i], 1);
@@ -216,8 +247,6 @@ serve_tc_kernel(const __grid_constant__ CUtensorMap tmap_q, const __grid_constan
       mbar_init(&sm.q_full[w], 1);
       mbar_init(&sm.q_empty[w], 1);
       for (int i = 0; i < 2; ++i) {
-        mbar_init(&sm.row_full[w][i], 1);
-        mbar_init(&sm.row_empty[w][i], 4);
         mbar_init(&sm.feat_full[w][i], 1);
         mbar_init(&sm.feat_empty[w][i], 5);
       }
@@ -235,7 +264,7 @@ serve_tc_kernel(const __grid_constant__ CUtensorMap tmap_q, const __grid_constan
   tc_fence_before();
   __syncthreads();
   tc_fence_after();
-  const uint32_t tmem = sm.tmem_base;
+  const uint32_t tmem = uniform(sm.tmem_base);
   auto wait = [&](uint64_t* bar, uint32_t parity) { return wait_bounded(bar, parity & 1u, abort_flag, err, prm.wait_ns); };
   // the same by a whole warp: false in every lane if any gave up
   auto wait_all = [&](uint64_t* bar, uint32_t parity) { return __all_sync(0xffffffffu, wait(bar, parity)) != 0; };
@@ -248,14 +277,14 @@ serve_tc_kernel(const __grid_constant__ CUtensorMap tmap_q, const __grid_constan
     const uint32_t base = tmem + kStreamCols * w + (static_cast<uint32_t>(32 * rg) << 16);
     const float sc = 1.4426950408889634f / sqrtf(static_cast<float>(D));
     int g = 0, items = 0;
-    float m2 = 0.0f, l = 0.0f;
     int d_h = 0, d_i0 = 0, d_c0 = 0, d_pos0 = 0, d_end = 0;  // the finished item, until its epilogue
+    float d_l = 1.0f, d_m = 0.0f;
     bool pending = false;
     // O / l of the item just finished, once its last product has completed
     auto epilogue = [&](int number) -> bool {
       if (!wait_all(&sm.o_full[w], number)) return false;
       tc_fence_after();
-      const float inv = 1.0f / l;
+      const float inv = 1.0f / d_l;
       const int p4 = lane & 3;
 #pragma unroll 1
       for (int blk = 0; blk < D / 32; ++blk) {
@@ -298,222 +327,182 @@ serve_tc_kernel(const __grid_constant__ CUtensorMap tmap_q, const __grid_constan
       const int p = d_i0 + r;
       if (p >= d_pos0 && p < d_end)
         row_sum[static_cast<size_t>(d_c0 + p - d_pos0) * H + d_h] =
-            (log2f(l) + m2 - 2.0f) * 0.6931471805599453f - logf(static_cast<float>(s));
+            (log2f(d_l) + d_m - 2.0f) * 0.6931471805599453f - logf(static_cast<float>(s));
       return true;
     };
-    for (int k = 0;; ++k) {
+    bool ok = true;
+    for (int k = 0; ok; ++k) {
       if (!wait_all(&sm.item_full[k % kItems], k / kItems)) break;
       const Item& item = sm.item[k % kItems];
-      const int valid = item.valid, first = item.first[w], low = item.low[w], h = item.h, i0 = 256 * item.tp + 128 * w;
+      const bool done = !item.valid;
+      const int first = item.first[w], low = item.low[w], h = item.h, i0 = 256 * item.tp + 128 * w;
       const int c0 = item.c0, pos0 = item.pos0, end = item.end;
       __syncwarp();
       if (lane == 0) mbar_arrive(&sm.item_empty[k % kItems]);
-      if (valid && first < low) continue;
+      if (!done && first < low) continue;
+      const bool mine = !done && i0 + r >= pos0 && i0 + r < end;  // the row holds a token
+      uint4 near[4];  // c of the 64 keys of the row's own key tile, one byte each
+#pragma unroll
+      for (int i = 0; i < 4; ++i) near[i] = make_uint4(0, 0, 0, 0);
+      if (mine) {
+        const uint4* src = reinterpret_cast<const uint4*>(prm.near + (static_cast<size_t>(h) * max_len + i0 + r) * kKeys);
+#pragma unroll
+        for (int i = 0; i < 4; ++i) near[i] = __ldg(src + i);
+      }
+      float m2 = 0.0f, l = 0.0f;
       MaskT pre = 0, mid = 0;
-      uint32_t cnt[16];  // c of the scanned keys, one byte each, as the halves of the tile: the warp's own 32 keys and, in odd blocks, the 32 before
-#pragma unroll
-      for (int i = 0; i < 16; ++i) cnt[i] = 0;
-      if (valid) {
-        const int rb = items & 1;
-        if (!wait_all(&sm.row_full[w][rb], items >> 1)) break;
-        const MaskT* bm = sm.bm[w][rb];
-        pre = sm.pre[w][rb][r];
-        // from the row down, four keys a step: own block first, then (odd blocks) the block before it
-        const int steps = (rg & 1) ? 16 : 8;
-#pragma unroll 1
-        for (int j = 0; j < steps; ++j) {
-          const int at = steps - 1 - j;               // word of four keys, counted from the tile half's first scanned key
-          const MaskT* b4 = bm + 32 * (rg & ~1) + 4 * at;
-          MaskT bv[4];
-          tiles::load4(b4, bv);
-          uint32_t four = 0;
-#pragma unroll
-          for (int e = 3; e >= 0; --e) {
-            if (32 * (rg & 1) + lane >= 4 * at + e) {
-              four |= static_cast<uint32_t>(s - popc_mask<MaskT>(mid)) << (8 * e);
-              mid = static_cast<MaskT>(mid | bv[e]);
-            }
+      for (int u = first; ok && (done || u >= low); --u, ++g) {
+        if (!done) {
+          const int fs = g & 1, rel = u - (i0 >> 6);
+          if (!wait_all(&sm.feat_full[w][fs], g >> 1)) { ok = false; break; }
+          if (u == first) {
+            pre = sm.pre[w][items & 1][r];
+            if (rg >= 2) mid = sm.mid[w][items & 1][r - 64];
           }
-#pragma unroll
-          for (int i = 0; i < 16; ++i)
-            if (i == at) cnt[i] = four;
-        }
-        // mid: OR from the row tile's half (row 0 or 64) to the row
-        __syncwarp();
-        if (lane == 0) mbar_arrive(&sm.row_empty[w][rb]);
-      }
-      if (pending) {
-        if (!epilogue(items - 1)) break;
-        pending = false;
-      }
-      if (!valid) break;
-      m2 = 0.0f;
-      l = 0.0f;
-      bool ok = true;
-      for (int u = first; u >= low; --u, ++g) {
-        const int fs = g & 1, rel = u - (i0 >> 6);
-        if (!wait_all(&sm.feat_full[w][fs], g >> 1)) { ok = false; break; }
-        // which 32-key halves hold weight for some row of the warp, and where its counts come from
-        const bool scan = rel >= 0 && rel == (rg >> 1);
-        bool live[2];
-        if (rel > 0 && rg < 2) {
-          live[0] = live[1] = false;
-        } else if (scan) {
-          // own keys in the half of the warp's block; odd blocks have the half before it too
-          live[1] = (rg & 1) != 0;
-          live[0] = true;
-        } else {
-          const MaskT keep = static_cast<MaskT>(FULL & ~((rel == 0 ? mid : pre) | sm.gap[w][fs]));
-          live[1] = __any_sync(0xffffffffu, keep != 0);
-          live[0] = __any_sync(0xffffffffu, static_cast<MaskT>(keep & ~sm.upper[w][fs]) != 0);
-        }
-        __syncwarp();
-        if (lane == 0) mbar_arrive(&sm.feat_empty[w][fs]);
-        if (!wait_all(&sm.c_full[w], g)) { ok = false; break; }
-        tc_fence_after();
-        if (scan) {  // the scanned counts join the others' place (C's columns, free until P goes there)
-#pragma unroll
-          for (int hf = 0; hf < 2; ++hf) {
-            if (!live[hf]) continue;
-            uint32_t cv[32];
-#pragma unroll
-            for (int i = 0; i < 32; ++i)
-              cv[i] = __float_as_uint(4.0f * static_cast<float>((cnt[8 * hf + (i >> 2)] >> (8 * (i & 3))) & 0xFFu));
-            tmem_st32(base + kColC + 32u * hf, cv);
+          // which 32-key halves hold weight for some row of the warp, and where the counts come from
+          const bool own = rel == (rg >> 1);
+          bool live0 = true, live1 = (rg & 1) != 0;  // own tile: the half of the warp's block, and for odd blocks the half before it
+          if (rel > 0 && rg < 2) {
+            live0 = live1 = false;
+          } else if (!own) {
+            const MaskT keep = static_cast<MaskT>(FULL & ~((rel == 0 ? mid : pre) | sm.gap[w][fs]));
+            live1 = __any_sync(0xffffffffu, keep != 0);
+            live0 = __any_sync(0xffffffffu, static_cast<MaskT>(keep & ~sm.upper[w][fs]) != 0);
           }
-          tmem_wait_st();
-        }
-        // P = 4c 2^(S sc - m) against the reference m, whatever S's maximum is: fp32 and bf16 hold P far beyond what the
-        // softmax needs, so m has to be near the maximum only within some 2^60
-        uint32_t pk[2][16];
-        const uint64_t sc2 = f2_pack(sc, sc), negm2 = f2_pack(-m2, -m2);
-        uint64_t ls2[2] = {0ull, 0ull};
-#pragma unroll
-        for (int hf = 0; hf < 2; ++hf) {
-          if (live[hf]) {
-            uint32_t sv[32], cv[32];
-            tmem_ld32(base + kColS + 32u * hf, sv);
-            tmem_ld32(base + kColC + 32u * hf, cv);
-            tmem_wait_ld();
-            regs_after_wait(sv);
-            regs_after_wait(cv);
-#pragma unroll
-            for (int i = 0; i < 16; ++i) {
-              float x0, x1;
-              f2_unpack(f2_fma(f2_pack(__uint_as_float(sv[2 * i]), __uint_as_float(sv[2 * i + 1])), sc2, negm2), x0, x1);
-              const uint64_t p2 = f2_mul(f2_pack(ex2_approx(x0), ex2_approx(x1)),
-                                         f2_pack(__uint_as_float(cv[2 * i]), __uint_as_float(cv[2 * i + 1])));
-              ls2[i & 1] = f2_add(ls2[i & 1], p2);
-              float p0, p1;
-              f2_unpack(p2, p0, p1);
-              pk[hf][i] = pack_bf16x2(p0, p1);
-            }
-          } else {
-#pragma unroll
-            for (int i = 0; i < 16; ++i) pk[hf][i] = 0u;
-          }
-        }
-        float lsum;
-        {
-          float a0, a1, b0, b1;
-          f2_unpack(ls2[0], a0, a1);
-          f2_unpack(ls2[1], b0, b1);
-          lsum = (a0 + a1) + (b0 + b1);
-        }
-        // out of range: a sum too large (or NaN: an infinite exponential of a key without weight), or, where the row's own key is, too small
-        const bool redo = i0 + r >= pos0 && i0 + r < end && (!(lsum <= kSumMax) || (scan && lsum < kSumMin));
-        if (!__any_sync(0xffffffffu, redo)) {
-          tmem_st16(base + kColC, pk[0]);
-          tmem_st16(base + kColC + 16u, pk[1]);
-        } else {
-          // the maximum of the keys with weight becomes those rows' reference; O and l follow (PV(g - 1) has completed: C(g) came after it)
-          float top = -INFINITY;
+          __syncwarp();
+          if (lane == 0) mbar_arrive(&sm.feat_empty[w][fs]);
+          if (!wait_all(&sm.c_full[w], g)) { ok = false; break; }
+          tc_fence_after();
+          // P = 4c 2^(S sc - m) against the reference m, whatever S's maximum is: fp32 and bf16 hold P far beyond what the
+          // softmax needs, so m has to be near the maximum only within some 2^60
+          float lsum = 0.0f;
 #pragma unroll 1
           for (int hf = 0; hf < 2; ++hf) {
-            if (!(hf ? live[1] : live[0])) continue;
-            uint32_t sv[32], cv[32];
-            tmem_ld32(base + kColS + 32u * hf, sv);
-            tmem_ld32(base + kColC + 32u * hf, cv);
-            tmem_wait_ld();
-            regs_after_wait(sv);
-            regs_after_wait(cv);
+            uint32_t pk[16];
 #pragma unroll
-            for (int i = 0; i < 32; ++i)
-              if (__uint_as_float(cv[i]) > 0.0f) top = fmaxf(top, __uint_as_float(sv[i]));
-          }
-          float alpha = 1.0f;
-          if (redo && top != -INFINITY) {  // a row that has a sum already keeps its reference or raises it
-            const float m_new = l > 0.0f ? fmaxf(m2, top * sc) : top * sc;
-            if (l > 0.0f) alpha = exp2f(m2 - m_new);
-            m2 = m_new;
-          }
-          l *= alpha;
-          if (u != first) {  // the first tile finds no O
-#pragma unroll 1
-            for (int q4 = 0; q4 < D / 16; ++q4) {
-              uint32_t raw[16];
-              tmem_ld16(base + kColO + 16u * q4, raw);
-              tmem_wait_ld();
-              regs_after_wait(raw);
-#pragma unroll
-              for (int e = 0; e < 16; ++e) raw[e] = __float_as_uint(__uint_as_float(raw[e]) * alpha);
-              tmem_st16(base + kColO + 16u * q4, raw);
-            }
-          }
-          float ls[4] = {0.0f, 0.0f, 0.0f, 0.0f};  // summed in the order of the path above: the warp's other rows keep their bits
-#pragma unroll 1
-          for (int hf = 0; hf < 2; ++hf) {
-            uint32_t pr[16];
-#pragma unroll
-            for (int i = 0; i < 16; ++i) pr[i] = 0u;
-            if (hf ? live[1] : live[0]) {
+            for (int i = 0; i < 16; ++i) pk[i] = 0u;
+            if (hf ? live1 : live0) {
               uint32_t sv[32], cv[32];
               tmem_ld32(base + kColS + 32u * hf, sv);
-              tmem_ld32(base + kColC + 32u * hf, cv);
+              if (own) {
+#pragma unroll
+                for (int i = 0; i < 8; ++i) {
+                  const uint4 n4 = hf ? near[2 + (i >> 2)] : near[i >> 2];
+                  const uint32_t w4 = (i & 3) == 0 ? n4.x : (i & 3) == 1 ? n4.y : (i & 3) == 2 ? n4.z : n4.w;
+                  // byte b as the float 2^23 + b, exactly; then 4 (f - 2^23)
+#pragma unroll
+                  for (int e = 0; e < 4; ++e)
+                    cv[4 * i + e] = __float_as_uint(fmaf(4.0f, __uint_as_float(__byte_perm(w4, 0x4B000000u, 0x7540u | e)), -33554432.0f));
+                }
+              } else {
+                tmem_ld32(base + kColC + 32u * hf, cv);
+              }
               tmem_wait_ld();
               regs_after_wait(sv);
               regs_after_wait(cv);
+              float hsum;
+              {
+                const uint64_t sc2 = f2_pack(sc, sc), negm2 = f2_pack(-m2, -m2);
+                uint64_t ls2[2] = {0ull, 0ull};
 #pragma unroll
-              for (int i = 0; i < 16; ++i) {
-                float p[2];
-#pragma unroll
-                for (int e = 0; e < 2; ++e) {
-                  const float c = __uint_as_float(cv[2 * i + e]);
-                  p[e] = c > 0.0f ? c * ex2_approx(fmaf(__uint_as_float(sv[2 * i + e]), sc, -m2)) : 0.0f;
-                  ls[2 * (i & 1) + e] += p[e];
+                for (int i = 0; i < 16; ++i) {
+                  float x0, x1;
+                  f2_unpack(f2_fma(f2_pack(__uint_as_float(sv[2 * i]), __uint_as_float(sv[2 * i + 1])), sc2, negm2), x0, x1);
+                  const uint64_t p2 = f2_mul(f2_pack(ex2_approx(x0), ex2_approx(x1)),
+                                             f2_pack(__uint_as_float(cv[2 * i]), __uint_as_float(cv[2 * i + 1])));
+                  ls2[i & 1] = f2_add(ls2[i & 1], p2);
+                  float p0, p1;
+                  f2_unpack(p2, p0, p1);
+                  pk[i] = pack_bf16x2(p0, p1);
                 }
-                pr[i] = pack_bf16x2(p[0], p[1]);
+                float a0, a1, b0, b1;
+                f2_unpack(ls2[0], a0, a1);
+                f2_unpack(ls2[1], b0, b1);
+                hsum = (a0 + a1) + (b0 + b1);
               }
+              // out of range: a sum too large (or NaN: an infinite exponential of a key without weight), or too small once the
+              // row's own key is in it
+              const bool redo = mine && (!(hsum <= kSumMax) || (own && hf == (rg & 1) && l + lsum + hsum < kSumMin));
+              if (__any_sync(0xffffffffu, redo)) {
+                // these rows' reference becomes the maximum so far over keys with weight, rounded up to a whole number, so that
+                // everything before follows by an exact power of two (PV(g - 1) has completed: C(g) came after it); the warp's other rows keep their bits
+                float top = -INFINITY;
+#pragma unroll
+                for (int i = 0; i < 32; ++i)
+                  if (__uint_as_float(cv[i]) > 0.0f) top = fmaxf(top, __uint_as_float(sv[i]));
+                float alpha = 1.0f;
+                if (redo && top != -INFINITY) {
+                  const float so_far = l + lsum;
+                  const float m_new = ceilf(so_far > 0.0f ? fmaxf(top * sc, m2 + log2f(so_far)) : top * sc);
+                  if (so_far > 0.0f) alpha = exp2f(fminf(fmaxf(m2 - m_new, -126.0f), 126.0f));
+                  m2 = m_new;
+                }
+                l *= alpha;
+                lsum *= alpha;
+                tmem_wait_st();
+                const uint32_t alpha2 = pack_bf16x2(alpha, alpha);
+#pragma unroll 1
+                for (int q4 = (u != first ? 0 : D / 16); q4 < D / 16 + hf; ++q4) {  // O unless the tile is the first, and P of the half before
+                  const bool is_p = q4 == D / 16;
+                  const uint32_t at = is_p ? base + kColC : base + kColO + 16u * q4;
+                  uint32_t raw[16];
+                  tmem_ld16(at, raw);
+                  tmem_wait_ld();
+                  regs_after_wait(raw);
+#pragma unroll
+                  for (int e = 0; e < 16; ++e) {
+                    const __nv_bfloat162 p2 = __hmul2(*reinterpret_cast<const __nv_bfloat162*>(&raw[e]),
+                                                      *reinterpret_cast<const __nv_bfloat162*>(&alpha2));
+                    raw[e] = is_p ? *reinterpret_cast<const uint32_t*>(&p2) : __float_as_uint(__uint_as_float(raw[e]) * alpha);
+                  }
+                  tmem_st16(at, raw);
+                }
+                float ls[4] = {0.0f, 0.0f, 0.0f, 0.0f};  // summed in the order of the path above
+#pragma unroll
+                for (int i = 0; i < 16; ++i) {
+                  float p[2];
+#pragma unroll
+                  for (int e = 0; e < 2; ++e) {
+                    const float c = __uint_as_float(cv[2 * i + e]);
+                    p[e] = c > 0.0f ? c * ex2_approx(fmaf(__uint_as_float(sv[2 * i + e]), sc, -m2)) : 0.0f;
+                    ls[2 * (i & 1) + e] += p[e];
+                  }
+                  pk[i] = pack_bf16x2(p[0], p[1]);
+                }
+                hsum = (ls[0] + ls[1]) + (ls[2] + ls[3]);
+              }
+              lsum += hsum;
             }
-            tmem_st16(base + kColC + 16u * hf, pr);  // over C of the half before, which has been read
+            tmem_st16(base + kColC + 16u * hf, pk);  // over C of this half or the one before, which have been read
           }
-          lsum = (ls[0] + ls[1]) + (ls[2] + ls[3]);
+          l += lsum;
         }
-        l += lsum;
+        if (pending) {  // the finished item's epilogue: its last product has run under this tile's exponentials
+          if (!epilogue(items - 1)) { ok = false; break; }
+          pending = false;
+        }
+        if (done) break;
         tmem_wait_st();
         tc_fence_before();
         __syncwarp();
         if (lane == 0) mbar_arrive(&sm.p_full[w]);
       }
-      if (!ok) break;
+      if (done) break;
       d_h = h;
       d_i0 = i0;
       d_c0 = c0;
       d_pos0 = pos0;
       d_end = end;
+      d_l = l;
+      d_m = m2;
       pending = true;
       ++items;
     }
   } else {
     regs_lower<kRegsRest>();
-  if (warp == kWarpLoad) {
-    // ------------------------------------------------------------ items, Q and the K/V tiles
-    if (lane == 0) {
-      tma_prefetch_desc(&tmap_q);
-      tma_prefetch_desc(&tmap_k);
-      tma_prefetch_desc(&tmap_v);
-    }
-    int n = 0, k = 0, loads[2] = {0, 0};  // key tiles, items and Q tiles per stream so far
+  if (warp == kWarpItems) {
+    // ------------------------------------------------------------ items, a few ahead of their use
+    int n = 0, k = 0;  // key tiles and items so far
     bool ok = true;
     // every other round backwards: the items' costs fall along the list, so each block's early ones weigh against its late ones
     for (int round = 0; ok; ++round) {
@@ -535,14 +524,14 @@ serve_tc_kernel(const __grid_constant__ CUtensorMap tmap_q, const __grid_constan
       it.end = sq.pos0 + sq.len;
       it.tp = (sq.pos0 >> 8) + slot - ((prm.sq.cu[si] >> 8) + mult * si);
       if (it.tp < 0 || sq.len == 0 || 256 * it.tp >= it.end) continue;
-      it.top = min(4 * it.tp + 3, (it.end - 1) >> 6);
+      const int highest = min(4 * it.tp + 3, (it.end - 1) >> 6);
       it.n0 = n;
-      int low = it.top;
+      it.bottom = highest;
 #pragma unroll
       for (int w = 0; w < 2; ++w) {
         const int i0 = 256 * it.tp + 128 * w;
         const bool rows = i0 < it.end && i0 + 128 > it.pos0;
-        it.first[w] = rows ? min(4 * it.tp + 2 * w + 1, it.top) : -1;
+        it.first[w] = rows ? min(4 * it.tp + 2 * w + 1, highest) : -1;
         it.low[w] = 0;
         if (rows) {
           int lo = prm.spans[(static_cast<size_t>(h) * T128 + (i0 >> 7)) * 2];
@@ -551,42 +540,60 @@ serve_tc_kernel(const __grid_constant__ CUtensorMap tmap_q, const __grid_constan
             lo = i0;
           }
           it.low[w] = lo >> 6;
-          low = min(low, it.low[w]);
+          it.bottom = min(it.bottom, it.low[w]);
         }
       }
-      const int top = max(it.first[0], it.first[1]);  // without rows above, the tiles above are not needed
-      it.top = top;
-      // the descriptor
-      const int slot_i = k % kItems;
-      if (k >= kItems && !wait_all(&sm.item_empty[slot_i], k / kItems + 1)) { ok = false; break; }
+      it.top = max(it.first[0], it.first[1]);  // without rows above, the tiles above are not needed
+      n += it.top - it.bottom + 1;
+      const int at = k % kItems;
+      if (k >= kItems && !wait_all(&sm.item_empty[at], k / kItems + 1)) { ok = false; break; }
       if (lane == 0) {
-        sm.item[slot_i] = it;
-        mbar_arrive(&sm.item_full[slot_i]);
+        sm.item[at] = it;
+        mbar_arrive(&sm.item_full[at]);
       }
       ++k;
       __syncwarp();
-      const int kvh = h / (H / prm.H_kv);
-      bool q_due[2] = {it.first[0] >= it.low[0], it.first[1] >= it.low[1]};
-      for (int u = top; u >= low; --u, ++n) {
-        // each stream's Q when its first key tile comes up (the upper tile's rows begin two key tiles earlier)
+    }
+    if (ok) {  // the end marker
+      const int at = k % kItems;
+      if (k < kItems || wait_all(&sm.item_empty[at], k / kItems + 1)) {
+        if (lane == 0) {
+          sm.item[at].valid = 0;
+          mbar_arrive(&sm.item_full[at]);
+        }
+      }
+    }
+  } else if (warp == kWarpLoad) {
+    // ------------------------------------------------------------ Q and the K/V tiles
+    if (lane == 0) {
+      tma_prefetch_desc(&tmap_q);
+      tma_prefetch_desc(&tmap_k);
+      tma_prefetch_desc(&tmap_v);
+      int n = 0, loads[2] = {0, 0};  // key tiles, and Q tiles per stream, so far
+      bool ok = true;
+      for (int k = 0; ok; ++k) {
+        if (!wait(&sm.item_full[k % kItems], k / kItems)) break;
+        const Item it = sm.item[k % kItems];
+        mbar_arrive(&sm.item_empty[k % kItems]);
+        if (!it.valid) break;
+        const int kvh = it.h / (H / prm.H_kv);
+        bool q_due[2] = {it.first[0] >= it.low[0], it.first[1] >= it.low[1]};
+        for (int u = it.top; ok && u >= it.bottom; --u, ++n) {
+          // each stream's Q when its first key tile comes up (the upper row tile's begin two key tiles earlier)
 #pragma unroll
-        for (int w = 1; w >= 0; --w) {
-          if (!q_due[w] || u > it.first[w]) continue;
-          q_due[w] = false;
-          if (loads[w] && !wait_all(&sm.q_empty[w], loads[w] + 1)) { ok = false; break; }
-          if (lane == 0) {
+          for (int w = 1; w >= 0; --w) {
+            if (!q_due[w] || u > it.first[w]) continue;
+            q_due[w] = false;
+            if (loads[w] && !wait(&sm.q_empty[w], loads[w] + 1)) { ok = false; break; }
             const int t = it.c0 + 256 * it.tp + 128 * w - it.pos0;
             mbar_arrive_expect_tx(&sm.q_full[w], Smem::kQBytes);
 #pragma unroll
             for (int c = 0; c < D / 64; ++c)
-              tma_load_3d(sm.q[w] + c * (kRows * 128), &tmap_q, 64 * c, prm.q_swap ? t : h, prm.q_swap ? h : t, &sm.q_full[w]);
+              tma_load_3d(sm.q[w] + c * (kRows * 128), &tmap_q, 64 * c, prm.q_swap ? t : it.h, prm.q_swap ? it.h : t, &sm.q_full[w]);
+            ++loads[w];
           }
-          ++loads[w];
-        }
-        if (!ok) break;
-        const int st = n % kStages;
-        if (n >= kStages && !wait_all(&sm.kv_empty[st], n / kStages + 1)) { ok = false; break; }
-        if (lane == 0) {
+          const int st = n % kStages;
+          if (!ok || (n >= kStages && !wait(&sm.kv_empty[st], n / kStages + 1))) { ok = false; break; }
           const int t = it.c0 + kKeys * u - it.pos0;
           mbar_arrive_expect_tx(&sm.kv_full[st], 2 * Smem::kKBytes);
 #pragma unroll
@@ -600,120 +607,121 @@ serve_tc_kernel(const __grid_constant__ CUtensorMap tmap_q, const __grid_constan
           for (int w = 0; w < 2; ++w)
             if (u > it.first[w] || u < it.low[w]) mbar_arrive(&sm.kv_empty[st]);
         }
-        __syncwarp();
       }
-    }
-    if (ok) {  // the end marker
-      const int slot_i = k % kItems;
-      if (k < kItems || wait_all(&sm.item_empty[slot_i], k / kItems + 1)) {
-        if (lane == 0) {
-          sm.item[slot_i].valid = 0;
-          mbar_arrive(&sm.item_full[slot_i]);
-        }
-      }
-    }
-    __syncwarp();
-    if (*abort_flag && lane == 0) {
-      // let every copy already issued land before the block can exit
-      for (int i = max(0, n - kStages); i < n; ++i) mbar_wait_drain(&sm.kv_full[i % kStages], (i / kStages) & 1, kDrainNs);
-      if (n > 0 || loads[0] || loads[1])
+      if (*abort_flag) {
+        // let every copy already issued land before the block can exit
+        for (int i = max(0, n - kStages); i < n; ++i) mbar_wait_drain(&sm.kv_full[i % kStages], (i / kStages) & 1, kDrainNs);
         for (int w = 0; w < 2; ++w)
           if (loads[w]) mbar_wait_drain(&sm.q_full[w], (loads[w] + 1) & 1, kDrainNs);
+      }
     }
   } else if (warp == kWarpMma || warp == kWarpMma + 1) {
     // ------------------------------------------------------------ one stream's MMAs
+    // The whole warp walks the tiles, one elected lane issues: descriptors and addresses then stay in uniform
+    // registers, where the instructions take them from.
     const int w = warp - kWarpMma;
-    if (lane == 0) {
-      constexpr uint32_t idesc_qk = idesc_bf16_f32(kRows, kKeys, 0);
-      constexpr uint32_t idesc_pv = idesc_bf16_f32(kRows, D, 1);
-      constexpr uint32_t idesc_c = idesc_e4m3_f32(kRows, kKeys);
-      const uint32_t base = tmem + kStreamCols * w;
-      const uint64_t q_desc = smem_desc_sw128(smem_u32(sm.q[w]), 16, 1024);
-      const uint64_t k_desc = smem_desc_sw128(smem_u32(sm.k[0]), 16, 1024);
-      const uint64_t v_desc = smem_desc_sw128(smem_u32(sm.v[0]), kKeys * 128, 1024);
-      const uint64_t a_desc = smem_desc_plain(smem_u32(sm.a[w][0]), kFeatGroup);
-      const uint64_t b_desc = smem_desc_plain(smem_u32(sm.b[w][0]), kFeatGroup);
-      int g = 0, items = 0;      // tiles and items of this stream so far
-      int pend = -1;             // stage of the tile whose PV is still to be issued
-      bool pend_first = false, pend_last = false;
-      auto issue_pv = [&]() {
-        tc_fence_after();
-        const uint64_t vd = v_desc + static_cast<uint64_t>((pend * Smem::kKBytes) >> 4);
+    const bool elected = elect_one();
+    constexpr uint32_t idesc_qk = idesc_bf16_f32(kRows, kKeys, 0);
+    constexpr uint32_t idesc_pv = idesc_bf16_f32(kRows, D, 1);
+    constexpr uint32_t idesc_c = idesc_e4m3_f32(kRows, kKeys);
+    const uint32_t base = tmem + kStreamCols * w;
+    const uint64_t q_desc = smem_desc_sw128(smem_u32(sm.q[w]), 16, 1024);
+    const uint64_t k_desc = smem_desc_sw128(smem_u32(sm.k[0]), 16, 1024);
+    const uint64_t v_desc = smem_desc_sw128(smem_u32(sm.v[0]), kKeys * 128, 1024);
+    const uint64_t a_desc = smem_desc_plain(smem_u32(sm.a[w][0]), kFeatGroup);
+    const uint64_t b_desc = smem_desc_plain(smem_u32(sm.b[w][0]), kFeatGroup);
+    int g = 0, items = 0;  // tiles and items of this stream so far
+    int pend = -1;         // stage of the tile whose PV is still to be issued
+    bool pend_first = false, pend_last = false;
+    auto flush = [&]() {
+      if (pend < 0) return true;
+      if (!wait_all(&sm.p_full[w], g - 1)) return false;
+      tc_fence_after();
+      const uint64_t vd = v_desc + static_cast<uint64_t>((pend * Smem::kKBytes) >> 4);
+      if (elected) {
 #pragma unroll
-        for (int kk = 0; kk < kKeys / 16; ++kk)
-          mma_ts(base + kColO, base + kColC + 8u * kk, vd + static_cast<uint64_t>((kk * 2048) >> 4), idesc_pv,
-                 (!pend_first || kk > 0) ? 1u : 0u);
+        for (uint32_t kk = 0; kk < kKeys / 16; ++kk)
+          mma_ts(base + kColO, base + kColC + 8u * kk, vd + 128u * kk, idesc_pv, (!pend_first || kk > 0) ? 1u : 0u);
         mma_commit(&sm.kv_empty[pend]);
         if (pend_last) mma_commit(&sm.o_full[w]);
-        pend = -1;
-      };
-      auto flush = [&]() {
-        if (pend < 0) return true;
-        if (!wait(&sm.p_full[w], g - 1)) return false;
-        issue_pv();
-        return true;
-      };
-      bool ok = !prm.withhold_mma;
-      for (int k = 0; ok; ++k) {
-        // the pending product first: the loads that come before the next item may need its tile's place
-        if (!flush()) break;
-        if (!wait(&sm.item_full[k % kItems], k / kItems)) break;
-        const Item& item = sm.item[k % kItems];
-        const int valid = item.valid, first = item.first[w], low = item.low[w], above = item.n0 + item.top, row_tile = 4 * item.tp + 2 * w;
-        mbar_arrive(&sm.item_empty[k % kItems]);
-        if (!valid) break;
-        for (int u = first; ok && u >= low; --u, ++g) {
-          const int n = above - u, st = n % kStages;
-          // P(g - 1) is there: S(g - 1) has been read too
-          const int fs = g & 1;
-          if (!flush() || !wait(&sm.kv_full[st], n / kStages) || !wait(&sm.feat_full[w][fs], g >> 1) ||
-              (u == first && !wait(&sm.q_full[w], items))) {
-            ok = false;
-            break;
-          }
-          tc_fence_after();
-          const uint64_t kd = k_desc + static_cast<uint64_t>((st * Smem::kKBytes) >> 4);
+      }
+      __syncwarp();
+      pend = -1;
+      return true;
+    };
+    bool ok = !prm.withhold_mma;
+    for (int k = 0; ok; ++k) {
+      // the pending product first: the loads that come before the next item may need its tile's place
+      if (!flush()) break;
+      if (!wait_all(&sm.item_full[k % kItems], k / kItems)) break;
+      const Item& item = sm.item[k % kItems];
+      const int valid = uniform(item.valid), first = uniform(item.first[w]), low = uniform(item.low[w]);
+      const int above = uniform(item.n0 + item.top), row_tile = uniform(4 * item.tp + 2 * w);
+      if (lane == 0) mbar_arrive(&sm.item_empty[k % kItems]);
+      if (!valid) break;
+      for (int u = first; u >= low; --u, ++g) {
+        const int n = above - u, st = n % kStages, fs = g & 1;
+        // P(g - 1) is there: S(g - 1) has been read too
+        if (!flush() || !wait_all(&sm.kv_full[st], n / kStages) || !wait_all(&sm.feat_full[w][fs], g >> 1) ||
+            (u == first && !wait_all(&sm.q_full[w], items))) {
+          ok = false;
+          break;
+        }
+        tc_fence_after();
+        const uint64_t kd = k_desc + static_cast<uint64_t>((st * Smem::kKBytes) >> 4);
+        // C(g), after PV(g - 1), whose P lies where C goes. The upper diagonal tile has none.
+        const int rel = u - row_tile;  // 1: keys 64..127 of the row tile, 0: keys 0..63, < 0: before it
+        const uint64_t ad = a_desc + static_cast<uint64_t>((rel == 0 ? 0 : kRows * kFeat) >> 4);
+        const uint64_t bd = b_desc + static_cast<uint64_t>((fs * (kKeys * kFeat)) >> 4);
+        if (elected) {
 #pragma unroll
-          for (int kk = 0; kk < D / 16; ++kk)
-            mma_ss(base + kColS, q_desc + static_cast<uint64_t>(((kk >> 2) * (kRows * 128) + (kk & 3) * 32) >> 4),
-                   kd + static_cast<uint64_t>(((kk >> 2) * (kKeys * 128) + (kk & 3) * 32) >> 4), idesc_qk, kk > 0 ? 1u : 0u);
+          for (uint32_t kk = 0; kk < D / 16; ++kk)
+            mma_ss(base + kColS, q_desc + (kk >> 2) * (kRows * 8) + (kk & 3) * 2, kd + (kk >> 2) * (kKeys * 8) + (kk & 3) * 2,
+                   idesc_qk, kk > 0 ? 1u : 0u);
           if (u == low) mma_commit(&sm.q_empty[w]);
-          // C(g), after PV(g - 1), whose P lies where C goes. The upper diagonal tile has none.
-          const int rel = u - row_tile;  // 1: keys 64..127 of the row tile, 0: keys 0..63, < 0: before it
           if (rel <= 0) {
-            const uint64_t ad = a_desc + static_cast<uint64_t>((rel == 0 ? 0 : kRows * kFeat) >> 4);
-            const uint64_t bd = b_desc + static_cast<uint64_t>((fs * (kKeys * kFeat)) >> 4);
 #pragma unroll
             for (int c = 0; c < kFeat / 32; ++c) mma_f8(base + kColC, ad + 16u * c, bd + 16u * c, idesc_c, c > 0 ? 1u : 0u);
           }
           mma_commit(&sm.feat_empty[w][fs]);
           mma_commit(&sm.c_full[w]);
-          pend = st;
-          pend_first = u == first;
-          pend_last = u == low;
         }
-        if (first >= low) ++items;
+        __syncwarp();
+        pend = st;
+        pend_first = u == first;
+        pend_last = u == low;
       }
-      if (ok) flush();
+      if (first >= low) ++items;
+    }
+    if (ok) flush();
+    if (elected) {
       mma_commit(&sm.drain[w]);  // every MMA issued so far completes before it arrives
       mbar_wait_drain(&sm.drain[w], 0, kDrainNs);
     }
+    __syncwarp();
   } else if (warp == kWarpMask || warp == kWarpMask + 1) {
     // ------------------------------------------------------------ one stream's count operands
     const int w = warp - kWarpMask;
-    int g = 0, items = 0;
+    int g = 0, items = 0, last_product = -1;
     bool ok = true;
     for (int k = 0; ok; ++k) {
       if (!wait_all(&sm.item_full[k % kItems], k / kItems)) break;
       const Item& item = sm.item[k % kItems];
       const int valid = item.valid, first = item.first[w], low = item.low[w], above = item.n0 + item.top, end = item.end;
       const int i0 = 256 * item.tp + 128 * w;
-      const MaskT* bm = bmask + static_cast<size_t>(item.h) * max_len;
+      const int h = item.h;
+      const MaskT* bm = bmask + static_cast<size_t>(h) * max_len;
       __syncwarp();
       if (lane == 0) mbar_arrive(&sm.item_empty[k % kItems]);
       if (!valid) break;
       if (first < low) continue;
       auto mask_at = [&](int p) { return p < max_len ? bm[p] : FULL; };
+      // the rows' near counts into the cache: the softmax comes for them later
+#pragma unroll
+      for (int q = 0; q < 2; ++q) {
+        const int p = i0 + 64 * q + 2 * lane;  // 128 bytes: two rows
+        if (p < end) asm volatile("prefetch.global.L2 [%0];" ::"l"(prm.near + (static_cast<size_t>(h) * max_len + p) * kKeys));
+      }
       MaskT rv[4];  // rows 32 q + lane
 #pragma unroll
       for (int q = 0; q < 4; ++q) rv[q] = mask_at(i0 + 32 * q + lane);
@@ -728,23 +736,18 @@ serve_tc_kernel(const __grid_constant__ CUtensorMap tmap_q, const __grid_constan
         in[q] = tiles::warp_prefix_or<MaskT>(rv[q], lane);
         tot[q] = __shfl_sync(0xffffffffu, in[q], 31);
       }
+      // published with the item's first tile; the item before last, which had this place, has been read once tile g - 2 has
+      if (g >= 2 && !wait_all(&sm.feat_empty[w][g & 1], (g >> 1) + 1)) { ok = false; break; }
       const int rb = items & 1;
-      if (items >= 2 && !wait_all(&sm.row_empty[w][rb], (items >> 1) + 1)) { ok = false; break; }
       MaskT before = 0;
 #pragma unroll
       for (int q = 0; q < 4; ++q) {
-        sm.bm[w][rb][32 * q + lane] = rv[q];
         sm.pre[w][rb][32 * q + lane] = static_cast<MaskT>(before | in[q]);
         before = static_cast<MaskT>(before | tot[q]);
       }
-      __syncwarp();
-      if (lane == 0) mbar_arrive(&sm.row_full[w][rb]);
-      // the last product of the previous item has read a
-      if (g >= 1 && !wait_all(&sm.feat_empty[w][(g - 1) & 1], (g - 1) >> 1)) { ok = false; break; }
-      put_bits<MaskT>(sm.a[w][0], 64 + lane, static_cast<MaskT>(FULL & ~in[2]));
-      put_bits<MaskT>(sm.a[w][0], 96 + lane, static_cast<MaskT>(FULL & ~(tot[2] | in[3])));
-#pragma unroll 1
-      for (int r = lane; r < kRows; r += 32) put_bits<MaskT>(sm.a[w][1], r, static_cast<MaskT>(FULL & ~sm.pre[w][rb][r]));
+      sm.mid[w][rb][lane] = in[2];
+      sm.mid[w][rb][32 + lane] = static_cast<MaskT>(tot[2] | in[3]);
+      bool built = false;
       MaskT gap = 0;
       for (int u = first; ok && u >= low; --u, ++g) {
         kv[0] = nx[0];
@@ -761,6 +764,14 @@ serve_tc_kernel(const __grid_constant__ CUtensorMap tmap_q, const __grid_constan
         MaskT a1 = __shfl_down_sync(0xffffffffu, s1, 1), a0 = __shfl_down_sync(0xffffffffu, s0, 1);
         if (lane == 31) a1 = a0 = 0;
         if (rel <= 0) {
+          if (!built) {  // the rows' operands: the product before this one, the previous item's last, has read them
+            built = true;
+            if (last_product >= 0 && !wait_all(&sm.feat_empty[w][last_product & 1], last_product >> 1)) { ok = false; break; }
+#pragma unroll 1
+            for (int r = lane; r < kRows; r += 32) put_bits<MaskT>(sm.a[w][1], r, static_cast<MaskT>(FULL & ~sm.pre[w][rb][r]));
+#pragma unroll 1
+            for (int r = lane; r < kRows / 2; r += 32) put_bits<MaskT>(sm.a[w][0], 64 + r, static_cast<MaskT>(FULL & ~sm.mid[w][rb][r]));
+          }
           put_bits<MaskT>(sm.b[w][fs], lane, static_cast<MaskT>(FULL & ~(a0 | t1 | gap)));
           put_bits<MaskT>(sm.b[w][fs], 32 + lane, static_cast<MaskT>(FULL & ~(a1 | gap)));
         }
@@ -785,6 +796,7 @@ serve_tc_kernel(const __grid_constant__ CUtensorMap tmap_q, const __grid_constan
         __syncwarp();
         if (lane == 0) mbar_arrive(&sm.feat_full[w][fs]);
       }
+      last_product = g - 1;
       ++items;
     }
   }
@@ -835,6 +847,7 @@ int launch(const ServeArgs& a, cudaStream_t st) {
   if (static_cast<long long>(prm.slots) * a.H > 0x7fffffffLL) return fail(PLSH_ERR_RANGE, "too many row tiles");
   prm.items = prm.slots * a.H;
   prm.spans = a.spans;
+  prm.near = a.near;
   prm.wait_ns = wait_limit_ns();
   prm.withhold_mma = withhold_mma() ? 1 : 0;
   auto kern = serve_tc_kernel<D, MaskT, kStages>;
@@ -850,6 +863,14 @@ int launch(const ServeArgs& a, cudaStream_t st) {
 }
 
 }  // namespace
+
+int launch_near(const void* bmask, int H, int s, int n, uint8_t* near, cudaStream_t st) {
+  const dim3 grid(ceil_div(n, 256), H);
+  if (s <= 32) near_kernel<uint32_t><<<grid, 256, 0, st>>>(static_cast<const uint32_t*>(bmask), s, n, near);
+  else near_kernel<unsigned long long><<<grid, 256, 0, st>>>(static_cast<const unsigned long long*>(bmask), s, n, near);
+  const cudaError_t e = cudaGetLastError();
+  return e == cudaSuccess ? PLSH_OK : cuda_fail(e, "near_kernel launch");
+}
 
 int launch_serve_tc(const ServeArgs& a, cudaStream_t st) {
   if (a.d == 128)

@@ -19,7 +19,7 @@ import numpy as np
 import torch
 
 from . import (PLSH_BF16, PLSH_F32, PLSH_MAX_S, PLSH_TILE, PlshError, decode_device_error, plsh_cache_append,
-               plsh_cache_read, plsh_draw_table_heads, plsh_packed_fwd, plsh_paged_fwd, plsh_window_from_table)
+               plsh_cache_read, plsh_draw_table_heads, plsh_near_counts, plsh_packed_fwd, plsh_paged_fwd, plsh_window_from_table)
 
 _CODES = {torch.bfloat16: PLSH_BF16, torch.float32: PLSH_F32}
 
@@ -192,6 +192,10 @@ class PlshServing(_Errors):
             self.spans = torch.empty((H, -(-max_len // PLSH_TILE), 2), dtype=torch.int32, device=self.device)
             self.bmask = torch.empty((H, max_len), dtype=torch.int32 if s <= 32 else torch.int64, device=self.device)
             plsh_window_from_table(self.table_dev, H, s, max_len, 1, self.bmax, self.spans, self.bmask, self.err)
+            self.near = None  # counts of each position's own 64-key tile: H * max_len * 64 bytes
+            if dtype == torch.bfloat16:
+                self.near = torch.empty((H, max_len, 64), dtype=torch.uint8, device=self.device)
+                plsh_near_counts(self.bmask, H, s, max_len, self.near)
             self.check()  # waits for the plan, so that any stream may use it from here on
 
     def _outputs(self, T: int, out, st) -> Tuple[torch.Tensor, torch.Tensor]:
@@ -222,7 +226,7 @@ class PlshServing(_Errors):
             O, row_sum = self._outputs(q.shape[0], out, st)
             if S and q.shape[0]:
                 plsh_packed_fwd(q, k, v, _CODES[self.dtype], cu_seqlens, self.H, self.H_kv, self.d, self.s, self.max_len,
-                                self.spans, self.bmask, O, row_sum, self.err, st)
+                                self.spans, self.bmask, self.near, O, row_sum, self.err, st)
         return O, row_sum
 
     def attend_paged(self, q: torch.Tensor, cache: PagedCache, page_table: torch.Tensor, cu_seqlens: torch.Tensor,

@@ -516,13 +516,23 @@ PLSH_API int plsh_attention_bwd_tc(const void* Q, const void* K, const void* V, 
  *   O[t][h]       = sum_{j <= i} c_ij e^{S_ij} V_j / sum_{j <= i} c_ij e^{S_ij},
  *   row_sum[t][h] = ln( sum_{j <= i} (c_ij / s) e^{S_ij} ),
  * j over the sequence's own positions.
+ *   near_dev [H][max_len][64] from plsh_near_counts; bf16 needs it, fp32 takes NULL.
  *   O        [T][H][d] out, row_sum [T][H] float32 out.
  */
 PLSH_API int plsh_packed_fwd(const void* Q, int64_t q_token, int64_t q_head, const void* K, int64_t k_token,
                              int64_t k_head, const void* V, int64_t v_token, int64_t v_head, int dtype, int T, int S,
                              const int32_t* cu_dev, int H, int H_kv, int d, int s, int max_len,
-                             const int32_t* tile_span_dev, const void* bmask_dev, void* O, float* row_sum,
-                             uint32_t* err_dev, void* stream);
+                             const int32_t* tile_span_dev, const void* bmask_dev, const uint8_t* near_dev, void* O,
+                             float* row_sum, uint32_t* err_dev, void* stream);
+
+/*
+ * plsh_near_counts -- c_ij of every position i with the keys j <= i of its own
+ * 64-key tile (64 (i / 64) ..), one byte each, 0 for j > i: part of a serving plan, built once from the
+ * boundary masks.
+ *   bmask_dev  [H][n] from plsh_window (or plsh_window_from_table).
+ *   near_dev   [H][n][64] uint8 out, 16-byte aligned.
+ */
+PLSH_API int plsh_near_counts(const void* bmask_dev, int H, int s, int n, uint8_t* near_dev, void* stream);
 
 /*
  * plsh_cache_append -- new tokens' K and V rows into their pages.

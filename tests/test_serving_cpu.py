@@ -19,8 +19,8 @@ def plsh():
     return m
 
 
-def _packed(Q=FAKE, qt=512, qh=128, kt=256, dtype=0, T=10, S=2, cu=FAKE, H=4, H_kv=2, d=128, s=20, max_len=100, spans=FAKE, O=FAKE):
-    return (Q, qt, qh, FAKE, kt, 128, FAKE, 256, 128, dtype, T, S, cu, H, H_kv, d, s, max_len, spans, FAKE, O, FAKE, FAKE, NULL)
+def _packed(Q=FAKE, qt=512, qh=128, kt=256, dtype=0, T=10, S=2, cu=FAKE, H=4, H_kv=2, d=128, s=20, max_len=100, spans=FAKE, near=FAKE, O=FAKE):
+    return (Q, qt, qh, FAKE, kt, 128, FAKE, 256, 128, dtype, T, S, cu, H, H_kv, d, s, max_len, spans, FAKE, near, O, FAKE, FAKE, NULL)
 
 
 def _append(K=FAKE, dtype=0, T=10, S=2, start=FAKE, d=128, kp=FAKE, ke=FAKE, ve=FAKE, width=3, pages=8, page=64):
@@ -39,9 +39,11 @@ def _paged(Q=FAKE, qt=512, dtype=0, T=10, S=2, start=FAKE, max_new=10, H=4, H_kv
 
 ODD = ctypes.c_void_p((1 << 20) + 8)
 REFUSED = [
+    ("plsh_near_counts", lambda H=2, s=8, n=10, near=FAKE: (FAKE, H, s, n, near, NULL),
+     [(dict(H=0), 1), (dict(s=65), 1), (dict(n=0), 1), (dict(near=NULL), 1), (dict(near=ODD), 1)]),
     ("plsh_packed_fwd", _packed, [(dict(Q=NULL), 1), (dict(Q=ODD), 1), (dict(qt=508), 1), (dict(qh=64), 1), (dict(kt=64), 1), (dict(dtype=7), 2),
                                   (dict(T=0), 1), (dict(S=0), 1), (dict(cu=NULL), 1), (dict(H_kv=3), 1), (dict(H=0), 1), (dict(d=96), 2),
-                                  (dict(s=0), 1), (dict(s=65), 1), (dict(max_len=0), 1), (dict(spans=NULL), 1), (dict(O=ODD), 1),
+                                  (dict(s=0), 1), (dict(s=65), 1), (dict(max_len=0), 1), (dict(spans=NULL), 1), (dict(near=NULL), 1), (dict(near=ODD), 1), (dict(O=ODD), 1),
                                   (dict(T=1 << 30, qt=1 << 20), 3), (dict(S=1 << 21), 3)]),
     ("plsh_cache_append", _append, [(dict(K=NULL), 1), (dict(dtype=2), 2), (dict(T=0), 1), (dict(S=0), 1), (dict(start=NULL), 1), (dict(d=32), 2),
                                     (dict(kp=NULL), 1), (dict(ke=NULL), 1), (dict(ve=NULL), 1), (dict(width=0), 1), (dict(pages=0), 1),
