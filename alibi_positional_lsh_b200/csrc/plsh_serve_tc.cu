@@ -14,15 +14,13 @@
 // 64-key tile, where no key lies behind all rows, are read: they depend on the position and the head alone, and the plan
 // holds them as bytes (near_kernel).
 //
-// Work. One item is a pair of 128-row tiles (256 positions) of one head; the tiles' windows
-// overlap, so both read the same 64-key tiles of K and V from shared memory, from the diagonal down.
-// Each row tile is a stream of its own: a warpgroup of softmax threads (one row each), a warp that issues its MMAs
-// and a warp that writes its counts' operands; the streams run half a step apart, so that one's
-// products run under the other's exponentials. Persistent blocks walk the items, heads with the widest
-// windows first. Tensor Memory, per stream: S (64 columns), 4 c (64 columns, P over them as
-// bf16), O (D columns).
+// Work. One item is a 128-row tile of one head, against 64-key tiles of K and V from the diagonal down. Two blocks share
+// an SM, each with half of Tensor Memory, so that one's products run under the other's exponentials; persistent
+// blocks walk the items, heads with the widest windows first. Eight warps: four of softmax threads (one row each), one that
+// finds the items, one that loads Q, K and V by TMA, one that issues the MMAs and one that writes the counts' operands.
+// Tensor Memory: S (64 columns), 4 c (64 columns, P over them as bf16), O (D columns).
 //
-// Per tile g of a stream:
+// Per key tile g:
 //   MMA      O += P(g - 1) V,  S(g) = Q K^T,  C(g) = A B^T
 //   softmax  P = 4c 2^(S log2e/sqrt(d) - m);  l += sum P
 // The reference m starts at 0 and changes only where a row leaves the range it is good for: a tile's sum above 2^64,
@@ -48,49 +46,48 @@ using namespace sm100;
 using namespace serve;
 using tiles::regs_after_wait;
 
-constexpr int kThreads = 512;                 // 16 warps
-constexpr int kSoftmaxWarps = 8;              // warps 0-3 stream 0 (the lower row tile), 4-7 stream 1
-constexpr int kWarpLoad = 8, kWarpMma = 9, kWarpMask = 11, kWarpItems = 13;  // one MMA and one mask warp per stream
+constexpr int kThreads = 256;
+constexpr int kSoftmaxWarps = 4;
+constexpr int kWarpItems = 4, kWarpLoad = 5, kWarpMma = 6, kWarpMask = 7;
 constexpr int kRows = 128, kKeys = 64;
 constexpr int kItems = 4;                     // item descriptors in flight
-constexpr uint32_t kTmemCols = 512, kStreamCols = 256;
+constexpr uint32_t kTmemCols = 256;           // half of Tensor Memory: two blocks share an SM
 constexpr uint32_t kColS = 0, kColC = 64, kColO = 128;
 constexpr float kSumMax = 1.8446744e19f, kSumMin = 9.3132257e-10f;  // 2^64, 2^-30
 constexpr int kMaxSortedHeads = 256;
 constexpr uint64_t kDrainNs = 100000000ull;
-// Registers per thread: 512 x 128 at launch; the two softmax warpgroups take 192, the other two keep 64.
+// Registers per thread: 256 x 128 at launch; the softmax warpgroup takes 192, the other one keeps 64.
 constexpr uint32_t kRegsSoftmax = 192, kRegsRest = 64;
 
-// Two row tiles of one head: positions 256 tp .. 256 tp + 255 of sequence s.
+// One row tile of one head: positions i0 .. i0 + 127 of sequence s, against key tiles top, top - 1, .., low.
 struct Item {
-  int valid, h, tp, c0, pos0, end, s;
-  int top, bottom;  // highest and lowest key tile
-  int low[2];    // lowest key tile of each stream
-  int first[2];  // highest key tile of each stream; first < low: the stream has no rows here
-  int n0;        // number of the first key tile in the block's sequence of loads
+  int valid, h, i0, c0, pos0, end, s, top, low;
 };
 
-template <int D, typename MaskT, int kStages>
+template <int D, typename MaskT>
 struct __align__(1024) TcSmem {
   static constexpr int kQBytes = kRows * D * 2, kKBytes = kKeys * D * 2;
+  static constexpr int kStages = D == 128 ? 2 : 4;
+  static constexpr int kVStages = D == 128 && sizeof(MaskT) == 8 ? 1 : kStages;  // 64 hashes' operands leave room for one
   static constexpr int kFeat = sizeof(MaskT) * 8;  // bytes of a row of a or b: one per hash
-  uint8_t q[2][kQBytes];
+  uint8_t q[kQBytes];
   uint8_t k[kStages][kKBytes];
-  uint8_t v[kStages][kKBytes];
-  uint8_t a[2][2][kRows * kFeat];   // [stream][0: pivot inside the row tile (rows 64..127), 1: pivot before it]
-  uint8_t b[2][2][kKeys * kFeat];   // [stream][stage]
-  MaskT pre[2][2][kRows];           // [stream][item parity]: OR of the boundary masks from the row tile's first row to the row
-  MaskT mid[2][2][kRows / 2];       // for rows 64..127: OR from row 64 to the row
-  MaskT gap[2][2], upper[2][2];     // [stream][stage]: OR between the key tile and the row tile; OR of the key tile's keys 32..63
+  uint8_t v[kVStages][kKBytes];
+  // rows of a: 128 with the pivot before the row tile, then rows 64..127 with the pivot inside it (their operand
+  // starts 64 rows earlier: the counts of its first 64 rows are not used)
+  uint8_t a[(kRows + kRows / 2) * kFeat];
+  uint8_t b[2][kKeys * kFeat];
+  MaskT pre[2][kRows];      // [item parity]: OR of the boundary masks from the row tile's first row to the row
+  MaskT mid[2][kRows / 2];  // for rows 64..127: OR from row 64 to the row
+  MaskT gap[2], upper[2];   // [stage]: OR between the key tile and the row tile; OR of the key tile's keys 32..63
   Item item[kItems];
   int16_t order[kMaxSortedHeads];
   int32_t width[kMaxSortedHeads];
   uint64_t item_full[kItems], item_empty[kItems];
-  uint64_t q_full[2], q_empty[2];
-  uint64_t kv_full[kStages], kv_empty[kStages];
-  uint64_t feat_full[2][2], feat_empty[2][2];
-  uint64_t c_full[2], p_full[2], o_full[2];
-  uint64_t drain[2];
+  uint64_t q_full, q_empty;
+  uint64_t k_full[kStages], k_empty[kStages], v_full[kVStages], v_empty[kVStages];
+  uint64_t feat_full[2], feat_empty[2];
+  uint64_t c_full, p_full, o_full, drain;
   uint32_t tmem_base;
   int abort_flag;
 };
@@ -139,6 +136,13 @@ __device__ __forceinline__ bool elect_one() {
 
 // A value that all lanes hold alike, known as such to the compiler.
 __device__ __forceinline__ int uniform(int x) { return __shfl_sync(0xffffffffu, x, 0); }
+
+// 32 bytes of a row in one store.
+__device__ __forceinline__ void store32(void* p, const uint32_t* w) {
+  asm volatile("st.global.v8.b32 [%0], {%1, %2, %3, %4, %5, %6, %7, %8};" ::"l"(p), "r"(w[0]), "r"(w[1]), "r"(w[2]), "r"(w[3]),
+               "r"(w[4]), "r"(w[5]), "r"(w[6]), "r"(w[7])
+               : "memory");
+}
 
 // Row r of a 0/1 operand: byte k is 0x40 (e4m3 2.0) where bit k is set. Four bits spread to four bytes by one multiply.
 __device__ __forceinline__ uint32_t spread4(uint32_t bits) { return ((bits & 0xFu) * (0x00204081u << 6)) & 0x40404040u; }
@@ -196,13 +200,14 @@ __global__ void __launch_bounds__(256) near_kernel(const MaskT* __restrict__ bma
 
 // ---- the kernel
 
-template <int D, typename MaskT, int kStages>
-__global__ void __launch_bounds__(kThreads, 1)
+template <int D, typename MaskT>
+__global__ void __launch_bounds__(kThreads, 2)
 serve_tc_kernel(const __grid_constant__ CUtensorMap tmap_q, const __grid_constant__ CUtensorMap tmap_k,
                 const __grid_constant__ CUtensorMap tmap_v, const __grid_constant__ TcParams prm,
                 const MaskT* __restrict__ bmask, __nv_bfloat16* __restrict__ O, float* __restrict__ row_sum,
                 uint32_t* __restrict__ err) {
-  using Smem = TcSmem<D, MaskT, kStages>;
+  using Smem = TcSmem<D, MaskT>;
+  constexpr int kStages = Smem::kStages, kVStages = Smem::kVStages;
   extern __shared__ __align__(1024) uint8_t smem_raw[];
   const uint32_t smem_pad = (1024u - (smem_u32(smem_raw) & 1023u)) & 1023u;
   auto& sm = *reinterpret_cast<Smem*>(smem_raw + smem_pad);
@@ -237,24 +242,26 @@ serve_tc_kernel(const __grid_constant__ CUtensorMap tmap_q, const __grid_constan
     sm.abort_flag = 0;
     for (int i = 0; i < kItems; ++i) {
       mbar_init(&sm.item_full[i], 1);
-      mbar_init(&sm.item_empty[i], kSoftmaxWarps + 5);
+      mbar_init(&sm.item_empty[i], kSoftmaxWarps + 3);
     }
     for (int i = 0; i < kStages; ++i) {
-      mbar_init(&sm.kv_full[i], 1);
-      mbar_init(&sm.kv_empty[i], 2);
+      mbar_init(&sm.k_full[i], 1);
+      mbar_init(&sm.k_empty[i], 1);
     }
-    for (int w = 0; w < 2; ++w) {
-      mbar_init(&sm.q_full[w], 1);
-      mbar_init(&sm.q_empty[w], 1);
-      for (int i = 0; i < 2; ++i) {
-        mbar_init(&sm.feat_full[w][i], 1);
-        mbar_init(&sm.feat_empty[w][i], 5);
-      }
-      mbar_init(&sm.c_full[w], 1);
-      mbar_init(&sm.p_full[w], 4);
-      mbar_init(&sm.o_full[w], 1);
-      mbar_init(&sm.drain[w], 1);
+    for (int i = 0; i < kVStages; ++i) {
+      mbar_init(&sm.v_full[i], 1);
+      mbar_init(&sm.v_empty[i], 1);
     }
+    for (int i = 0; i < 2; ++i) {
+      mbar_init(&sm.feat_full[i], 1);
+      mbar_init(&sm.feat_empty[i], kSoftmaxWarps + 1);
+    }
+    mbar_init(&sm.q_full, 1);
+    mbar_init(&sm.q_empty, 1);
+    mbar_init(&sm.c_full, 1);
+    mbar_init(&sm.p_full, kSoftmaxWarps);
+    mbar_init(&sm.o_full, 1);
+    mbar_init(&sm.drain, 1);
     fence_mbarrier_init();
   }
   if (warp == kWarpMma) {
@@ -272,62 +279,39 @@ serve_tc_kernel(const __grid_constant__ CUtensorMap tmap_q, const __grid_constan
   if (warp < kSoftmaxWarps) {
     regs_raise<kRegsSoftmax>();
     // ------------------------------------------------------------ softmax: one row per thread
-    const int w = warp >> 2, rg = warp & 3;
-    const int r = 32 * rg + lane;
-    const uint32_t base = tmem + kStreamCols * w + (static_cast<uint32_t>(32 * rg) << 16);
+    const int rg = warp, r = threadIdx.x;
+    const uint32_t base = tmem + (static_cast<uint32_t>(32 * rg) << 16);
     const float sc = 1.4426950408889634f / sqrtf(static_cast<float>(D));
     int g = 0, items = 0;
     int d_h = 0, d_i0 = 0, d_c0 = 0, d_pos0 = 0, d_end = 0;  // the finished item, until its epilogue
     float d_l = 1.0f, d_m = 0.0f;
     bool pending = false;
-    // O / l of the item just finished, once its last product has completed
+    // O / l of the item just finished, once its last product has completed: 32 bytes of the thread's own row at a time
     auto epilogue = [&](int number) -> bool {
-      if (!wait_all(&sm.o_full[w], number)) return false;
+      if (!wait_all(&sm.o_full, number)) return false;
       tc_fence_after();
       const float inv = 1.0f / d_l;
-      const int p4 = lane & 3;
+      const int p = d_i0 + r;
+      const bool row = p >= d_pos0 && p < d_end;
+      const size_t at = static_cast<size_t>(row ? d_c0 + p - d_pos0 : 0) * H + d_h;
+      __nv_bfloat16* out = O + at * D;
 #pragma unroll 1
-      for (int blk = 0; blk < D / 32; ++blk) {
+      for (int c = 0; c < D; c += 32) {
         uint32_t raw[32];
-        tmem_ld32(base + kColO + 32u * blk, raw);
+        tmem_ld32(base + kColO + c, raw);
         tmem_wait_ld();
         regs_after_wait(raw);
-        uint32_t a[4][4];  // [16-byte chunk][word] of this row's 32 columns
+        uint32_t o[16];
 #pragma unroll
-        for (int c = 0; c < 4; ++c)
-#pragma unroll
-          for (int e = 0; e < 4; ++e)
-            a[c][e] = pack_bf16x2(__uint_as_float(raw[8 * c + 2 * e]) * inv, __uint_as_float(raw[8 * c + 2 * e + 1]) * inv);
-        // 4x4 transpose of 16-byte chunks inside each quad of lanes: lane p then holds chunk p of the quad's four rows
-#pragma unroll
-        for (int msk = 2; msk >= 1; msk >>= 1) {
-          const bool lo_lane = (p4 & msk) == 0;
-#pragma unroll
-          for (int c = 0; c < 4; ++c) {
-            if (c & msk) continue;
-#pragma unroll
-            for (int e = 0; e < 4; ++e) {
-              const uint32_t send = lo_lane ? a[c | msk][e] : a[c][e];
-              const uint32_t recv = __shfl_xor_sync(0xffffffffu, send, msk);
-              if (lo_lane) a[c | msk][e] = recv;
-              else a[c][e] = recv;
-            }
-          }
-        }
-#pragma unroll
-        for (int e = 0; e < 4; ++e) {
-          const int p = d_i0 + (r & ~3) + e;
-          if (p >= d_pos0 && p < d_end) {
-            const size_t t = static_cast<size_t>(d_c0 + p - d_pos0);
-            *reinterpret_cast<uint4*>(O + (t * H + d_h) * D + 32 * blk + 8 * p4) = make_uint4(a[e][0], a[e][1], a[e][2], a[e][3]);
-          }
+        for (int i = 0; i < 16; ++i)
+          o[i] = pack_bf16x2(__uint_as_float(raw[2 * i]) * inv, __uint_as_float(raw[2 * i + 1]) * inv);
+        if (row) {
+          store32(out + c, o);
+          store32(out + c + 16, o + 8);
         }
       }
       tc_fence_before();
-      const int p = d_i0 + r;
-      if (p >= d_pos0 && p < d_end)
-        row_sum[static_cast<size_t>(d_c0 + p - d_pos0) * H + d_h] =
-            (log2f(d_l) + d_m - 2.0f) * 0.6931471805599453f - logf(static_cast<float>(s));
+      if (row) row_sum[at] = (log2f(d_l) + d_m - 2.0f) * 0.6931471805599453f - logf(static_cast<float>(s));
       return true;
     };
     bool ok = true;
@@ -335,29 +319,21 @@ serve_tc_kernel(const __grid_constant__ CUtensorMap tmap_q, const __grid_constan
       if (!wait_all(&sm.item_full[k % kItems], k / kItems)) break;
       const Item& item = sm.item[k % kItems];
       const bool done = !item.valid;
-      const int first = item.first[w], low = item.low[w], h = item.h, i0 = 256 * item.tp + 128 * w;
-      const int c0 = item.c0, pos0 = item.pos0, end = item.end;
+      const int first = item.top, low = item.low, h = item.h, i0 = item.i0, c0 = item.c0, pos0 = item.pos0, end = item.end;
       __syncwarp();
       if (lane == 0) mbar_arrive(&sm.item_empty[k % kItems]);
-      if (!done && first < low) continue;
       const bool mine = !done && i0 + r >= pos0 && i0 + r < end;  // the row holds a token
-      uint4 near[4];  // c of the 64 keys of the row's own key tile, one byte each
-#pragma unroll
-      for (int i = 0; i < 4; ++i) near[i] = make_uint4(0, 0, 0, 0);
-      if (mine) {
-        const uint4* src = reinterpret_cast<const uint4*>(prm.near + (static_cast<size_t>(h) * max_len + i0 + r) * kKeys);
-#pragma unroll
-        for (int i = 0; i < 4; ++i) near[i] = __ldg(src + i);
-      }
+      // c of the 64 keys of the row's own key tile, one byte each
+      const uint4* near = reinterpret_cast<const uint4*>(prm.near + (static_cast<size_t>(h) * max_len + (mine ? i0 + r : 0)) * kKeys);
       float m2 = 0.0f, l = 0.0f;
       MaskT pre = 0, mid = 0;
       for (int u = first; ok && (done || u >= low); --u, ++g) {
         if (!done) {
           const int fs = g & 1, rel = u - (i0 >> 6);
-          if (!wait_all(&sm.feat_full[w][fs], g >> 1)) { ok = false; break; }
+          if (!wait_all(&sm.feat_full[fs], g >> 1)) { ok = false; break; }
           if (u == first) {
-            pre = sm.pre[w][items & 1][r];
-            if (rg >= 2) mid = sm.mid[w][items & 1][r - 64];
+            pre = sm.pre[items & 1][r];
+            if (rg >= 2) mid = sm.mid[items & 1][r - 64];
           }
           // which 32-key halves hold weight for some row of the warp, and where the counts come from
           const bool own = rel == (rg >> 1);
@@ -365,13 +341,13 @@ serve_tc_kernel(const __grid_constant__ CUtensorMap tmap_q, const __grid_constan
           if (rel > 0 && rg < 2) {
             live0 = live1 = false;
           } else if (!own) {
-            const MaskT keep = static_cast<MaskT>(FULL & ~((rel == 0 ? mid : pre) | sm.gap[w][fs]));
+            const MaskT keep = static_cast<MaskT>(FULL & ~((rel == 0 ? mid : pre) | sm.gap[fs]));
             live1 = __any_sync(0xffffffffu, keep != 0);
-            live0 = __any_sync(0xffffffffu, static_cast<MaskT>(keep & ~sm.upper[w][fs]) != 0);
+            live0 = __any_sync(0xffffffffu, static_cast<MaskT>(keep & ~sm.upper[fs]) != 0);
           }
           __syncwarp();
-          if (lane == 0) mbar_arrive(&sm.feat_empty[w][fs]);
-          if (!wait_all(&sm.c_full[w], g)) { ok = false; break; }
+          if (lane == 0) mbar_arrive(&sm.feat_empty[fs]);
+          if (!wait_all(&sm.c_full, g)) { ok = false; break; }
           tc_fence_after();
           // P = 4c 2^(S sc - m) against the reference m, whatever S's maximum is: fp32 and bf16 hold P far beyond what the
           // softmax needs, so m has to be near the maximum only within some 2^60
@@ -385,10 +361,12 @@ serve_tc_kernel(const __grid_constant__ CUtensorMap tmap_q, const __grid_constan
               uint32_t sv[32], cv[32];
               tmem_ld32(base + kColS + 32u * hf, sv);
               if (own) {
+                uint4 n4[2];
+                n4[0] = __ldg(near + 2 * hf);
+                n4[1] = __ldg(near + 2 * hf + 1);
 #pragma unroll
                 for (int i = 0; i < 8; ++i) {
-                  const uint4 n4 = hf ? near[2 + (i >> 2)] : near[i >> 2];
-                  const uint32_t w4 = (i & 3) == 0 ? n4.x : (i & 3) == 1 ? n4.y : (i & 3) == 2 ? n4.z : n4.w;
+                  const uint32_t w4 = (i & 3) == 0 ? n4[i >> 2].x : (i & 3) == 1 ? n4[i >> 2].y : (i & 3) == 2 ? n4[i >> 2].z : n4[i >> 2].w;
                   // byte b as the float 2^23 + b, exactly; then 4 (f - 2^23)
 #pragma unroll
                   for (int e = 0; e < 4; ++e)
@@ -485,7 +463,7 @@ serve_tc_kernel(const __grid_constant__ CUtensorMap tmap_q, const __grid_constan
         tmem_wait_st();
         tc_fence_before();
         __syncwarp();
-        if (lane == 0) mbar_arrive(&sm.p_full[w]);
+        if (lane == 0) mbar_arrive(&sm.p_full);
       }
       if (done) break;
       d_h = h;
@@ -502,7 +480,7 @@ serve_tc_kernel(const __grid_constant__ CUtensorMap tmap_q, const __grid_constan
     regs_lower<kRegsRest>();
   if (warp == kWarpItems) {
     // ------------------------------------------------------------ items, a few ahead of their use
-    int n = 0, k = 0;  // key tiles and items so far
+    int k = 0;
     bool ok = true;
     // every other round backwards: the items' costs fall along the list, so each block's early ones weigh against its late ones
     for (int round = 0; ok; ++round) {
@@ -513,42 +491,20 @@ serve_tc_kernel(const __grid_constant__ CUtensorMap tmap_q, const __grid_constan
       const int hr = x / prm.slots, slot = x % prm.slots;
       const int h = H <= kMaxSortedHeads ? static_cast<int>(sm.order[hr]) : hr;
       const int mult = prm.sq.start ? 2 : 1;
-      const int si = warp_find(prm.sq.cu, prm.sq.S, 8, mult, slot);
+      const int si = warp_find(prm.sq.cu, prm.sq.S, 7, mult, slot);
       const Seq sq = load_seq(prm.sq, si);
-      Item it;
-      it.valid = 1;
-      it.h = h;
-      it.s = si;
-      it.c0 = sq.c0;
-      it.pos0 = sq.pos0;
-      it.end = sq.pos0 + sq.len;
-      it.tp = (sq.pos0 >> 8) + slot - ((prm.sq.cu[si] >> 8) + mult * si);
-      if (it.tp < 0 || sq.len == 0 || 256 * it.tp >= it.end) continue;
-      const int highest = min(4 * it.tp + 3, (it.end - 1) >> 6);
-      it.n0 = n;
-      it.bottom = highest;
-#pragma unroll
-      for (int w = 0; w < 2; ++w) {
-        const int i0 = 256 * it.tp + 128 * w;
-        const bool rows = i0 < it.end && i0 + 128 > it.pos0;
-        it.first[w] = rows ? min(4 * it.tp + 2 * w + 1, highest) : -1;
-        it.low[w] = 0;
-        if (rows) {
-          int lo = prm.spans[(static_cast<size_t>(h) * T128 + (i0 >> 7)) * 2];
-          if (lo < 0 || lo > i0) {
-            if (lane == 0) atomicOr(err, PLSH_DEVERR_WINDOW);
-            lo = i0;
-          }
-          it.low[w] = lo >> 6;
-          it.bottom = min(it.bottom, it.low[w]);
-        }
+      const int tile = (sq.pos0 >> 7) + slot - ((prm.sq.cu[si] >> 7) + mult * si);
+      const int end = sq.pos0 + sq.len, i0 = kRows * tile;
+      if (tile < 0 || sq.len == 0 || i0 >= end) continue;
+      int lo = prm.spans[(static_cast<size_t>(h) * T128 + tile) * 2];
+      if (lo < 0 || lo > i0) {
+        if (lane == 0) atomicOr(err, PLSH_DEVERR_WINDOW);
+        lo = i0;
       }
-      it.top = max(it.first[0], it.first[1]);  // without rows above, the tiles above are not needed
-      n += it.top - it.bottom + 1;
       const int at = k % kItems;
       if (k >= kItems && !wait_all(&sm.item_empty[at], k / kItems + 1)) { ok = false; break; }
       if (lane == 0) {
-        sm.item[at] = it;
+        sm.item[at] = Item{1, h, i0, sq.c0, sq.pos0, end, si, min((i0 + kRows - 1) >> 6, (end - 1) >> 6), lo >> 6};
         mbar_arrive(&sm.item_full[at]);
       }
       ++k;
@@ -569,101 +525,89 @@ serve_tc_kernel(const __grid_constant__ CUtensorMap tmap_q, const __grid_constan
       tma_prefetch_desc(&tmap_q);
       tma_prefetch_desc(&tmap_k);
       tma_prefetch_desc(&tmap_v);
-      int n = 0, loads[2] = {0, 0};  // key tiles, and Q tiles per stream, so far
+      int n = 0, nv = 0, loads = 0;  // K, V and Q tiles so far
       bool ok = true;
       for (int k = 0; ok; ++k) {
         if (!wait(&sm.item_full[k % kItems], k / kItems)) break;
         const Item it = sm.item[k % kItems];
         mbar_arrive(&sm.item_empty[k % kItems]);
         if (!it.valid) break;
-        const int kvh = it.h / (H / prm.H_kv);
-        bool q_due[2] = {it.first[0] >= it.low[0], it.first[1] >= it.low[1]};
-        for (int u = it.top; ok && u >= it.bottom; --u, ++n) {
-          // each stream's Q when its first key tile comes up (the upper row tile's begin two key tiles earlier)
+        const int kvh = it.h / (H / prm.H_kv), row0 = it.c0 - it.pos0;
+        for (int u = it.top; u >= it.low; --u, ++n) {
+          const int st = n % kStages, t = row0 + kKeys * u;
+          if (n >= kStages && !wait(&sm.k_empty[st], n / kStages + 1)) { ok = false; break; }
+          mbar_arrive_expect_tx(&sm.k_full[st], Smem::kKBytes);
 #pragma unroll
-          for (int w = 1; w >= 0; --w) {
-            if (!q_due[w] || u > it.first[w]) continue;
-            q_due[w] = false;
-            if (loads[w] && !wait(&sm.q_empty[w], loads[w] + 1)) { ok = false; break; }
-            const int t = it.c0 + 256 * it.tp + 128 * w - it.pos0;
-            mbar_arrive_expect_tx(&sm.q_full[w], Smem::kQBytes);
+          for (int c = 0; c < D / 64; ++c)
+            tma_load_3d(sm.k[st] + c * (kKeys * 128), &tmap_k, 64 * c, prm.k_swap ? t : kvh, prm.k_swap ? kvh : t, &sm.k_full[st]);
+          if (u == it.top) {
+            if (loads && !wait(&sm.q_empty, loads + 1)) { ok = false; ++n; break; }
+            const int tq = row0 + it.i0;
+            mbar_arrive_expect_tx(&sm.q_full, Smem::kQBytes);
 #pragma unroll
             for (int c = 0; c < D / 64; ++c)
-              tma_load_3d(sm.q[w] + c * (kRows * 128), &tmap_q, 64 * c, prm.q_swap ? t : it.h, prm.q_swap ? it.h : t, &sm.q_full[w]);
-            ++loads[w];
+              tma_load_3d(sm.q + c * (kRows * 128), &tmap_q, 64 * c, prm.q_swap ? tq : it.h, prm.q_swap ? it.h : tq, &sm.q_full);
+            ++loads;
           }
-          const int st = n % kStages;
-          if (!ok || (n >= kStages && !wait(&sm.kv_empty[st], n / kStages + 1))) { ok = false; break; }
-          const int t = it.c0 + kKeys * u - it.pos0;
-          mbar_arrive_expect_tx(&sm.kv_full[st], 2 * Smem::kKBytes);
+          const int sv = n % kVStages;
+          if (n >= kVStages && !wait(&sm.v_empty[sv], n / kVStages + 1)) { ok = false; ++n; break; }
+          mbar_arrive_expect_tx(&sm.v_full[sv], Smem::kKBytes);
 #pragma unroll
           for (int c = 0; c < D / 64; ++c)
-            tma_load_3d(sm.k[st] + c * (kKeys * 128), &tmap_k, 64 * c, prm.k_swap ? t : kvh, prm.k_swap ? kvh : t, &sm.kv_full[st]);
-#pragma unroll
-          for (int c = 0; c < D / 64; ++c)
-            tma_load_3d(sm.v[st] + c * (kKeys * 128), &tmap_v, 64 * c, prm.v_swap ? t : kvh, prm.v_swap ? kvh : t, &sm.kv_full[st]);
-          // a stream that has no use for the tile has released it already
-#pragma unroll
-          for (int w = 0; w < 2; ++w)
-            if (u > it.first[w] || u < it.low[w]) mbar_arrive(&sm.kv_empty[st]);
+            tma_load_3d(sm.v[sv] + c * (kKeys * 128), &tmap_v, 64 * c, prm.v_swap ? t : kvh, prm.v_swap ? kvh : t, &sm.v_full[sv]);
+          nv = n + 1;
         }
       }
       if (*abort_flag) {
         // let every copy already issued land before the block can exit
-        for (int i = max(0, n - kStages); i < n; ++i) mbar_wait_drain(&sm.kv_full[i % kStages], (i / kStages) & 1, kDrainNs);
-        for (int w = 0; w < 2; ++w)
-          if (loads[w]) mbar_wait_drain(&sm.q_full[w], (loads[w] + 1) & 1, kDrainNs);
+        for (int i = max(0, n - kStages); i < n; ++i) mbar_wait_drain(&sm.k_full[i % kStages], (i / kStages) & 1, kDrainNs);
+        for (int i = max(0, nv - kVStages); i < nv; ++i) mbar_wait_drain(&sm.v_full[i % kVStages], (i / kVStages) & 1, kDrainNs);
+        if (loads) mbar_wait_drain(&sm.q_full, (loads + 1) & 1, kDrainNs);
       }
     }
-  } else if (warp == kWarpMma || warp == kWarpMma + 1) {
-    // ------------------------------------------------------------ one stream's MMAs
+  } else if (warp == kWarpMma) {
+    // ------------------------------------------------------------ MMAs
     // The whole warp walks the tiles, one elected lane issues: descriptors and addresses then stay in uniform
     // registers, where the instructions take them from.
-    const int w = warp - kWarpMma;
     const bool elected = elect_one();
     constexpr uint32_t idesc_qk = idesc_bf16_f32(kRows, kKeys, 0);
     constexpr uint32_t idesc_pv = idesc_bf16_f32(kRows, D, 1);
     constexpr uint32_t idesc_c = idesc_e4m3_f32(kRows, kKeys);
-    const uint32_t base = tmem + kStreamCols * w;
-    const uint64_t q_desc = smem_desc_sw128(smem_u32(sm.q[w]), 16, 1024);
+    const uint64_t q_desc = smem_desc_sw128(smem_u32(sm.q), 16, 1024);
     const uint64_t k_desc = smem_desc_sw128(smem_u32(sm.k[0]), 16, 1024);
     const uint64_t v_desc = smem_desc_sw128(smem_u32(sm.v[0]), kKeys * 128, 1024);
-    const uint64_t a_desc = smem_desc_plain(smem_u32(sm.a[w][0]), kFeatGroup);
-    const uint64_t b_desc = smem_desc_plain(smem_u32(sm.b[w][0]), kFeatGroup);
-    int g = 0, items = 0;  // tiles and items of this stream so far
-    int pend = -1;         // stage of the tile whose PV is still to be issued
+    const uint64_t a_desc = smem_desc_plain(smem_u32(sm.a), kFeatGroup);
+    const uint64_t b_desc = smem_desc_plain(smem_u32(sm.b[0]), kFeatGroup);
+    int n = 0, items = 0;   // tiles and items so far
     bool pend_first = false, pend_last = false;
+    // PV of the tile before
     auto flush = [&]() {
-      if (pend < 0) return true;
-      if (!wait_all(&sm.p_full[w], g - 1)) return false;
+      const int st = (n - 1) % kVStages;
+      if (!wait_all(&sm.p_full, n - 1) || !wait_all(&sm.v_full[st], (n - 1) / kVStages)) return false;
       tc_fence_after();
-      const uint64_t vd = v_desc + static_cast<uint64_t>((pend * Smem::kKBytes) >> 4);
+      const uint64_t vd = v_desc + static_cast<uint64_t>((st * Smem::kKBytes) >> 4);
       if (elected) {
 #pragma unroll
         for (uint32_t kk = 0; kk < kKeys / 16; ++kk)
-          mma_ts(base + kColO, base + kColC + 8u * kk, vd + 128u * kk, idesc_pv, (!pend_first || kk > 0) ? 1u : 0u);
-        mma_commit(&sm.kv_empty[pend]);
-        if (pend_last) mma_commit(&sm.o_full[w]);
+          mma_ts(tmem + kColO, tmem + kColC + 8u * kk, vd + 128u * kk, idesc_pv, (!pend_first || kk > 0) ? 1u : 0u);
+        mma_commit(&sm.v_empty[st]);
+        if (pend_last) mma_commit(&sm.o_full);
       }
       __syncwarp();
-      pend = -1;
       return true;
     };
     bool ok = !prm.withhold_mma;
     for (int k = 0; ok; ++k) {
-      // the pending product first: the loads that come before the next item may need its tile's place
-      if (!flush()) break;
-      if (!wait_all(&sm.item_full[k % kItems], k / kItems)) break;
+      if (!wait_all(&sm.item_full[k % kItems], k / kItems)) { ok = false; break; }
       const Item& item = sm.item[k % kItems];
-      const int valid = uniform(item.valid), first = uniform(item.first[w]), low = uniform(item.low[w]);
-      const int above = uniform(item.n0 + item.top), row_tile = uniform(4 * item.tp + 2 * w);
+      const int valid = uniform(item.valid), top = uniform(item.top), low = uniform(item.low), row_tile = uniform(item.i0 >> 6);
       if (lane == 0) mbar_arrive(&sm.item_empty[k % kItems]);
       if (!valid) break;
-      for (int u = first; u >= low; --u, ++g) {
-        const int n = above - u, st = n % kStages, fs = g & 1;
+      for (int u = top; u >= low; --u, ++n) {
+        const int st = n % kStages, fs = n & 1;
         // P(g - 1) is there: S(g - 1) has been read too
-        if (!flush() || !wait_all(&sm.kv_full[st], n / kStages) || !wait_all(&sm.feat_full[w][fs], g >> 1) ||
-            (u == first && !wait_all(&sm.q_full[w], items))) {
+        if ((n > 0 && !flush()) || !wait_all(&sm.k_full[st], n / kStages) || !wait_all(&sm.feat_full[fs], n >> 1) ||
+            (u == top && !wait_all(&sm.q_full, items))) {
           ok = false;
           break;
         }
@@ -671,56 +615,54 @@ serve_tc_kernel(const __grid_constant__ CUtensorMap tmap_q, const __grid_constan
         const uint64_t kd = k_desc + static_cast<uint64_t>((st * Smem::kKBytes) >> 4);
         // C(g), after PV(g - 1), whose P lies where C goes. The upper diagonal tile has none.
         const int rel = u - row_tile;  // 1: keys 64..127 of the row tile, 0: keys 0..63, < 0: before it
-        const uint64_t ad = a_desc + static_cast<uint64_t>((rel == 0 ? 0 : kRows * kFeat) >> 4);
+        const uint64_t ad = a_desc + static_cast<uint64_t>((rel == 0 ? kRows / 2 * kFeat : 0) >> 4);
         const uint64_t bd = b_desc + static_cast<uint64_t>((fs * (kKeys * kFeat)) >> 4);
         if (elected) {
 #pragma unroll
           for (uint32_t kk = 0; kk < D / 16; ++kk)
-            mma_ss(base + kColS, q_desc + (kk >> 2) * (kRows * 8) + (kk & 3) * 2, kd + (kk >> 2) * (kKeys * 8) + (kk & 3) * 2,
+            mma_ss(tmem + kColS, q_desc + (kk >> 2) * (kRows * 8) + (kk & 3) * 2, kd + (kk >> 2) * (kKeys * 8) + (kk & 3) * 2,
                    idesc_qk, kk > 0 ? 1u : 0u);
-          if (u == low) mma_commit(&sm.q_empty[w]);
+          mma_commit(&sm.k_empty[st]);
+          if (u == low) mma_commit(&sm.q_empty);
           if (rel <= 0) {
 #pragma unroll
-            for (int c = 0; c < kFeat / 32; ++c) mma_f8(base + kColC, ad + 16u * c, bd + 16u * c, idesc_c, c > 0 ? 1u : 0u);
+            for (int c = 0; c < kFeat / 32; ++c) mma_f8(tmem + kColC, ad + 16u * c, bd + 16u * c, idesc_c, c > 0 ? 1u : 0u);
           }
-          mma_commit(&sm.feat_empty[w][fs]);
-          mma_commit(&sm.c_full[w]);
+          mma_commit(&sm.feat_empty[fs]);
+          mma_commit(&sm.c_full);
         }
         __syncwarp();
-        pend = st;
-        pend_first = u == first;
+        pend_first = u == top;
         pend_last = u == low;
       }
-      if (first >= low) ++items;
+      ++items;
     }
-    if (ok) flush();
+    if (ok && n > 0) flush();
     if (elected) {
-      mma_commit(&sm.drain[w]);  // every MMA issued so far completes before it arrives
-      mbar_wait_drain(&sm.drain[w], 0, kDrainNs);
+      mma_commit(&sm.drain);  // every MMA issued so far completes before it arrives
+      mbar_wait_drain(&sm.drain, 0, kDrainNs);
     }
     __syncwarp();
-  } else if (warp == kWarpMask || warp == kWarpMask + 1) {
-    // ------------------------------------------------------------ one stream's count operands
-    const int w = warp - kWarpMask;
+  } else {
+    // ------------------------------------------------------------ the counts' operands
     int g = 0, items = 0, last_product = -1;
     bool ok = true;
     for (int k = 0; ok; ++k) {
       if (!wait_all(&sm.item_full[k % kItems], k / kItems)) break;
       const Item& item = sm.item[k % kItems];
-      const int valid = item.valid, first = item.first[w], low = item.low[w], above = item.n0 + item.top, end = item.end;
-      const int i0 = 256 * item.tp + 128 * w;
-      const int h = item.h;
+      const int valid = item.valid, first = item.top, low = item.low, end = item.end, i0 = item.i0, h = item.h;
       const MaskT* bm = bmask + static_cast<size_t>(h) * max_len;
       __syncwarp();
       if (lane == 0) mbar_arrive(&sm.item_empty[k % kItems]);
       if (!valid) break;
-      if (first < low) continue;
       auto mask_at = [&](int p) { return p < max_len ? bm[p] : FULL; };
-      // the rows' near counts into the cache: the softmax comes for them later
+      // the rows' near counts into this SM's cache: the softmax comes for them with the diagonal tiles
 #pragma unroll
       for (int q = 0; q < 2; ++q) {
         const int p = i0 + 64 * q + 2 * lane;  // 128 bytes: two rows
-        if (p < end) asm volatile("prefetch.global.L2 [%0];" ::"l"(prm.near + (static_cast<size_t>(h) * max_len + p) * kKeys));
+        uint32_t x;
+        if (p < end)
+          asm volatile("ld.global.ca.u32 %0, [%1];" : "=r"(x) : "l"(prm.near + (static_cast<size_t>(h) * max_len + p) * kKeys));
       }
       MaskT rv[4];  // rows 32 q + lane
 #pragma unroll
@@ -737,16 +679,16 @@ serve_tc_kernel(const __grid_constant__ CUtensorMap tmap_q, const __grid_constan
         tot[q] = __shfl_sync(0xffffffffu, in[q], 31);
       }
       // published with the item's first tile; the item before last, which had this place, has been read once tile g - 2 has
-      if (g >= 2 && !wait_all(&sm.feat_empty[w][g & 1], (g >> 1) + 1)) { ok = false; break; }
+      if (g >= 2 && !wait_all(&sm.feat_empty[g & 1], (g >> 1) + 1)) { ok = false; break; }
       const int rb = items & 1;
       MaskT before = 0;
 #pragma unroll
       for (int q = 0; q < 4; ++q) {
-        sm.pre[w][rb][32 * q + lane] = static_cast<MaskT>(before | in[q]);
+        sm.pre[rb][32 * q + lane] = static_cast<MaskT>(before | in[q]);
         before = static_cast<MaskT>(before | tot[q]);
       }
-      sm.mid[w][rb][lane] = in[2];
-      sm.mid[w][rb][32 + lane] = static_cast<MaskT>(tot[2] | in[3]);
+      sm.mid[rb][lane] = in[2];
+      sm.mid[rb][32 + lane] = static_cast<MaskT>(tot[2] | in[3]);
       bool built = false;
       MaskT gap = 0;
       for (int u = first; ok && u >= low; --u, ++g) {
@@ -757,7 +699,7 @@ serve_tc_kernel(const __grid_constant__ CUtensorMap tmap_q, const __grid_constan
           for (int q = 0; q < 2; ++q) nx[q] = mask_at(kKeys * (u - 1) + 32 * q + lane);
         }
         const int rel = u - (i0 >> 6), fs = g & 1;
-        if (g >= 2 && !wait_all(&sm.feat_empty[w][fs], (g >> 1) + 1)) { ok = false; break; }
+        if (g >= 2 && !wait_all(&sm.feat_empty[fs], (g >> 1) + 1)) { ok = false; break; }
         // keys: OR after the key, up to the tile's last
         const MaskT s1 = tiles::warp_suffix_or<MaskT>(kv[1], lane), s0 = tiles::warp_suffix_or<MaskT>(kv[0], lane);
         const MaskT t1 = __shfl_sync(0xffffffffu, s1, 0), t0 = __shfl_sync(0xffffffffu, s0, 0);
@@ -766,35 +708,35 @@ serve_tc_kernel(const __grid_constant__ CUtensorMap tmap_q, const __grid_constan
         if (rel <= 0) {
           if (!built) {  // the rows' operands: the product before this one, the previous item's last, has read them
             built = true;
-            if (last_product >= 0 && !wait_all(&sm.feat_empty[w][last_product & 1], last_product >> 1)) { ok = false; break; }
+            if (last_product >= 0 && !wait_all(&sm.feat_empty[last_product & 1], last_product >> 1)) { ok = false; break; }
 #pragma unroll 1
-            for (int r = lane; r < kRows; r += 32) put_bits<MaskT>(sm.a[w][1], r, static_cast<MaskT>(FULL & ~sm.pre[w][rb][r]));
+            for (int r = lane; r < kRows; r += 32) put_bits<MaskT>(sm.a, r, static_cast<MaskT>(FULL & ~sm.pre[rb][r]));
 #pragma unroll 1
-            for (int r = lane; r < kRows / 2; r += 32) put_bits<MaskT>(sm.a[w][0], 64 + r, static_cast<MaskT>(FULL & ~sm.mid[w][rb][r]));
+            for (int r = lane; r < kRows / 2; r += 32) put_bits<MaskT>(sm.a, kRows + r, static_cast<MaskT>(FULL & ~sm.mid[rb][r]));
           }
-          put_bits<MaskT>(sm.b[w][fs], lane, static_cast<MaskT>(FULL & ~(a0 | t1 | gap)));
-          put_bits<MaskT>(sm.b[w][fs], 32 + lane, static_cast<MaskT>(FULL & ~(a1 | gap)));
+          put_bits<MaskT>(sm.b[fs], lane, static_cast<MaskT>(FULL & ~(a0 | t1 | gap)));
+          put_bits<MaskT>(sm.b[fs], 32 + lane, static_cast<MaskT>(FULL & ~(a1 | gap)));
         }
         if (lane == 0) {
-          sm.gap[w][fs] = gap;
-          sm.upper[w][fs] = t1;
+          sm.gap[fs] = gap;
+          sm.upper[fs] = t1;
         }
         if (rel < 0) gap = static_cast<MaskT>(gap | t0 | t1);
         // rows past the end: another sequence's, or nothing at all
         if (kKeys * (u + 1) > end) {
-          const int n = above - u, st = n % kStages;
-          if (!wait_all(&sm.kv_full[st], n / kStages)) { ok = false; break; }
+          const int st = g % kStages, sv = g % kVStages;
+          if (!wait_all(&sm.k_full[st], g / kStages) || !wait_all(&sm.v_full[sv], g / kVStages)) { ok = false; break; }
           const int r0 = end - kKeys * u;
           for (int e = lane; e < (kKeys - r0) * (D / 8); e += 32) {
             const int r = r0 + e / (D / 8), c = e % (D / 8);
             const int at = (c >> 3) * (kKeys * 128) + r * 128 + (c & 7) * 16;
             *reinterpret_cast<uint4*>(sm.k[st] + at) = make_uint4(0, 0, 0, 0);
-            *reinterpret_cast<uint4*>(sm.v[st] + at) = make_uint4(0, 0, 0, 0);
+            *reinterpret_cast<uint4*>(sm.v[sv] + at) = make_uint4(0, 0, 0, 0);
           }
         }
         fence_proxy_async_smem();
         __syncwarp();
-        if (lane == 0) mbar_arrive(&sm.feat_full[w][fs]);
+        if (lane == 0) mbar_arrive(&sm.feat_full[fs]);
       }
       last_product = g - 1;
       ++items;
@@ -832,7 +774,7 @@ int make_rows_map(CUtensorMap* map, const void* p, RowStrides st, int T, int hea
   return PLSH_OK;
 }
 
-template <int D, typename MaskT, int kStages>
+template <int D, typename MaskT>
 int launch(const ServeArgs& a, cudaStream_t st) {
   CUtensorMap mq, mk, mv;
   TcParams prm{};
@@ -843,19 +785,19 @@ int launch(const ServeArgs& a, cudaStream_t st) {
   prm.H = a.H;
   prm.H_kv = a.H_kv;
   prm.s = a.s;
-  prm.slots = (a.sq.T >> 8) + (a.sq.start ? 2 : 1) * a.sq.S;
+  prm.slots = (a.sq.T >> 7) + (a.sq.start ? 2 : 1) * a.sq.S;
   if (static_cast<long long>(prm.slots) * a.H > 0x7fffffffLL) return fail(PLSH_ERR_RANGE, "too many row tiles");
   prm.items = prm.slots * a.H;
   prm.spans = a.spans;
   prm.near = a.near;
   prm.wait_ns = wait_limit_ns();
   prm.withhold_mma = withhold_mma() ? 1 : 0;
-  auto kern = serve_tc_kernel<D, MaskT, kStages>;
-  constexpr size_t smem = sizeof(TcSmem<D, MaskT, kStages>) + 1024;
-  static_assert(smem <= 232448, "shared memory budget");
+  auto kern = serve_tc_kernel<D, MaskT>;
+  constexpr size_t smem = sizeof(TcSmem<D, MaskT>) + 1024;
+  static_assert(smem <= 115712, "shared memory of two blocks on an SM");
   cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, static_cast<int>(smem));
   if (e != cudaSuccess) return cuda_fail(e, "cudaFuncSetAttribute(serve_tc_kernel)");
-  const int grid = prm.items < tiles::sm_count() ? prm.items : tiles::sm_count();
+  const int grid = prm.items < 2 * tiles::sm_count() ? prm.items : 2 * tiles::sm_count();
   kern<<<grid, kThreads, smem, st>>>(mq, mk, mv, prm, static_cast<const MaskT*>(a.bmask), static_cast<__nv_bfloat16*>(a.O),
                                      a.row_sum, a.err);
   e = cudaGetLastError();
@@ -874,8 +816,8 @@ int launch_near(const void* bmask, int H, int s, int n, uint8_t* near, cudaStrea
 
 int launch_serve_tc(const ServeArgs& a, cudaStream_t st) {
   if (a.d == 128)
-    return a.s <= 32 ? launch<128, uint32_t, 4>(a, st) : launch<128, unsigned long long, 3>(a, st);
-  return a.s <= 32 ? launch<64, uint32_t, 6>(a, st) : launch<64, unsigned long long, 6>(a, st);
+    return a.s <= 32 ? launch<128, uint32_t>(a, st) : launch<128, unsigned long long>(a, st);
+  return a.s <= 32 ? launch<64, uint32_t>(a, st) : launch<64, unsigned long long>(a, st);
 }
 
 }  // namespace plsh
