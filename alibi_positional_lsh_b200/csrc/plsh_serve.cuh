@@ -39,6 +39,7 @@ __device__ __forceinline__ Seq load_seq(const SeqArgs& a, int s) {
 // Sets PLSH_DEVERR_SEQUENCE if any sequence of the call is malformed (called by one block).
 __device__ __forceinline__ void check_seqs(const SeqArgs& a, uint32_t* err) {
   bool bad = false;
+#pragma unroll 1
   for (int s = threadIdx.x; s < a.S; s += blockDim.x) bad |= !load_seq(a, s).ok;
   if (bad) atomicOr(err, PLSH_DEVERR_SEQUENCE);
 }
@@ -50,6 +51,7 @@ __device__ __forceinline__ void check_seqs(const SeqArgs& a, uint32_t* err) {
 __device__ __forceinline__ int warp_find(const int32_t* cu, int S, int lg_tile, int k, int x) {
   const int lane = threadIdx.x & 31;
   int lo = 0, n = S;
+#pragma unroll 1
   while (n > 1) {
     const int step = (n + 31) / 32;
     const int i = lo + lane * step;

@@ -21,7 +21,7 @@
 // Tensor Memory: S (64 columns), 4 c (64 columns, P over them as bf16), O (D columns).
 //
 // Per key tile g:
-//   MMA      O += P(g - 1) V,  S(g) = Q K^T,  C(g) = A B^T
+//   MMA      S(g) = Q K^T once S(g - 1) has been read,  O += P(g - 1) V,  C(g) = A B^T
 //   softmax  P = 4c 2^(S log2e/sqrt(d) - m);  l += sum P
 // The reference m starts at 0 and changes only where a row leaves the range it is good for: a tile's sum above 2^64,
 // or a sum below 2^-30 in the tile of the row's own key (which has the largest weight). fp32 and bf16 hold such P with
@@ -32,6 +32,8 @@
 // products, so that nothing there, not even a NaN, meets a zero weight: a sequence's result has the same bits whatever it is packed with.
 //
 // Every barrier wait is bounded in time (PLSH_DEVERR_TIMEOUT), as in the fused kernel.
+#include <cmath>
+
 #include <cuda.h>
 #include <cudaTypedefs.h>
 
@@ -48,7 +50,7 @@ using tiles::regs_after_wait;
 
 constexpr int kThreads = 256;
 constexpr int kSoftmaxWarps = 4;
-constexpr int kWarpItems = 4, kWarpLoad = 5, kWarpMma = 6, kWarpMask = 7;
+constexpr int kWarpItems = 4, kWarpLoad = 5, kWarpMma = 6;  // and 7, the counts' operands
 constexpr int kRows = 128, kKeys = 64;
 constexpr int kItems = 4;                     // item descriptors in flight
 constexpr uint32_t kTmemCols = 256;           // half of Tensor Memory: two blocks share an SM
@@ -77,8 +79,8 @@ struct __align__(1024) TcSmem {
   // starts 64 rows earlier: the counts of its first 64 rows are not used)
   uint8_t a[(kRows + kRows / 2) * kFeat];
   uint8_t b[2][kKeys * kFeat];
-  MaskT pre[2][kRows];      // [item parity]: OR of the boundary masks from the row tile's first row to the row
-  MaskT mid[2][kRows / 2];  // for rows 64..127: OR from row 64 to the row
+  // [item parity]: OR of the boundary masks from the row tile's first row to the row, then for rows 64..127 from row 64 on
+  MaskT rows[2][kRows + kRows / 2];
   MaskT gap[2], upper[2];   // [stage]: OR between the key tile and the row tile; OR of the key tile's keys 32..63
   Item item[kItems];
   int16_t order[kMaxSortedHeads];
@@ -87,7 +89,7 @@ struct __align__(1024) TcSmem {
   uint64_t q_full, q_empty;
   uint64_t k_full[kStages], k_empty[kStages], v_full[kVStages], v_empty[kVStages];
   uint64_t feat_full[2], feat_empty[2];
-  uint64_t c_full, p_full, o_full, drain;
+  uint64_t s_free, c_full, p_full, o_full, drain;
   uint32_t tmem_base;
   int abort_flag;
 };
@@ -98,7 +100,8 @@ struct TcParams {
   int q_swap, k_swap, v_swap;  // tensor map's second coordinate is the token (head-major storage) instead of the head
   const int32_t* spans;
   const uint8_t* near;  // [H][max_len][64]: c of the keys of each position's own 64-key tile
-  uint64_t wait_ns;
+  uint32_t wait_limit;  // of every barrier wait, in steps of 2^20 ns
+  float log_s;
   int withhold_mma;
 };
 
@@ -159,18 +162,16 @@ __device__ __forceinline__ void put_bits(uint8_t* base, int r, MaskT bits) {
 }
 
 // mbar_wait (plsh_sm100.cuh) with the polling loop in place: a kernel that moves registers between its warpgroups cannot
-// call a function, whose own registers would be those of the launch.
-__device__ __forceinline__ bool wait_bounded(uint64_t* bar, uint32_t parity, volatile int* abort_flag, uint32_t* err,
-                                             uint64_t limit_ns) {
-  if (mbar_try_wait(bar, parity)) return true;
-  uint64_t t0 = 0;
-  for (uint32_t i = 1; !mbar_try_wait(bar, parity); ++i) {
-    if (i & 63u) continue;
-    if (*abort_flag) return false;
-    if (!t0) t0 = global_timer_ns();
-    if (global_timer_ns() - t0 > limit_ns) {
+// call a function, whose own registers would be those of the launch. It is kept short (the limit in steps of 2^20 ns, the error
+// word written once at the kernel's end): at some twenty places, its code decides whether the kernel's loops stay in
+// the instruction cache (with the longer form the kernel had 68 KB, and ran half as fast again).
+__device__ __forceinline__ bool wait_bounded(uint64_t* bar, uint32_t parity, volatile int* abort_flag, uint32_t limit) {
+  uint32_t until = 0;
+  while (!mbar_try_wait(bar, parity)) {
+    const uint32_t now = static_cast<uint32_t>(global_timer_ns() >> 20);
+    if (until == 0) until = now + limit;
+    if (*abort_flag || static_cast<int32_t>(now - until) > 0) {
       *abort_flag = 1;
-      atomicOr(err, PLSH_DEVERR_TIMEOUT);
       return false;
     }
   }
@@ -223,14 +224,17 @@ serve_tc_kernel(const __grid_constant__ CUtensorMap tmap_q, const __grid_constan
   if (blockIdx.x == 0) check_seqs(prm.sq, err);
   // heads by decreasing window width of the middle row tile
   if (H <= kMaxSortedHeads) {
+#pragma unroll 1
     for (int h = threadIdx.x; h < H; h += kThreads) {
       const int t = T128 / 2;
       sm.width[h] = min(max_len, t * PLSH_TILE + PLSH_TILE) - prm.spans[(static_cast<size_t>(h) * T128 + t) * 2];
     }
     __syncthreads();
+#pragma unroll 1
     for (int h = threadIdx.x; h < H; h += kThreads) {
       const int wh = sm.width[h];
       int rank = 0;
+#pragma unroll 1
       for (int o = 0; o < H; ++o) {
         const int wo = sm.width[o];
         rank += (wo > wh) || (wo == wh && o < h);
@@ -258,6 +262,7 @@ serve_tc_kernel(const __grid_constant__ CUtensorMap tmap_q, const __grid_constan
     }
     mbar_init(&sm.q_full, 1);
     mbar_init(&sm.q_empty, 1);
+    mbar_init(&sm.s_free, kSoftmaxWarps);
     mbar_init(&sm.c_full, 1);
     mbar_init(&sm.p_full, kSoftmaxWarps);
     mbar_init(&sm.o_full, 1);
@@ -272,7 +277,7 @@ serve_tc_kernel(const __grid_constant__ CUtensorMap tmap_q, const __grid_constan
   __syncthreads();
   tc_fence_after();
   const uint32_t tmem = uniform(sm.tmem_base);
-  auto wait = [&](uint64_t* bar, uint32_t parity) { return wait_bounded(bar, parity & 1u, abort_flag, err, prm.wait_ns); };
+  auto wait = [&](uint64_t* bar, uint32_t parity) { return wait_bounded(bar, parity & 1u, abort_flag, prm.wait_limit); };
   // the same by a whole warp: false in every lane if any gave up
   auto wait_all = [&](uint64_t* bar, uint32_t parity) { return __all_sync(0xffffffffu, wait(bar, parity)) != 0; };
 
@@ -311,7 +316,7 @@ serve_tc_kernel(const __grid_constant__ CUtensorMap tmap_q, const __grid_constan
         }
       }
       tc_fence_before();
-      if (row) row_sum[at] = (log2f(d_l) + d_m - 2.0f) * 0.6931471805599453f - logf(static_cast<float>(s));
+      if (row) row_sum[at] = (__log2f(d_l) + d_m - 2.0f) * 0.6931471805599453f - prm.log_s;
       return true;
     };
     bool ok = true;
@@ -332,11 +337,18 @@ serve_tc_kernel(const __grid_constant__ CUtensorMap tmap_q, const __grid_constan
           const int fs = g & 1, rel = u - (i0 >> 6);
           if (!wait_all(&sm.feat_full[fs], g >> 1)) { ok = false; break; }
           if (u == first) {
-            pre = sm.pre[items & 1][r];
-            if (rg >= 2) mid = sm.mid[items & 1][r - 64];
+            pre = sm.rows[items & 1][r];
+            if (rg >= 2) mid = sm.rows[items & 1][r + 64];
           }
           // which 32-key halves hold weight for some row of the warp, and where the counts come from
           const bool own = rel == (rg >> 1);
+          uint32_t nc[16];  // its counts
+          if (own) {
+#pragma unroll
+            for (int i = 0; i < 4; ++i)
+              asm volatile("ld.global.ca.v4.u32 {%0, %1, %2, %3}, [%4];"
+                           : "=r"(nc[4 * i]), "=r"(nc[4 * i + 1]), "=r"(nc[4 * i + 2]), "=r"(nc[4 * i + 3]) : "l"(near + i));
+          }
           bool live0 = true, live1 = (rg & 1) != 0;  // own tile: the half of the warp's block, and for odd blocks the half before it
           if (rel > 0 && rg < 2) {
             live0 = live1 = false;
@@ -352,6 +364,12 @@ serve_tc_kernel(const __grid_constant__ CUtensorMap tmap_q, const __grid_constan
           // P = 4c 2^(S sc - m) against the reference m, whatever S's maximum is: fp32 and bf16 hold P far beyond what the
           // softmax needs, so m has to be near the maximum only within some 2^60
           float lsum = 0.0f;
+          auto s_read = [&]() {
+            tc_fence_before();
+            __syncwarp();
+            if (lane == 0) mbar_arrive(&sm.s_free);
+          };
+          if (!live1 && !live0) s_read();
 #pragma unroll 1
           for (int hf = 0; hf < 2; ++hf) {
             uint32_t pk[16];
@@ -361,12 +379,9 @@ serve_tc_kernel(const __grid_constant__ CUtensorMap tmap_q, const __grid_constan
               uint32_t sv[32], cv[32];
               tmem_ld32(base + kColS + 32u * hf, sv);
               if (own) {
-                uint4 n4[2];
-                n4[0] = __ldg(near + 2 * hf);
-                n4[1] = __ldg(near + 2 * hf + 1);
 #pragma unroll
                 for (int i = 0; i < 8; ++i) {
-                  const uint32_t w4 = (i & 3) == 0 ? n4[i >> 2].x : (i & 3) == 1 ? n4[i >> 2].y : (i & 3) == 2 ? n4[i >> 2].z : n4[i >> 2].w;
+                  const uint32_t w4 = hf ? nc[8 + i] : nc[i];
                   // byte b as the float 2^23 + b, exactly; then 4 (f - 2^23)
 #pragma unroll
                   for (int e = 0; e < 4; ++e)
@@ -378,6 +393,7 @@ serve_tc_kernel(const __grid_constant__ CUtensorMap tmap_q, const __grid_constan
               tmem_wait_ld();
               regs_after_wait(sv);
               regs_after_wait(cv);
+              if (hf == (live1 ? 1 : 0)) s_read();  // the last half with weight
               float hsum;
               {
                 const uint64_t sc2 = f2_pack(sc, sc), negm2 = f2_pack(-m2, -m2);
@@ -537,14 +553,14 @@ serve_tc_kernel(const __grid_constant__ CUtensorMap tmap_q, const __grid_constan
           const int st = n % kStages, t = row0 + kKeys * u;
           if (n >= kStages && !wait(&sm.k_empty[st], n / kStages + 1)) { ok = false; break; }
           mbar_arrive_expect_tx(&sm.k_full[st], Smem::kKBytes);
-#pragma unroll
+#pragma unroll 1
           for (int c = 0; c < D / 64; ++c)
             tma_load_3d(sm.k[st] + c * (kKeys * 128), &tmap_k, 64 * c, prm.k_swap ? t : kvh, prm.k_swap ? kvh : t, &sm.k_full[st]);
           if (u == it.top) {
             if (loads && !wait(&sm.q_empty, loads + 1)) { ok = false; ++n; break; }
             const int tq = row0 + it.i0;
             mbar_arrive_expect_tx(&sm.q_full, Smem::kQBytes);
-#pragma unroll
+#pragma unroll 1
             for (int c = 0; c < D / 64; ++c)
               tma_load_3d(sm.q + c * (kRows * 128), &tmap_q, 64 * c, prm.q_swap ? tq : it.h, prm.q_swap ? it.h : tq, &sm.q_full);
             ++loads;
@@ -552,7 +568,7 @@ serve_tc_kernel(const __grid_constant__ CUtensorMap tmap_q, const __grid_constan
           const int sv = n % kVStages;
           if (n >= kVStages && !wait(&sm.v_empty[sv], n / kVStages + 1)) { ok = false; ++n; break; }
           mbar_arrive_expect_tx(&sm.v_full[sv], Smem::kKBytes);
-#pragma unroll
+#pragma unroll 1
           for (int c = 0; c < D / 64; ++c)
             tma_load_3d(sm.v[sv] + c * (kKeys * 128), &tmap_v, 64 * c, prm.v_swap ? t : kvh, prm.v_swap ? kvh : t, &sm.v_full[sv]);
           nv = n + 1;
@@ -578,52 +594,68 @@ serve_tc_kernel(const __grid_constant__ CUtensorMap tmap_q, const __grid_constan
     const uint64_t v_desc = smem_desc_sw128(smem_u32(sm.v[0]), kKeys * 128, 1024);
     const uint64_t a_desc = smem_desc_plain(smem_u32(sm.a), kFeatGroup);
     const uint64_t b_desc = smem_desc_plain(smem_u32(sm.b[0]), kFeatGroup);
+    constexpr bool kEarlyS = kVStages > 1;
     int n = 0, items = 0;   // tiles and items so far
     bool pend_first = false, pend_last = false;
-    // PV of the tile before
-    auto flush = [&]() {
-      const int st = (n - 1) % kVStages;
-      if (!wait_all(&sm.p_full, n - 1) || !wait_all(&sm.v_full[st], (n - 1) / kVStages)) return false;
-      tc_fence_after();
-      const uint64_t vd = v_desc + static_cast<uint64_t>((st * Smem::kKBytes) >> 4);
-      if (elected) {
-#pragma unroll
-        for (uint32_t kk = 0; kk < kKeys / 16; ++kk)
-          mma_ts(tmem + kColO, tmem + kColC + 8u * kk, vd + 128u * kk, idesc_pv, (!pend_first || kk > 0) ? 1u : 0u);
-        mma_commit(&sm.v_empty[st]);
-        if (pend_last) mma_commit(&sm.o_full);
-      }
-      __syncwarp();
-      return true;
-    };
     bool ok = !prm.withhold_mma;
     for (int k = 0; ok; ++k) {
       if (!wait_all(&sm.item_full[k % kItems], k / kItems)) { ok = false; break; }
       const Item& item = sm.item[k % kItems];
-      const int valid = uniform(item.valid), top = uniform(item.top), low = uniform(item.low), row_tile = uniform(item.i0 >> 6);
+      const bool done = uniform(item.valid) == 0;
+      const int top = uniform(item.top), low = uniform(item.low), row_tile = uniform(item.i0 >> 6);
       if (lane == 0) mbar_arrive(&sm.item_empty[k % kItems]);
-      if (!valid) break;
-      for (int u = top; u >= low; --u, ++n) {
-        const int st = n % kStages, fs = n & 1;
-        // P(g - 1) is there: S(g - 1) has been read too
-        if ((n > 0 && !flush()) || !wait_all(&sm.k_full[st], n / kStages) || !wait_all(&sm.feat_full[fs], n >> 1) ||
-            (u == top && !wait_all(&sm.q_full, items))) {
-          ok = false;
-          break;
+      for (int u = top; done || u >= low; --u, ++n) {
+        const int st = n % kStages, sv = (n - 1) % kVStages, fs = n & 1;
+        // S(g), as soon as its operands are there and S(g - 1) has been read; then PV(g - 1), when P(g - 1) is there; then C(g), which goes
+        // where P(g - 1) lies (the upper diagonal tile has none). Every wait but P's passes while the softmax works.
+        auto issue_s = [&]() {
+          tc_fence_after();
+          const uint64_t kd = k_desc + static_cast<uint64_t>((st * Smem::kKBytes) >> 4);
+          if (elected) {
+#pragma unroll
+            for (uint32_t kk = 0; kk < D / 16; ++kk)
+              mma_ss(tmem + kColS, q_desc + (kk >> 2) * (kRows * 8) + (kk & 3) * 2, kd + (kk >> 2) * (kKeys * 8) + (kk & 3) * 2,
+                     idesc_qk, kk > 0 ? 1u : 0u);
+            mma_commit(&sm.k_empty[st]);
+            if (u == low) mma_commit(&sm.q_empty);
+          }
+          __syncwarp();
+        };
+        // V(g - 1); Q (an item's first tile), K, the counts' operands, S(g - 1) read: one place for five waits. With one
+        // place for V, V(g) comes after PV(g - 1), and the operands of a tile with cleared rows after V(g): S(g) then waits its turn.
+        const int from = n > 0 ? 0 : 1, to = done ? 1 : kEarlyS ? (n > 0 ? 5 : 4) : 3;
+#pragma unroll 1
+        for (int i = from; ok && i < to; ++i) {
+          if (i == 1 && u != top) continue;
+          ok = wait_all(i == 0 ? &sm.v_full[sv] : i == 1 ? &sm.q_full : i == 2 ? &sm.k_full[st] : i == 3 ? &sm.feat_full[fs] : &sm.s_free,
+                        i == 0 ? (n - 1) / kVStages : i == 1 ? items : i == 2 ? n / kStages : i == 3 ? n >> 1 : n - 1);
         }
-        tc_fence_after();
-        const uint64_t kd = k_desc + static_cast<uint64_t>((st * Smem::kKBytes) >> 4);
-        // C(g), after PV(g - 1), whose P lies where C goes. The upper diagonal tile has none.
+        if (!ok) break;
+        if (kEarlyS && !done) issue_s();
+        if (n > 0) {
+          ok = wait_all(&sm.p_full, n - 1);
+          if (!ok) break;
+          tc_fence_after();
+          const uint64_t vd = v_desc + static_cast<uint64_t>((sv * Smem::kKBytes) >> 4);
+          if (elected) {
+#pragma unroll
+            for (uint32_t kk = 0; kk < kKeys / 16; ++kk)
+              mma_ts(tmem + kColO, tmem + kColC + 8u * kk, vd + 128u * kk, idesc_pv, (!pend_first || kk > 0) ? 1u : 0u);
+            mma_commit(&sm.v_empty[sv]);
+            if (pend_last) mma_commit(&sm.o_full);
+          }
+          __syncwarp();
+        }
+        if (done) break;
+        if (!kEarlyS) {
+          ok = wait_all(&sm.feat_full[fs], n >> 1);
+          if (!ok) break;
+          issue_s();
+        }
         const int rel = u - row_tile;  // 1: keys 64..127 of the row tile, 0: keys 0..63, < 0: before it
         const uint64_t ad = a_desc + static_cast<uint64_t>((rel == 0 ? kRows / 2 * kFeat : 0) >> 4);
         const uint64_t bd = b_desc + static_cast<uint64_t>((fs * (kKeys * kFeat)) >> 4);
         if (elected) {
-#pragma unroll
-          for (uint32_t kk = 0; kk < D / 16; ++kk)
-            mma_ss(tmem + kColS, q_desc + (kk >> 2) * (kRows * 8) + (kk & 3) * 2, kd + (kk >> 2) * (kKeys * 8) + (kk & 3) * 2,
-                   idesc_qk, kk > 0 ? 1u : 0u);
-          mma_commit(&sm.k_empty[st]);
-          if (u == low) mma_commit(&sm.q_empty);
           if (rel <= 0) {
 #pragma unroll
             for (int c = 0; c < kFeat / 32; ++c) mma_f8(tmem + kColC, ad + 16u * c, bd + 16u * c, idesc_c, c > 0 ? 1u : 0u);
@@ -635,9 +667,9 @@ serve_tc_kernel(const __grid_constant__ CUtensorMap tmap_q, const __grid_constan
         pend_first = u == top;
         pend_last = u == low;
       }
+      if (done) break;
       ++items;
     }
-    if (ok && n > 0) flush();
     if (elected) {
       mma_commit(&sm.drain);  // every MMA issued so far completes before it arrives
       mbar_wait_drain(&sm.drain, 0, kDrainNs);
@@ -664,36 +696,33 @@ serve_tc_kernel(const __grid_constant__ CUtensorMap tmap_q, const __grid_constan
         if (p < end)
           asm volatile("ld.global.ca.u32 %0, [%1];" : "=r"(x) : "l"(prm.near + (static_cast<size_t>(h) * max_len + p) * kKeys));
       }
-      MaskT rv[4];  // rows 32 q + lane
+      MaskT rv[4], nx[2];  // masks of rows 32 q + lane, and of the first key tile
 #pragma unroll
       for (int q = 0; q < 4; ++q) rv[q] = mask_at(i0 + 32 * q + lane);
-      // the first tiles' masks
-      MaskT kv[2], nx[2];
 #pragma unroll
       for (int q = 0; q < 2; ++q) nx[q] = mask_at(kKeys * first + 32 * q + lane);
-      // rows: OR inside the 32-row block, then from the tile's middle and from its first row
-      MaskT in[4], tot[4];
-#pragma unroll
-      for (int q = 0; q < 4; ++q) {
-        in[q] = tiles::warp_prefix_or<MaskT>(rv[q], lane);
-        tot[q] = __shfl_sync(0xffffffffu, in[q], 31);
-      }
       // published with the item's first tile; the item before last, which had this place, has been read once tile g - 2 has
       if (g >= 2 && !wait_all(&sm.feat_empty[g & 1], (g >> 1) + 1)) { ok = false; break; }
       const int rb = items & 1;
-      MaskT before = 0;
+      MaskT* rows = sm.rows[rb];
 #pragma unroll
+      for (int q = 0; q < 4; ++q) rows[32 * q + lane] = rv[q];
+      MaskT before = 0, before_mid = 0;
+#pragma unroll 1
       for (int q = 0; q < 4; ++q) {
-        sm.pre[rb][32 * q + lane] = static_cast<MaskT>(before | in[q]);
-        before = static_cast<MaskT>(before | tot[q]);
+        const MaskT in = tiles::warp_prefix_or<MaskT>(rows[32 * q + lane], lane);
+        const MaskT tot = __shfl_sync(0xffffffffu, in, 31);
+        rows[32 * q + lane] = static_cast<MaskT>(before | in);
+        before = static_cast<MaskT>(before | tot);
+        if (q >= 2) {
+          rows[64 + 32 * q + lane] = static_cast<MaskT>(before_mid | in);
+          before_mid = tot;
+        }
       }
-      sm.mid[rb][lane] = in[2];
-      sm.mid[rb][32 + lane] = static_cast<MaskT>(tot[2] | in[3]);
       bool built = false;
       MaskT gap = 0;
       for (int u = first; ok && u >= low; --u, ++g) {
-        kv[0] = nx[0];
-        kv[1] = nx[1];
+        const MaskT kv[2] = {nx[0], nx[1]};
         if (u > low) {
 #pragma unroll
           for (int q = 0; q < 2; ++q) nx[q] = mask_at(kKeys * (u - 1) + 32 * q + lane);
@@ -710,12 +739,11 @@ serve_tc_kernel(const __grid_constant__ CUtensorMap tmap_q, const __grid_constan
             built = true;
             if (last_product >= 0 && !wait_all(&sm.feat_empty[last_product & 1], last_product >> 1)) { ok = false; break; }
 #pragma unroll 1
-            for (int r = lane; r < kRows; r += 32) put_bits<MaskT>(sm.a, r, static_cast<MaskT>(FULL & ~sm.pre[rb][r]));
-#pragma unroll 1
-            for (int r = lane; r < kRows / 2; r += 32) put_bits<MaskT>(sm.a, kRows + r, static_cast<MaskT>(FULL & ~sm.mid[rb][r]));
+            for (int r = lane; r < kRows + kRows / 2; r += 32) put_bits<MaskT>(sm.a, r, static_cast<MaskT>(FULL & ~rows[r]));
           }
-          put_bits<MaskT>(sm.b[fs], lane, static_cast<MaskT>(FULL & ~(a0 | t1 | gap)));
-          put_bits<MaskT>(sm.b[fs], 32 + lane, static_cast<MaskT>(FULL & ~(a1 | gap)));
+#pragma unroll 1
+          for (int q = 0; q < 2; ++q)
+            put_bits<MaskT>(sm.b[fs], 32 * q + lane, static_cast<MaskT>(FULL & ~((q ? a1 : static_cast<MaskT>(a0 | t1)) | gap)));
         }
         if (lane == 0) {
           sm.gap[fs] = gap;
@@ -727,6 +755,7 @@ serve_tc_kernel(const __grid_constant__ CUtensorMap tmap_q, const __grid_constan
           const int st = g % kStages, sv = g % kVStages;
           if (!wait_all(&sm.k_full[st], g / kStages) || !wait_all(&sm.v_full[sv], g / kVStages)) { ok = false; break; }
           const int r0 = end - kKeys * u;
+#pragma unroll 1
           for (int e = lane; e < (kKeys - r0) * (D / 8); e += 32) {
             const int r = r0 + e / (D / 8), c = e % (D / 8);
             const int at = (c >> 3) * (kKeys * 128) + r * 128 + (c & 7) * 16;
@@ -746,6 +775,7 @@ serve_tc_kernel(const __grid_constant__ CUtensorMap tmap_q, const __grid_constan
 
   tc_fence_before();
   __syncthreads();
+  if (threadIdx.x == 0 && *abort_flag) atomicOr(err, PLSH_DEVERR_TIMEOUT);
   if (warp == kWarpMma) {
     __syncwarp();
     tc_fence_after();
@@ -790,7 +820,8 @@ int launch(const ServeArgs& a, cudaStream_t st) {
   prm.items = prm.slots * a.H;
   prm.spans = a.spans;
   prm.near = a.near;
-  prm.wait_ns = wait_limit_ns();
+  prm.wait_limit = static_cast<uint32_t>(wait_limit_ns() >> 20);
+  prm.log_s = std::log(static_cast<float>(a.s));
   prm.withhold_mma = withhold_mma() ? 1 : 0;
   auto kern = serve_tc_kernel<D, MaskT>;
   constexpr size_t smem = sizeof(TcSmem<D, MaskT>) + 1024;
