@@ -279,7 +279,10 @@ serve_tc_kernel(const __grid_constant__ CUtensorMap tmap_q, const __grid_constan
   const uint32_t tmem = uniform(sm.tmem_base);
   auto wait = [&](uint64_t* bar, uint32_t parity) { return wait_bounded(bar, parity & 1u, abort_flag, prm.wait_limit); };
   // the same by a whole warp: false in every lane if any gave up
-  auto wait_all = [&](uint64_t* bar, uint32_t parity) { return __all_sync(0xffffffffu, wait(bar, parity)) != 0; };
+  auto wait_all = [&](uint64_t* bar, uint32_t parity) {
+    if (__all_sync(0xffffffffu, mbar_try_wait(bar, parity & 1u))) return true;
+    return __all_sync(0xffffffffu, wait(bar, parity)) != 0;
+  };
 
   if (warp < kSoftmaxWarps) {
     regs_raise<kRegsSoftmax>();
@@ -364,36 +367,36 @@ serve_tc_kernel(const __grid_constant__ CUtensorMap tmap_q, const __grid_constan
           // P = 4c 2^(S sc - m) against the reference m, whatever S's maximum is: fp32 and bf16 hold P far beyond what the
           // softmax needs, so m has to be near the maximum only within some 2^60
           float lsum = 0.0f;
-          auto s_read = [&]() {
-            tc_fence_before();
-            __syncwarp();
-            if (lane == 0) mbar_arrive(&sm.s_free);
-          };
-          if (!live1 && !live0) s_read();
-#pragma unroll 1
-          for (int hf = 0; hf < 2; ++hf) {
+          // S and C of both halves into registers at once; S is then free for the next tile's
+          uint32_t s0[32], s1[32], c0v[32], c1v[32];
+          if (live0) tmem_ld32(base + kColS, s0);
+          if (live1) tmem_ld32(base + kColS + 32u, s1);
+          if (!own) {
+            if (live0) tmem_ld32(base + kColC, c0v);
+            if (live1) tmem_ld32(base + kColC + 32u, c1v);
+          }
+          tmem_wait_ld();
+          regs_after_wait(s0);
+          regs_after_wait(s1);
+          regs_after_wait(c0v);
+          regs_after_wait(c1v);
+          tc_fence_before();
+          __syncwarp();
+          if (lane == 0) mbar_arrive(&sm.s_free);
+          if (own) {
+#pragma unroll
+            for (int i = 0; i < 32; ++i) {  // byte b as the float 2^23 + b, exactly; then 4 (f - 2^23)
+              c0v[i] = __float_as_uint(fmaf(4.0f, __uint_as_float(__byte_perm(nc[i >> 2], 0x4B000000u, 0x7540u | (i & 3))), -33554432.0f));
+              c1v[i] = __float_as_uint(fmaf(4.0f, __uint_as_float(__byte_perm(nc[8 + (i >> 2)], 0x4B000000u, 0x7540u | (i & 3))), -33554432.0f));
+            }
+          }
+          // one half: P of 32 keys to their place over C, whose reading is done
+          auto half = [&](int hf, bool live, const uint32_t (&sv)[32], const uint32_t (&cv)[32]) {
             uint32_t pk[16];
+            if (!live) {
 #pragma unroll
-            for (int i = 0; i < 16; ++i) pk[i] = 0u;
-            if (hf ? live1 : live0) {
-              uint32_t sv[32], cv[32];
-              tmem_ld32(base + kColS + 32u * hf, sv);
-              if (own) {
-#pragma unroll
-                for (int i = 0; i < 8; ++i) {
-                  const uint32_t w4 = hf ? nc[8 + i] : nc[i];
-                  // byte b as the float 2^23 + b, exactly; then 4 (f - 2^23)
-#pragma unroll
-                  for (int e = 0; e < 4; ++e)
-                    cv[4 * i + e] = __float_as_uint(fmaf(4.0f, __uint_as_float(__byte_perm(w4, 0x4B000000u, 0x7540u | e)), -33554432.0f));
-                }
-              } else {
-                tmem_ld32(base + kColC + 32u * hf, cv);
-              }
-              tmem_wait_ld();
-              regs_after_wait(sv);
-              regs_after_wait(cv);
-              if (hf == (live1 ? 1 : 0)) s_read();  // the last half with weight
+              for (int i = 0; i < 16; ++i) pk[i] = 0u;
+            } else {
               float hsum;
               {
                 const uint64_t sc2 = f2_pack(sc, sc), negm2 = f2_pack(-m2, -m2);
@@ -467,8 +470,10 @@ serve_tc_kernel(const __grid_constant__ CUtensorMap tmap_q, const __grid_constan
               }
               lsum += hsum;
             }
-            tmem_st16(base + kColC + 16u * hf, pk);  // over C of this half or the one before, which have been read
-          }
+            tmem_st16(base + kColC + 16u * hf, pk);
+          };
+          half(0, live0, s0, c0v);
+          half(1, live1, s1, c1v);
           l += lsum;
         }
         if (pending) {  // the finished item's epilogue: its last product has run under this tile's exponentials
