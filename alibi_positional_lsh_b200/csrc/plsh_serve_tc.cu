@@ -58,8 +58,8 @@ constexpr uint32_t kColS = 0, kColC = 64, kColO = 128;
 constexpr float kSumMax = 1.8446744e19f, kSumMin = 9.3132257e-10f;  // 2^64, 2^-30
 constexpr int kMaxSortedHeads = 256;
 constexpr uint64_t kDrainNs = 100000000ull;
-// Registers per thread: 256 x 128 at launch; the softmax warpgroup takes 192, the other one keeps 64.
-constexpr uint32_t kRegsSoftmax = 192, kRegsRest = 64;
+// Registers per thread: 256 x 128 at launch; the softmax warpgroup takes 216, the other one keeps 40 (192 and 64: 7% slower, by spills).
+constexpr uint32_t kRegsSoftmax = 216, kRegsRest = 40;
 
 // One row tile of one head: positions i0 .. i0 + 127 of sequence s, against key tiles top, top - 1, .., low.
 struct Item {
@@ -291,51 +291,24 @@ serve_tc_kernel(const __grid_constant__ CUtensorMap tmap_q, const __grid_constan
     const uint32_t base = tmem + (static_cast<uint32_t>(32 * rg) << 16);
     const float sc = 1.4426950408889634f / sqrtf(static_cast<float>(D));
     int g = 0, items = 0;
-    int d_h = 0, d_i0 = 0, d_c0 = 0, d_pos0 = 0, d_end = 0;  // the finished item, until its epilogue
+    int d_at = -1;  // the finished item's row of O (-1: none) and its sum and reference, until its epilogue
     float d_l = 1.0f, d_m = 0.0f;
     bool pending = false;
-    // O / l of the item just finished, once its last product has completed: 32 bytes of the thread's own row at a time
-    auto epilogue = [&](int number) -> bool {
-      if (!wait_all(&sm.o_full, number)) return false;
-      tc_fence_after();
-      const float inv = 1.0f / d_l;
-      const int p = d_i0 + r;
-      const bool row = p >= d_pos0 && p < d_end;
-      const size_t at = static_cast<size_t>(row ? d_c0 + p - d_pos0 : 0) * H + d_h;
-      __nv_bfloat16* out = O + at * D;
-#pragma unroll 1
-      for (int c = 0; c < D; c += 32) {
-        uint32_t raw[32];
-        tmem_ld32(base + kColO + c, raw);
-        tmem_wait_ld();
-        regs_after_wait(raw);
-        uint32_t o[16];
-#pragma unroll
-        for (int i = 0; i < 16; ++i)
-          o[i] = pack_bf16x2(__uint_as_float(raw[2 * i]) * inv, __uint_as_float(raw[2 * i + 1]) * inv);
-        if (row) {
-          store32(out + c, o);
-          store32(out + c + 16, o + 8);
-        }
-      }
-      tc_fence_before();
-      if (row) row_sum[at] = (__log2f(d_l) + d_m - 2.0f) * 0.6931471805599453f - prm.log_s;
-      return true;
-    };
     bool ok = true;
     for (int k = 0; ok; ++k) {
       if (!wait_all(&sm.item_full[k % kItems], k / kItems)) break;
       const Item& item = sm.item[k % kItems];
       const bool done = !item.valid;
-      const int first = item.top, low = item.low, h = item.h, i0 = item.i0, c0 = item.c0, pos0 = item.pos0, end = item.end;
+      const int first = item.top, low = item.low, i0 = item.i0;
+      // the row's place in O, [T][H] rows; -1 where it holds no token
+      const int at = !done && i0 + r >= item.pos0 && i0 + r < item.end ? (item.c0 + i0 + r - item.pos0) * H + item.h : -1;
+      // c of the 64 keys of the row's own key tile, one byte each
+      const uint4* near = reinterpret_cast<const uint4*>(prm.near + (static_cast<size_t>(item.h) * max_len + (at >= 0 ? i0 + r : 0)) * kKeys);
       __syncwarp();
       if (lane == 0) mbar_arrive(&sm.item_empty[k % kItems]);
-      const bool mine = !done && i0 + r >= pos0 && i0 + r < end;  // the row holds a token
-      // c of the 64 keys of the row's own key tile, one byte each
-      const uint4* near = reinterpret_cast<const uint4*>(prm.near + (static_cast<size_t>(h) * max_len + (mine ? i0 + r : 0)) * kKeys);
       float m2 = 0.0f, l = 0.0f;
       MaskT pre = 0, mid = 0;
-      for (int u = first; ok && (done || u >= low); --u, ++g) {
+      for (int u = first; done ? pending : u >= low; --u, ++g) {
         if (!done) {
           const int fs = g & 1, rel = u - (i0 >> 6);
           if (!wait_all(&sm.feat_full[fs], g >> 1)) { ok = false; break; }
@@ -419,7 +392,7 @@ serve_tc_kernel(const __grid_constant__ CUtensorMap tmap_q, const __grid_constan
               }
               // out of range: a sum too large (or NaN: an infinite exponential of a key without weight), or too small once the
               // row's own key is in it
-              const bool redo = mine && (!(hsum <= kSumMax) || (own && hf == (rg & 1) && l + lsum + hsum < kSumMin));
+              const bool redo = at >= 0 && (!(hsum <= kSumMax) || (own && hf == (rg & 1) && l + lsum + hsum < kSumMin));
               if (__any_sync(0xffffffffu, redo)) {
                 // these rows' reference becomes the maximum so far over keys with weight, rounded up to a whole number, so that
                 // everything before follows by an exact power of two (PV(g - 1) has completed: C(g) came after it); the warp's other rows keep their bits
@@ -476,22 +449,45 @@ serve_tc_kernel(const __grid_constant__ CUtensorMap tmap_q, const __grid_constan
           half(1, live1, s1, c1v);
           l += lsum;
         }
-        if (pending) {  // the finished item's epilogue: its last product has run under this tile's exponentials
-          if (!epilogue(items - 1)) { ok = false; break; }
-          pending = false;
+        auto p_written = [&]() {
+          tmem_wait_st();
+          tc_fence_before();
+          __syncwarp();
+          if (lane == 0) mbar_arrive(&sm.p_full);
+        };
+        if (!pending) {
+          p_written();
+          continue;
+        }
+        // the finished item, whose last product has run under this tile's exponentials: O / l into registers before
+        // this tile's product overwrites it, and from there to memory after P has been handed over
+        pending = false;
+        if (!wait_all(&sm.o_full, items - 1)) { ok = false; break; }
+        tc_fence_after();
+        {
+          const float inv = 1.0f / d_l;
+          uint32_t o[D / 2];
+#pragma unroll
+          for (int c = 0; c < D; c += 32) {
+            uint32_t raw[32];
+            tmem_ld32(base + kColO + c, raw);
+            tmem_wait_ld();
+            regs_after_wait(raw);
+#pragma unroll
+            for (int i = 0; i < 16; ++i)
+              o[c / 2 + i] = pack_bf16x2(__uint_as_float(raw[2 * i]) * inv, __uint_as_float(raw[2 * i + 1]) * inv);
+          }
+          if (!done) p_written();
+          if (d_at >= 0) {
+#pragma unroll
+            for (int c = 0; c < D; c += 16) store32(O + static_cast<size_t>(d_at) * D + c, o + c / 2);
+            row_sum[d_at] = (__log2f(d_l) + d_m - 2.0f) * 0.6931471805599453f - prm.log_s;
+          }
         }
         if (done) break;
-        tmem_wait_st();
-        tc_fence_before();
-        __syncwarp();
-        if (lane == 0) mbar_arrive(&sm.p_full);
       }
       if (done) break;
-      d_h = h;
-      d_i0 = i0;
-      d_c0 = c0;
-      d_pos0 = pos0;
-      d_end = end;
+      d_at = at;
       d_l = l;
       d_m = m2;
       pending = true;
