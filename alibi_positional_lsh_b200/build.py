@@ -35,6 +35,7 @@ SOURCES = [
     "plsh_cache.cu",
     "plsh_serve_simt.cu",
     "plsh_serve_tc.cu",
+    "plsh_serve_rows.cu",
 ]
 
 ARCH = ["-gencode", "arch=compute_100a,code=sm_100a"]

@@ -121,8 +121,12 @@ struct ServeArgs {
   int dtype, H, H_kv, d, s;
   const int32_t* spans; const void* bmask;  // plsh_window's, causal, over max_len positions
   const uint8_t* near;                      // launch_near's; the bf16 kernel's
+  // paged bf16: sequences with at most this many new tokens are the row kernel's, the others the tile kernel's (0: all theirs)
+  int few;
   void* O; float* row_sum; uint32_t* err;
 };
+constexpr int kFewTokens = 16;
+int launch_serve_rows(const ServeArgs& a, cudaStream_t st);
 int launch_serve_simt(const ServeArgs& a, cudaStream_t st);
 int launch_near(const void* bmask, int H, int s, int n, uint8_t* near, cudaStream_t st);
 int launch_serve_tc(const ServeArgs& a, cudaStream_t st);  // bf16, packed K and V

@@ -166,5 +166,11 @@ extern "C" int plsh_paged_fwd(const void* Q, int64_t q_token, int64_t q_head, in
   a.dtype = dtype; a.H = H; a.H_kv = H_kv; a.d = d; a.s = s;
   a.spans = tile_span_dev; a.bmask = bmask_dev;
   a.O = O; a.row_sum = row_sum; a.err = err_dev;
-  return plsh::launch_serve_simt(a, static_cast<cudaStream_t>(stream));
+  const cudaStream_t st = static_cast<cudaStream_t>(stream);
+  if (dtype == PLSH_BF16) {
+    a.few = plsh::kFewTokens;
+    if (int rc = plsh::launch_serve_rows(a, st)) return rc;
+    if (max_new <= a.few) return PLSH_OK;
+  }
+  return plsh::launch_serve_simt(a, st);
 }

@@ -46,7 +46,7 @@ __global__ void __launch_bounds__(kThreads) serve_simt_kernel(ServeArgs a) {
   const int tile = (sq.pos0 >> 6) + static_cast<int>(blockIdx.x) - ((a.sq.cu[sm.sid] >> 6) + mult * sm.sid);
   const int end = sq.pos0 + sq.len;
   const int i0 = tile * kRows;
-  if (tile < 0 || sq.len == 0 || i0 >= end) return;
+  if (tile < 0 || sq.len <= a.few || i0 >= end) return;
   const int h = blockIdx.y, kvh = h / (a.H / a.pg.H_kv);
   const MaskT* bm = static_cast<const MaskT*>(a.bmask) + static_cast<size_t>(h) * a.sq.max_len;
   const float sc = 1.4426950408889634f / sqrtf(static_cast<float>(D));
