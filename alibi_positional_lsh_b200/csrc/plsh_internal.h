@@ -123,13 +123,16 @@ struct ServeArgs {
   const uint8_t* near;                      // launch_near's; the bf16 kernel's
   // paged bf16: sequences with at most this many new tokens are the row kernel's, the others the tile kernel's (0: all theirs)
   int few;
+  void* scratch; int max_window;            // e4m3 pages: serve_scratch_bytes for the tile kernel's sequences
+  int kv_rows, kv_pad;                      // rows of K and V, set by the launcher
   void* O; float* row_sum; uint32_t* err;
 };
 constexpr int kFewTokens = 16;
 int launch_serve_rows(const ServeArgs& a, cudaStream_t st);
 int launch_serve_simt(const ServeArgs& a, cudaStream_t st);
 int launch_near(const void* bmask, int H, int s, int n, uint8_t* near, cudaStream_t st);
-int launch_serve_tc(const ServeArgs& a, cudaStream_t st);  // bf16, packed K and V
+size_t serve_scratch_bytes(int T, int S, int H_kv, int d, int max_window);
+int launch_serve_tc(const ServeArgs& a, cudaStream_t st);  // bf16
 int launch_attention_tc(const AttnArgs& a, cudaStream_t st);
 
 }  // namespace plsh

@@ -145,11 +145,17 @@ extern "C" int plsh_cache_read(const void* k_pages, const void* v_pages, const i
                                  err_dev, static_cast<cudaStream_t>(stream));
 }
 
+extern "C" size_t plsh_paged_scratch_bytes(int T, int S, int max_new, int H_kv, int d, int max_window) {
+  if (T < 1 || S < 1 || H_kv < 1 || d < 1 || max_window < 1 || max_new <= plsh::kFewTokens) return 0;
+  return plsh::serve_scratch_bytes(T, S, H_kv, d, max_window);
+}
+
 extern "C" int plsh_paged_fwd(const void* Q, int64_t q_token, int64_t q_head, int dtype, int T, int S, const int32_t* cu_dev,
                               const int32_t* start_dev, int max_new, int H, int H_kv, int d, const void* k_pages,
                               const void* v_pages, const int8_t* k_exp, const int8_t* v_exp, const int32_t* page_table_dev,
                               int table_width, int num_pages, int page_size, int s, int max_len, const int32_t* tile_span_dev,
-                              const void* bmask_dev, void* O, float* row_sum, uint32_t* err_dev, void* stream) {
+                              const void* bmask_dev, const uint8_t* near_dev, int max_window, void* scratch_dev, size_t scratch_bytes,
+                              void* O, float* row_sum, uint32_t* err_dev, void* stream) {
   const char* fn = "plsh_paged_fwd";
   if (int rc = plsh::check_seqs(fn, T, S, cu_dev, max_len)) return rc;
   if (int rc = plsh::check_heads(fn, T, H, H_kv, dtype, d)) return rc;
@@ -157,10 +163,23 @@ extern "C" int plsh_paged_fwd(const void* Q, int64_t q_token, int64_t q_head, in
   if (int rc = plsh::check_pages(fn, k_pages, v_pages, k_exp, v_exp, page_table_dev, table_width, num_pages, page_size)) return rc;
   if (int rc = plsh::check_plan(fn, s, tile_span_dev, bmask_dev, O, row_sum, err_dev)) return rc;
   if (!start_dev) return fail(PLSH_ERR_INVALID_ARG, "%s: null pointer", fn);
+  const bool tiles = dtype == PLSH_BF16 && max_new > plsh::kFewTokens;
+  if (tiles && (!near_dev || !plsh::aligned16(near_dev)))
+    return fail(PLSH_ERR_INVALID_ARG, "%s: bf16 with max_new > %d needs near_dev, 16-byte aligned", fn, plsh::kFewTokens);
+  if (tiles && k_exp) {
+    if (max_window < 1 || max_window > max_len)
+      return fail(PLSH_ERR_INVALID_ARG, "%s: need 1 <= max_window <= max_len (max_window=%d)", fn, max_window);
+    const size_t need = plsh_paged_scratch_bytes(T, S, max_new, H_kv, d, max_window);
+    if (!scratch_dev || !plsh::aligned16(scratch_dev) || scratch_bytes < need)
+      return fail(PLSH_ERR_INVALID_ARG, "%s: scratch (16-byte aligned) holds %zu bytes, %zu needed", fn, scratch_bytes, need);
+  }
   if (max_new < 1) return fail(PLSH_ERR_INVALID_ARG, "%s: need max_new >= 1 (max_new=%d)", fn, max_new);
   plsh::ServeArgs a{};
   a.Q = Q; a.qs = {q_token, q_head};
   a.paged = true;
+  a.near = near_dev;
+  a.scratch = scratch_dev;
+  a.max_window = max_window;
   a.pg = plsh::pages(k_pages, v_pages, k_exp, v_exp, page_table_dev, table_width, num_pages, page_size, H_kv);
   a.sq = {cu_dev, start_dev, S, T, max_len, max_new};
   a.dtype = dtype; a.H = H; a.H_kv = H_kv; a.d = d; a.s = s;
@@ -170,7 +189,7 @@ extern "C" int plsh_paged_fwd(const void* Q, int64_t q_token, int64_t q_head, in
   if (dtype == PLSH_BF16) {
     a.few = plsh::kFewTokens;
     if (int rc = plsh::launch_serve_rows(a, st)) return rc;
-    if (max_new <= a.few) return PLSH_OK;
+    return tiles ? plsh::launch_serve_tc(a, st) : PLSH_OK;
   }
   return plsh::launch_serve_simt(a, st);
 }

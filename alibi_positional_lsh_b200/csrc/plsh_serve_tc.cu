@@ -64,6 +64,7 @@ constexpr uint32_t kRegsSoftmax = 216, kRegsRest = 40;
 // One row tile of one head: positions i0 .. i0 + 127 of sequence s, against key tiles top, top - 1, .., low.
 struct Item {
   int valid, h, i0, c0, pos0, end, s, top, low;
+  int kv0;  // row of K and V that holds position 0
 };
 
 template <int D, typename MaskT>
@@ -97,6 +98,9 @@ struct __align__(1024) TcSmem {
 struct TcParams {
   SeqArgs sq;
   int H, H_kv, s, slots, items;
+  int few;       // sequences with at most this many tokens are the row kernel's
+  int kv_pad;    // gathered K and V: rows before a sequence's new tokens (0: K and V are packed as Q)
+  PageArgs pg;   // pages of bf16 (kPaged)
   int q_swap, k_swap, v_swap;  // tensor map's second coordinate is the token (head-major storage) instead of the head
   const int32_t* spans;
   const uint8_t* near;  // [H][max_len][64]: c of the keys of each position's own 64-key tile
@@ -201,7 +205,7 @@ __global__ void __launch_bounds__(256) near_kernel(const MaskT* __restrict__ bma
 
 // ---- the kernel
 
-template <int D, typename MaskT>
+template <int D, typename MaskT, bool kPaged>
 __global__ void __launch_bounds__(kThreads, 2)
 serve_tc_kernel(const __grid_constant__ CUtensorMap tmap_q, const __grid_constant__ CUtensorMap tmap_k,
                 const __grid_constant__ CUtensorMap tmap_v, const __grid_constant__ TcParams prm,
@@ -512,7 +516,7 @@ serve_tc_kernel(const __grid_constant__ CUtensorMap tmap_q, const __grid_constan
       const Seq sq = load_seq(prm.sq, si);
       const int tile = (sq.pos0 >> 7) + slot - ((prm.sq.cu[si] >> 7) + mult * si);
       const int end = sq.pos0 + sq.len, i0 = kRows * tile;
-      if (tile < 0 || sq.len == 0 || i0 >= end) continue;
+      if (tile < 0 || sq.len <= prm.few || i0 >= end) continue;
       int lo = prm.spans[(static_cast<size_t>(h) * T128 + tile) * 2];
       if (lo < 0 || lo > i0) {
         if (lane == 0) atomicOr(err, PLSH_DEVERR_WINDOW);
@@ -521,7 +525,8 @@ serve_tc_kernel(const __grid_constant__ CUtensorMap tmap_q, const __grid_constan
       const int at = k % kItems;
       if (k >= kItems && !wait_all(&sm.item_empty[at], k / kItems + 1)) { ok = false; break; }
       if (lane == 0) {
-        sm.item[at] = Item{1, h, i0, sq.c0, sq.pos0, end, si, min((i0 + kRows - 1) >> 6, (end - 1) >> 6), lo >> 6};
+        sm.item[at] = Item{1, h, i0, sq.c0, sq.pos0, end, si, min((i0 + kRows - 1) >> 6, (end - 1) >> 6), lo >> 6,
+                           sq.c0 - sq.pos0 + (prm.kv_pad ? (si + 1) * prm.kv_pad - kKeys : 0)};
         mbar_arrive(&sm.item_full[at]);
       }
       ++k;
@@ -549,17 +554,42 @@ serve_tc_kernel(const __grid_constant__ CUtensorMap tmap_q, const __grid_constan
         const Item it = sm.item[k % kItems];
         mbar_arrive(&sm.item_empty[k % kItems]);
         if (!it.valid) break;
-        const int kvh = it.h / (H / prm.H_kv), row0 = it.c0 - it.pos0;
+        const int kvh = it.h / (H / prm.H_kv);
+        // a tile of K or V: one box, or one for each page that it touches. Pages behind the sequence's end are not looked up (their rows
+        // are cleared), and one outside the pool is replaced by page 0: the call reports it, and reads nothing else's memory.
+        auto load_tile = [&](uint8_t* dst, const CUtensorMap* map, int swap, int u, uint64_t* bar) {
+          if constexpr (kPaged) {
+            const int rows = min(kKeys, 1 << prm.pg.lg_page);
+#pragma unroll 1
+            for (int r = 0; r < kKeys; r += rows) {
+              const int p = kKeys * u + r, slot = p >> prm.pg.lg_page;
+              int page = 0;
+              if (p < it.end) {
+                page = slot < prm.pg.width ? prm.pg.table[static_cast<long long>(it.s) * prm.pg.width + slot] : -1;
+                if (page < 0 || page >= prm.pg.num_pages) {
+                  atomicOr(err, PLSH_DEVERR_PAGE);
+                  page = 0;
+                }
+              }
+#pragma unroll 1
+              for (int c = 0; c < D / 64; ++c)
+                tma_load_3d(dst + c * (kKeys * 128) + r * 128, map, 64 * c, p & ((1 << prm.pg.lg_page) - 1), page * prm.H_kv + kvh, bar);
+            }
+          } else {
+            const int t = it.kv0 + kKeys * u;
+#pragma unroll 1
+            for (int c = 0; c < D / 64; ++c)
+              tma_load_3d(dst + c * (kKeys * 128), map, 64 * c, swap ? t : kvh, swap ? kvh : t, bar);
+          }
+        };
         for (int u = it.top; u >= it.low; --u, ++n) {
-          const int st = n % kStages, t = row0 + kKeys * u;
+          const int st = n % kStages;
           if (n >= kStages && !wait(&sm.k_empty[st], n / kStages + 1)) { ok = false; break; }
           mbar_arrive_expect_tx(&sm.k_full[st], Smem::kKBytes);
-#pragma unroll 1
-          for (int c = 0; c < D / 64; ++c)
-            tma_load_3d(sm.k[st] + c * (kKeys * 128), &tmap_k, 64 * c, prm.k_swap ? t : kvh, prm.k_swap ? kvh : t, &sm.k_full[st]);
+          load_tile(sm.k[st], &tmap_k, prm.k_swap, u, &sm.k_full[st]);
           if (u == it.top) {
             if (loads && !wait(&sm.q_empty, loads + 1)) { ok = false; ++n; break; }
-            const int tq = row0 + it.i0;
+            const int tq = it.c0 - it.pos0 + it.i0;
             mbar_arrive_expect_tx(&sm.q_full, Smem::kQBytes);
 #pragma unroll 1
             for (int c = 0; c < D / 64; ++c)
@@ -569,9 +599,7 @@ serve_tc_kernel(const __grid_constant__ CUtensorMap tmap_q, const __grid_constan
           const int sv = n % kVStages;
           if (n >= kVStages && !wait(&sm.v_empty[sv], n / kVStages + 1)) { ok = false; ++n; break; }
           mbar_arrive_expect_tx(&sm.v_full[sv], Smem::kKBytes);
-#pragma unroll 1
-          for (int c = 0; c < D / 64; ++c)
-            tma_load_3d(sm.v[sv] + c * (kKeys * 128), &tmap_v, 64 * c, prm.v_swap ? t : kvh, prm.v_swap ? kvh : t, &sm.v_full[sv]);
+          load_tile(sm.v[sv], &tmap_v, prm.v_swap, u, &sm.v_full[sv]);
           nv = n + 1;
         }
       }
@@ -805,13 +833,84 @@ int make_rows_map(CUtensorMap* map, const void* p, RowStrides st, int T, int hea
   return PLSH_OK;
 }
 
-template <int D, typename MaskT>
+// Pages [planes][rows][D] of bf16: boxes of 64 columns x up to 64 rows of one plane, 128-byte swizzle.
+int make_pages_map(CUtensorMap* map, const void* p, int rows, long long planes, int D) {
+  auto enc = tiles::get_encode_fn();
+  if (!enc) return fail(PLSH_ERR_CUDA, "cuTensorMapEncodeTiled is not available from the driver");
+  cuuint64_t dims[3] = {static_cast<cuuint64_t>(D), static_cast<cuuint64_t>(rows), static_cast<cuuint64_t>(planes)};
+  cuuint64_t strides[2] = {static_cast<cuuint64_t>(D) * 2, static_cast<cuuint64_t>(rows) * D * 2};
+  cuuint32_t box[3] = {64, static_cast<cuuint32_t>(rows < kKeys ? rows : kKeys), 1};
+  cuuint32_t estr[3] = {1, 1, 1};
+  const CUresult r = enc(map, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 3, const_cast<void*>(p), dims, strides, box, estr,
+                         CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
+                         CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE);
+  if (r != CUDA_SUCCESS) return fail(PLSH_ERR_CUDA, "cuTensorMapEncodeTiled failed (%d)", static_cast<int>(r));
+  return PLSH_OK;
+}
+
+// The e4m3 rows that the tile kernel's sequences need, as bf16 (exact), in front of their new tokens: row
+// c0 + (s + 1) kv_pad - 64 + p - pos0 of [rows][H_kv][D] holds position p of sequence s. A block takes 64 positions of one
+// KV head, from the window of its widest head on.
+template <int D>
+__global__ void __launch_bounds__(256) gather_kernel(SeqArgs sq, PageArgs pg, const int32_t* __restrict__ spans, int H, int few,
+                                                     int kv_pad, __nv_bfloat16* __restrict__ K, __nv_bfloat16* __restrict__ V,
+                                                     uint32_t* __restrict__ err) {
+  const int kvh = blockIdx.y, G = H / pg.H_kv, k = kv_pad / kKeys + 2;
+  const int si = warp_find(sq.cu, sq.S, 6, k, blockIdx.x);
+  const Seq q = load_seq(sq, si);
+  if (q.len <= few) return;
+  const int u = (q.pos0 >> 6) - kv_pad / kKeys + static_cast<int>(blockIdx.x) - ((sq.cu[si] >> 6) + k * si);
+  const int end = q.pos0 + q.len;
+  const int T128 = (sq.max_len + PLSH_TILE - 1) / PLSH_TILE;
+  int lo = q.pos0;
+  for (int h = 0; h < G; ++h) lo = min(lo, spans[(static_cast<size_t>(kvh * G + h) * T128 + (q.pos0 >> 7)) * 2]);
+  lo = max(lo, max(0, q.pos0 - (kv_pad - kKeys)));
+  if (u < (lo >> 6) || kKeys * u >= end) return;
+  constexpr int kPer = D / 16;  // 16-byte pieces of a row
+  const long long out0 = q.c0 + static_cast<long long>(si + 1) * kv_pad - kKeys - q.pos0;
+  for (int e = threadIdx.x; e < kKeys * kPer; e += 256) {
+    const int p = kKeys * u + e / kPer, c = e % kPer;
+    if (p >= end) break;
+    const long long row = page_row(pg, si, p, kvh, err);
+    __nv_bfloat16* out[2] = {K + ((out0 + p) * pg.H_kv + kvh) * D + 16 * c, V + ((out0 + p) * pg.H_kv + kvh) * D + 16 * c};
+#pragma unroll
+    for (int kv = 0; kv < 2; ++kv) {
+      uint4 w = make_uint4(0, 0, 0, 0);
+      float sc = 0.0f;
+      if (row >= 0) {
+        w = __ldg(reinterpret_cast<const uint4*>(static_cast<const uint8_t*>(kv ? pg.v : pg.k) + row * D) + c);
+        sc = pow2((kv ? pg.v_exp : pg.k_exp)[row]);
+      }
+      const uint32_t ws[4] = {w.x, w.y, w.z, w.w};
+      uint32_t o[8];
+#pragma unroll
+      for (int i = 0; i < 4; ++i) {
+        float f[4];
+        e4m3_to_float4(ws[i], f);
+        o[2 * i] = pack_bf16x2(f[0] * sc, f[1] * sc);
+        o[2 * i + 1] = pack_bf16x2(f[2] * sc, f[3] * sc);
+      }
+      store32(out[kv], o);
+    }
+  }
+}
+
+template <int D, typename MaskT, bool kPaged>
 int launch(const ServeArgs& a, cudaStream_t st) {
   CUtensorMap mq, mk, mv;
   TcParams prm{};
   if (int rc = make_rows_map(&mq, a.Q, a.qs, a.sq.T, a.H, D, kRows, &prm.q_swap)) return rc;
-  if (int rc = make_rows_map(&mk, a.K, a.ks, a.sq.T, a.H_kv, D, kKeys, &prm.k_swap)) return rc;
-  if (int rc = make_rows_map(&mv, a.V, a.vs, a.sq.T, a.H_kv, D, kKeys, &prm.v_swap)) return rc;
+  if (kPaged) {
+    const long long planes = static_cast<long long>(a.pg.num_pages) * a.H_kv;
+    if (int rc = make_pages_map(&mk, a.pg.k, 1 << a.pg.lg_page, planes, D)) return rc;
+    if (int rc = make_pages_map(&mv, a.pg.v, 1 << a.pg.lg_page, planes, D)) return rc;
+  } else {
+    if (int rc = make_rows_map(&mk, a.K, a.ks, a.kv_rows, a.H_kv, D, kKeys, &prm.k_swap)) return rc;
+    if (int rc = make_rows_map(&mv, a.V, a.vs, a.kv_rows, a.H_kv, D, kKeys, &prm.v_swap)) return rc;
+  }
+  prm.few = a.few;
+  prm.kv_pad = a.kv_pad;
+  prm.pg = a.pg;
   prm.sq = a.sq;
   prm.H = a.H;
   prm.H_kv = a.H_kv;
@@ -824,7 +923,7 @@ int launch(const ServeArgs& a, cudaStream_t st) {
   prm.wait_limit = static_cast<uint32_t>(wait_limit_ns() >> 20);
   prm.log_s = std::log(static_cast<float>(a.s));
   prm.withhold_mma = withhold_mma() ? 1 : 0;
-  auto kern = serve_tc_kernel<D, MaskT>;
+  auto kern = serve_tc_kernel<D, MaskT, kPaged>;
   constexpr size_t smem = sizeof(TcSmem<D, MaskT>) + 1024;
   static_assert(smem <= 115712, "shared memory of two blocks on an SM");
   cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, static_cast<int>(smem));
@@ -846,10 +945,49 @@ int launch_near(const void* bmask, int H, int s, int n, uint8_t* near, cudaStrea
   return e == cudaSuccess ? PLSH_OK : cuda_fail(e, "near_kernel launch");
 }
 
+namespace {
+
+template <bool kPaged>
+int launch_types(const ServeArgs& a, cudaStream_t st) {
+  if (a.d == 128) return a.s <= 32 ? launch<128, uint32_t, kPaged>(a, st) : launch<128, unsigned long long, kPaged>(a, st);
+  return a.s <= 32 ? launch<64, uint32_t, kPaged>(a, st) : launch<64, unsigned long long, kPaged>(a, st);
+}
+
+}  // namespace
+
+// Rows that a sequence's window may take before its new tokens, in whole key tiles (a row tile's window reaches up to 127 keys
+// further down than a row's own), and a tile's slack at either end.
+int serve_kv_pad(int max_window) { return ceil_div(max_window + 2 * PLSH_TILE, kKeys) * kKeys; }
+
+size_t serve_scratch_bytes(int T, int S, int H_kv, int d, int max_window) {
+  return 2 * (static_cast<size_t>(T) + static_cast<size_t>(S) * serve_kv_pad(max_window)) * H_kv * d * 2;
+}
+
 int launch_serve_tc(const ServeArgs& a, cudaStream_t st) {
-  if (a.d == 128)
-    return a.s <= 32 ? launch<128, uint32_t>(a, st) : launch<128, unsigned long long>(a, st);
-  return a.s <= 32 ? launch<64, uint32_t>(a, st) : launch<64, unsigned long long>(a, st);
+  if (!a.paged) {
+    ServeArgs b = a;
+    b.kv_rows = a.sq.T;
+    return launch_types<false>(b, st);
+  }
+  if (!a.pg.k_exp) return launch_types<true>(a, st);
+  // e4m3 pages: the rows in reach as bf16 in the caller's scratch, then as if they were packed
+  ServeArgs b = a;
+  b.kv_pad = serve_kv_pad(a.max_window);
+  const long long rows = static_cast<long long>(a.sq.T) + static_cast<long long>(a.sq.S) * b.kv_pad;
+  const long long slots = (a.sq.T >> 6) + static_cast<long long>(a.sq.S) * (b.kv_pad / kKeys + 2);
+  if (rows > 0x7fffffffLL || slots > 0x7fffffffLL) return fail(PLSH_ERR_RANGE, "plsh_paged_fwd: too many cached rows in reach");
+  b.kv_rows = static_cast<int>(rows);
+  __nv_bfloat16* k = static_cast<__nv_bfloat16*>(a.scratch);
+  __nv_bfloat16* v = k + rows * a.H_kv * a.d;
+  b.K = k;
+  b.V = v;
+  b.ks = b.vs = {static_cast<long long>(a.H_kv) * a.d, a.d};
+  const dim3 grid(static_cast<unsigned>(slots), a.H_kv);
+  if (a.d == 128) gather_kernel<128><<<grid, 256, 0, st>>>(a.sq, a.pg, a.spans, a.H, a.few, b.kv_pad, k, v, a.err);
+  else gather_kernel<64><<<grid, 256, 0, st>>>(a.sq, a.pg, a.spans, a.H, a.few, b.kv_pad, k, v, a.err);
+  const cudaError_t e = cudaGetLastError();
+  if (e != cudaSuccess) return cuda_fail(e, "gather_kernel launch");
+  return launch_types<false>(b, st);
 }
 
 }  // namespace plsh

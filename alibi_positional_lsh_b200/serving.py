@@ -19,7 +19,7 @@ import numpy as np
 import torch
 
 from . import (PLSH_BF16, PLSH_F32, PLSH_MAX_S, PLSH_TILE, PlshError, decode_device_error, plsh_cache_append,
-               plsh_cache_read, plsh_draw_table_heads, plsh_near_counts, plsh_packed_fwd, plsh_paged_fwd, plsh_window_from_table)
+               plsh_cache_read, plsh_draw_table_heads, plsh_near_counts, plsh_packed_fwd, plsh_paged_fwd, plsh_paged_scratch_bytes, plsh_window_from_table)
 
 _CODES = {torch.bfloat16: PLSH_BF16, torch.float32: PLSH_F32}
 
@@ -197,6 +197,7 @@ class PlshServing(_Errors):
                 self.near = torch.empty((H, max_len, 64), dtype=torch.uint8, device=self.device)
                 plsh_near_counts(self.bmask, H, s, max_len, self.near)
             self.check()  # waits for the plan, so that any stream may use it from here on
+            self.max_window = int(self.bmax.max().item())  # the longest block
 
     def _outputs(self, T: int, out, st) -> Tuple[torch.Tensor, torch.Tensor]:
         if out is None:
@@ -249,7 +250,14 @@ class PlshServing(_Errors):
             st = torch.cuda.current_stream() if stream is None else stream
             O, row_sum = self._outputs(T, out, st)
             if S and T:
-                plsh_paged_fwd(q, _CODES[self.dtype], cu_seqlens, start, T if max_new is None else min(max_new, T), self.H,
-                               self.H_kv, self.d, cache.k_pages, cache.v_pages, cache.k_exp, cache.v_exp, page_table, self.s,
-                               self.max_len, self.spans, self.bmask, O, row_sum, self.err, st)
+                most = T if max_new is None else min(max_new, T)
+                scratch = None
+                if cache.quantised and self.near is not None:
+                    need = plsh_paged_scratch_bytes(T, S, most, self.H_kv, self.d, self.max_window)
+                    if need:
+                        with torch.cuda.stream(st):
+                            scratch = torch.empty((need,), dtype=torch.uint8, device=self.device)
+                plsh_paged_fwd(q, _CODES[self.dtype], cu_seqlens, start, most, self.H, self.H_kv, self.d, cache.k_pages,
+                               cache.v_pages, cache.k_exp, cache.v_exp, page_table, self.s, self.max_len, self.spans,
+                               self.bmask, self.near, self.max_window, scratch, O, row_sum, self.err, st)
         return O, row_sum
