@@ -18,45 +18,98 @@ from typing import Optional, Sequence, Tuple
 import numpy as np
 import torch
 
-from . import (PLSH_BF16, PLSH_F32, PLSH_MAX_S, PLSH_TILE, PlshError, decode_device_error, plsh_cache_append,
-               plsh_cache_read, plsh_draw_table_heads, plsh_near_counts, plsh_packed_fwd, plsh_paged_fwd, plsh_paged_scratch_bytes, plsh_window_from_table)
+from . import (PLSH_BF16, PLSH_F32, PLSH_MAX_S, PLSH_TILE, PlshError, _check, _lib, decode_device_error,
+               plsh_draw_table_heads, plsh_near_counts, plsh_window_from_table)
 
 _CODES = {torch.bfloat16: PLSH_BF16, torch.float32: PLSH_F32}
 
 
-def _rows(t: torch.Tensor, name: str, shape: Tuple[Optional[int], ...], dtypes, device) -> None:
-    """t is [tokens][heads][d] on `device`, with rows that the kernels can load 16 bytes at a time."""
-    if t.dim() != len(shape) or any(b is not None and a != b for a, b in zip(t.shape, shape)):
-        raise ValueError(f"{name} must have shape {tuple('T' if b is None else b for b in shape)}, got {tuple(t.shape)}")
-    if t.dtype not in dtypes or t.device != device:
-        raise ValueError(f"{name} must be {' or '.join(map(str, dtypes))} on {device}, got {t.dtype} on {t.device}")
-    if t.numel() == 0:
-        return
-    step = 16 // t.element_size()
-    if t.stride(-1) != 1 or t.data_ptr() % 16 or any(n > 1 and (s % step or s < t.shape[-1])
-                                                     for n, s in zip(t.shape[:-1], t.stride()[:-1])):
-        raise ValueError(f"{name} must have contiguous, 16-byte aligned rows that do not overlap")
+_EMPTY = (0, 0, 0)
 
 
-def _ints(t: torch.Tensor, name: str, dims: int, device) -> None:
-    if t.dim() != dims or t.dtype != torch.int32 or t.device != device or not t.is_contiguous():
+def _stream(stream: Optional[torch.cuda.Stream], device: torch.device) -> int:
+    # the handle without the Stream object around it, which takes longer to make than the rest of a call's checks
+    return torch._C._cuda_getCurrentRawStream(device.index) if stream is None else stream.cuda_stream
+
+
+def _rows(t: torch.Tensor, name: str, T: Optional[int], heads: int, d: int, dtype: torch.dtype, device: torch.device) -> Tuple[int, int, int]:
+    """(pointer, token stride, head stride) of t, which must be [T][heads][d] of dtype on `device`, with rows that the kernels can
+    load 16 bytes at a time. T None: any."""
+    shape = t.shape
+    if len(shape) != 3 or shape[1] != heads or shape[2] != d or (T is not None and shape[0] != T):
+        raise ValueError(f"{name} must have shape {('T' if T is None else T, heads, d)}, got {tuple(shape)}")
+    if t.dtype is not dtype or t.device != device:
+        raise ValueError(f"{name} must be {dtype} on {device}, got {t.dtype} on {t.device}")
+    n = shape[0]
+    if n == 0:
+        return _EMPTY
+    p = t.data_ptr()
+    if t.is_contiguous():
+        if p % 16 == 0:
+            return p, heads * d, d
+    else:
+        # the stride of a dimension of one element says nothing: torch leaves any number there
+        token, head, one = t.stride()
+        if heads == 1:
+            head = d
+        if n == 1:
+            token = heads * head
+        step = 16 // t.element_size()
+        if one == 1 and p % 16 == 0 and token % step == 0 and head % step == 0 and token >= d and head >= d:
+            return p, token, head
+    raise ValueError(f"{name} must have contiguous, 16-byte aligned rows that do not overlap")
+
+
+def _ints(t: torch.Tensor, name: str, dims: int, device: torch.device) -> int:
+    if t.dtype is not torch.int32 or t.dim() != dims or t.device != device or not t.is_contiguous():
         raise ValueError(f"{name} must be a contiguous int32 tensor of {dims} dimension(s) on {device}")
+    return t.data_ptr()
 
 
-def _sequences(cu_seqlens: torch.Tensor, start: Optional[torch.Tensor], page_table: Optional[torch.Tensor], device) -> int:
-    _ints(cu_seqlens, "cu_seqlens", 1, device)
+def _sequences(cu_seqlens: torch.Tensor, device: torch.device) -> Tuple[int, int]:
+    p = _ints(cu_seqlens, "cu_seqlens", 1, device)
     S = cu_seqlens.shape[0] - 1
     if S < 0:
         raise ValueError("cu_seqlens must hold one entry more than there are sequences")
-    if start is not None:
-        _ints(start, "start", 1, device)
-        if start.shape[0] != S:
-            raise ValueError(f"start must hold one entry per sequence ({S})")
-    if page_table is not None:
-        _ints(page_table, "page_table", 2, device)
-        if page_table.shape[0] != S or page_table.shape[1] < 1:
-            raise ValueError(f"page_table must be [{S}][pages] with at least one page per sequence")
-    return S
+    return p, S
+
+
+def _cached(start: torch.Tensor, page_table: torch.Tensor, S: int, device: torch.device) -> Tuple[int, int, int]:
+    """Pointers of start and the page table, and the table's width."""
+    ps, pt = _ints(start, "start", 1, device), _ints(page_table, "page_table", 2, device)
+    if start.shape[0] != S:
+        raise ValueError(f"start must hold one entry per sequence ({S})")
+    if page_table.shape[0] != S or page_table.shape[1] < 1:
+        raise ValueError(f"page_table must be [{S}][pages] with at least one page per sequence")
+    return ps, pt, page_table.shape[1]
+
+
+class _On:
+    """The current device for the launches of a call: `device`, without work where it is current already (the usual case, which
+    torch.cuda.device's own steps would make up a good part of a decoding step's host time)."""
+
+    __slots__ = ("index", "back")
+
+    def __init__(self, index: int):
+        self.index, self.back = index, -1
+
+    def __enter__(self) -> None:
+        now = torch._C._cuda_getDevice()
+        if now != self.index:
+            self.back = now
+            torch.cuda.set_device(self.index)
+
+    def __exit__(self, *exc) -> None:
+        if self.back >= 0:
+            torch.cuda.set_device(self.back)
+
+
+def _empty(shape, dtype: torch.dtype, device: torch.device, stream: Optional[torch.cuda.Stream]) -> torch.Tensor:
+    """A new tensor for work on `stream` (None: the current one)."""
+    if stream is None:
+        return torch.empty(shape, dtype=dtype, device=device)
+    with torch.cuda.stream(stream):
+        return torch.empty(shape, dtype=dtype, device=device)
 
 
 class _Errors:
@@ -108,6 +161,7 @@ class PagedCache(_Errors):
                 raise ValueError(f"{nm} must be int8 [num_pages][H_kv][page_size]")
         self.k_pages, self.v_pages, self.k_exp, self.v_exp = k_pages, v_pages, k_exp, v_exp
         self.err = torch.zeros((4,), dtype=torch.int32, device=self.device)
+        self._pages = tuple(0 if x is None else x.data_ptr() for x in (k_pages, v_pages, k_exp, v_exp))
 
     @classmethod
     def empty(cls, num_pages: int, H_kv: int, page_size: int, d: int, dtype: torch.dtype = torch.float8_e4m3fn,
@@ -120,14 +174,19 @@ class PagedCache(_Errors):
     def append(self, k: torch.Tensor, v: torch.Tensor, page_table: torch.Tensor, cu_seqlens: torch.Tensor,
                start: torch.Tensor, stream: Optional[torch.cuda.Stream] = None) -> None:
         """Writes rows [cu[s], cu[s + 1]) of k, v [T][H_kv][d] to positions start[s] .. of sequence s."""
-        dtypes = tuple(_CODES) if self.quantised else (self.dtype,)
-        _rows(k, "k", (None, self.H_kv, self.d), dtypes, self.device)
-        _rows(v, "v", (k.shape[0], self.H_kv, self.d), (k.dtype,), self.device)
-        if _sequences(cu_seqlens, start, page_table, self.device) == 0 or k.shape[0] == 0:
+        dtype = k.dtype
+        if dtype not in _CODES or (not self.quantised and dtype is not self.dtype):
+            raise ValueError(f"k of {dtype} cannot go into {self.dtype} pages")
+        T, dev = k.shape[0], self.device
+        kr = _rows(k, "k", None, self.H_kv, self.d, dtype, dev)
+        vr = _rows(v, "v", T, self.H_kv, self.d, dtype, dev)
+        cu, S = _sequences(cu_seqlens, dev)
+        st, pt, width = _cached(start, page_table, S, dev)
+        if S == 0 or T == 0:
             return
-        with torch.cuda.device(self.device):
-            plsh_cache_append(k, v, _CODES[k.dtype], cu_seqlens, start, self.H_kv, self.d, self.k_pages, self.v_pages,
-                              self.k_exp, self.v_exp, page_table, self.err, stream)
+        with _On(dev.index):
+            _check(_lib.plsh_cache_append(*kr, *vr, _CODES[dtype], T, S, cu, st, self.H_kv, self.d, *self._pages, pt, width,
+                                          self.num_pages, self.page_size, self.err.data_ptr(), _stream(stream, dev)))
 
     def read(self, page_table: torch.Tensor, cu_seqlens: torch.Tensor, start: torch.Tensor, total: int,
              dtype: Optional[torch.dtype] = None, out: Optional[Tuple[torch.Tensor, torch.Tensor]] = None,
@@ -139,22 +198,24 @@ class PagedCache(_Errors):
         dtype = dtype if dtype is not None else (out[0].dtype if out is not None else torch.bfloat16 if self.quantised else self.dtype)
         if dtype not in (tuple(_CODES) if self.quantised else (self.dtype,)):
             raise ValueError(f"cannot read {self.dtype} pages as {dtype}")
-        S = _sequences(cu_seqlens, start, page_table, self.device)
+        dev = self.device
+        cu, S = _sequences(cu_seqlens, dev)
+        st, pt, width = _cached(start, page_table, S, dev)
         if total < 0:
             raise ValueError("total must be >= 0")
-        with torch.cuda.device(self.device):
-            st = torch.cuda.current_stream() if stream is None else stream
+        with _On(dev.index):
             if out is None:
-                with torch.cuda.stream(st):
-                    out = tuple(torch.empty((total, self.H_kv, self.d), dtype=dtype, device=self.device) for _ in range(2))
-            for t, nm in zip(out, ("K", "V")):
-                _rows(t, nm, (total, self.H_kv, self.d), (dtype,), self.device)
-                if not t.is_contiguous():
+                shape = (total, self.H_kv, self.d)
+                out = _empty(shape, dtype, dev, stream), _empty(shape, dtype, dev, stream)
+            K, V = out
+            for x, nm in ((K, "K"), (V, "V")):
+                _rows(x, nm, total, self.H_kv, self.d, dtype, dev)
+                if not x.is_contiguous():
                     raise ValueError(f"{nm} must be contiguous")
             if S and total:
-                plsh_cache_read(self.k_pages, self.v_pages, self.k_exp, self.v_exp, page_table, cu_seqlens, start, self.H_kv,
-                                self.d, _CODES[dtype], out[0], out[1], self.err, st)
-        return out
+                _check(_lib.plsh_cache_read(*self._pages, pt, width, self.num_pages, self.page_size, total, S, cu, st, self.H_kv,
+                                            self.d, _CODES[dtype], K.data_ptr(), V.data_ptr(), self.err.data_ptr(), _stream(stream, dev)))
+        return K, V
 
 
 class PlshServing(_Errors):
@@ -172,6 +233,7 @@ class PlshServing(_Errors):
         self.dtype, self.device = dtype, torch.device(device)
         if self.device.type != "cuda":
             raise ValueError("device must be a CUDA device")
+        torch.cuda.init()
         if self.device.index is None:
             self.device = torch.device("cuda", torch.cuda.current_device())
         self.sigma_host = np.ascontiguousarray(sigma, dtype=np.float64)
@@ -198,14 +260,15 @@ class PlshServing(_Errors):
                 plsh_near_counts(self.bmask, H, s, max_len, self.near)
             self.check()  # waits for the plan, so that any stream may use it from here on
             self.max_window = int(self.bmax.max().item())  # the longest block
+        self._code, self._err = _CODES[dtype], self.err.data_ptr()
+        self._plan = self.spans.data_ptr(), self.bmask.data_ptr(), 0 if self.near is None else self.near.data_ptr()
 
-    def _outputs(self, T: int, out, st) -> Tuple[torch.Tensor, torch.Tensor]:
+    def _outputs(self, T: int, out, stream) -> Tuple[torch.Tensor, torch.Tensor]:
         if out is None:
-            with torch.cuda.stream(st):
-                return (torch.empty((T, self.H, self.d), dtype=self.dtype, device=self.device),
-                        torch.empty((T, self.H), dtype=torch.float32, device=self.device))
+            return (_empty((T, self.H, self.d), self.dtype, self.device, stream),
+                    _empty((T, self.H), torch.float32, self.device, stream))
         O, row_sum = out
-        _rows(O, "O", (T, self.H, self.d), (self.dtype,), self.device)
+        _rows(O, "O", T, self.H, self.d, self.dtype, self.device)
         if row_sum.shape != (T, self.H) or row_sum.dtype != torch.float32 or row_sum.device != self.device \
                 or not row_sum.is_contiguous() or not O.is_contiguous():
             raise ValueError(f"out must be contiguous {self.dtype} [T][H][d] and float32 [T][H] on {self.device}")
@@ -218,16 +281,16 @@ class PlshServing(_Errors):
 
         Returns new tensors O [T][H][d] and row_sum [T][H] (float32), or fills `out`; tokens of no sequence (behind the
         last) are left as they are. Views with contiguous rows, as a fused QKV projection gives, need no copy."""
-        _rows(q, "q", (None, self.H, self.d), (self.dtype,), self.device)
-        _rows(k, "k", (q.shape[0], self.H_kv, self.d), (self.dtype,), self.device)
-        _rows(v, "v", (q.shape[0], self.H_kv, self.d), (self.dtype,), self.device)
-        S = _sequences(cu_seqlens, None, None, self.device)
-        with torch.cuda.device(self.device):
-            st = torch.cuda.current_stream() if stream is None else stream
-            O, row_sum = self._outputs(q.shape[0], out, st)
-            if S and q.shape[0]:
-                plsh_packed_fwd(q, k, v, _CODES[self.dtype], cu_seqlens, self.H, self.H_kv, self.d, self.s, self.max_len,
-                                self.spans, self.bmask, self.near, O, row_sum, self.err, st)
+        T, dev, dtype = q.shape[0], self.device, self.dtype
+        qr = _rows(q, "q", None, self.H, self.d, dtype, dev)
+        kr = _rows(k, "k", T, self.H_kv, self.d, dtype, dev)
+        vr = _rows(v, "v", T, self.H_kv, self.d, dtype, dev)
+        cu, S = _sequences(cu_seqlens, dev)
+        with _On(dev.index):
+            O, row_sum = self._outputs(T, out, stream)
+            if S and T:
+                _check(_lib.plsh_packed_fwd(*qr, *kr, *vr, self._code, T, S, cu, self.H, self.H_kv, self.d, self.s, self.max_len,
+                                            *self._plan, O.data_ptr(), row_sum.data_ptr(), self._err, _stream(stream, dev)))
         return O, row_sum
 
     def attend_paged(self, q: torch.Tensor, cache: PagedCache, page_table: torch.Tensor, cu_seqlens: torch.Tensor,
@@ -238,26 +301,26 @@ class PlshServing(_Errors):
 
         The cache holds the new tokens' own K and V already (append first). max_new: the most new tokens of a sequence
         where the caller knows it (1 when decoding); it chooses the kernels. Returns as attend_packed."""
-        _rows(q, "q", (None, self.H, self.d), (self.dtype,), self.device)
-        if cache.device != self.device or cache.H_kv != self.H_kv or cache.d != self.d or \
+        T, dev = q.shape[0], self.device
+        qr = _rows(q, "q", None, self.H, self.d, self.dtype, dev)
+        if cache.device != dev or cache.H_kv != self.H_kv or cache.d != self.d or \
                 (not cache.quantised and cache.dtype != self.dtype):
             raise ValueError("the cache's device, heads, head dim or type do not match the plan")
-        S = _sequences(cu_seqlens, start, page_table, self.device)
-        T = q.shape[0]
+        cu, S = _sequences(cu_seqlens, dev)
+        st, pt, width = _cached(start, page_table, S, dev)
         if max_new is not None and max_new < 1:
             raise ValueError("max_new must be >= 1")
-        with torch.cuda.device(self.device):
-            st = torch.cuda.current_stream() if stream is None else stream
-            O, row_sum = self._outputs(T, out, st)
+        most = T if max_new is None else min(max_new, T)
+        with _On(dev.index):
+            O, row_sum = self._outputs(T, out, stream)
             if S and T:
-                most = T if max_new is None else min(max_new, T)
-                scratch = None
+                scratch, need = None, 0
                 if cache.quantised and self.near is not None:
-                    need = plsh_paged_scratch_bytes(T, S, most, self.H_kv, self.d, self.max_window)
+                    need = _lib.plsh_paged_scratch_bytes(T, S, most, self.H_kv, self.d, self.max_window)
                     if need:
-                        with torch.cuda.stream(st):
-                            scratch = torch.empty((need,), dtype=torch.uint8, device=self.device)
-                plsh_paged_fwd(q, _CODES[self.dtype], cu_seqlens, start, most, self.H, self.H_kv, self.d, cache.k_pages,
-                               cache.v_pages, cache.k_exp, cache.v_exp, page_table, self.s, self.max_len, self.spans,
-                               self.bmask, self.near, self.max_window, scratch, O, row_sum, self.err, st)
+                        scratch = _empty((need,), torch.uint8, dev, stream)
+                _check(_lib.plsh_paged_fwd(*qr, self._code, T, S, cu, st, most, self.H, self.H_kv, self.d, *cache._pages, pt, width,
+                                           cache.num_pages, cache.page_size, self.s, self.max_len, *self._plan, self.max_window,
+                                           scratch.data_ptr() if need else 0, need, O.data_ptr(), row_sum.data_ptr(), self._err,
+                                           _stream(stream, dev)))
         return O, row_sum
