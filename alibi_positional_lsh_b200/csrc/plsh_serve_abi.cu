@@ -153,22 +153,23 @@ extern "C" size_t plsh_paged_scratch_bytes(int T, int S, int max_new, int H_kv, 
 extern "C" int plsh_paged_fwd(const void* Q, int64_t q_token, int64_t q_head, int dtype, int T, int S, const int32_t* cu_dev,
                               const int32_t* start_dev, int max_new, int H, int H_kv, int d, const void* k_pages,
                               const void* v_pages, const int8_t* k_exp, const int8_t* v_exp, const int32_t* page_table_dev,
-                              int table_width, int num_pages, int page_size, int s, int max_len, const int32_t* tile_span_dev,
-                              const void* bmask_dev, const uint8_t* near_dev, int max_window, void* scratch_dev, size_t scratch_bytes,
-                              void* O, float* row_sum, uint32_t* err_dev, void* stream) {
+                              int table_width, int num_pages, int page_size, int s, int max_len, const double* table_dev,
+                              const int32_t* tile_span_dev, const void* bmask_dev, const uint8_t* near_dev, int max_window,
+                              void* scratch_dev, size_t scratch_bytes, void* O, float* row_sum, uint32_t* err_dev,
+                              void* stream) {
   const char* fn = "plsh_paged_fwd";
   if (int rc = plsh::check_seqs(fn, T, S, cu_dev, max_len)) return rc;
   if (int rc = plsh::check_heads(fn, T, H, H_kv, dtype, d)) return rc;
   if (int rc = plsh::check_rows(fn, "Q", Q, dtype, d, H, T, q_token, q_head)) return rc;
   if (int rc = plsh::check_pages(fn, k_pages, v_pages, k_exp, v_exp, page_table_dev, table_width, num_pages, page_size)) return rc;
   if (int rc = plsh::check_plan(fn, s, tile_span_dev, bmask_dev, O, row_sum, err_dev)) return rc;
-  if (!start_dev) return fail(PLSH_ERR_INVALID_ARG, "%s: null pointer", fn);
+  if (!table_dev || !start_dev) return fail(PLSH_ERR_INVALID_ARG, "%s: null pointer", fn);
+  if (max_window < 1 || max_window > max_len)
+    return fail(PLSH_ERR_INVALID_ARG, "%s: need 1 <= max_window <= max_len (max_window=%d)", fn, max_window);
   const bool tiles = dtype == PLSH_BF16 && max_new > plsh::kFewTokens;
   if (tiles && (!near_dev || !plsh::aligned16(near_dev)))
     return fail(PLSH_ERR_INVALID_ARG, "%s: bf16 with max_new > %d needs near_dev, 16-byte aligned", fn, plsh::kFewTokens);
   if (tiles && k_exp) {
-    if (max_window < 1 || max_window > max_len)
-      return fail(PLSH_ERR_INVALID_ARG, "%s: need 1 <= max_window <= max_len (max_window=%d)", fn, max_window);
     const size_t need = plsh_paged_scratch_bytes(T, S, max_new, H_kv, d, max_window);
     if (!scratch_dev || !plsh::aligned16(scratch_dev) || scratch_bytes < need)
       return fail(PLSH_ERR_INVALID_ARG, "%s: scratch (16-byte aligned) holds %zu bytes, %zu needed", fn, scratch_bytes, need);
@@ -178,6 +179,7 @@ extern "C" int plsh_paged_fwd(const void* Q, int64_t q_token, int64_t q_head, in
   a.Q = Q; a.qs = {q_token, q_head};
   a.paged = true;
   a.near = near_dev;
+  a.table = table_dev;
   a.scratch = scratch_dev;
   a.max_window = max_window;
   a.pg = plsh::pages(k_pages, v_pages, k_exp, v_exp, page_table_dev, table_width, num_pages, page_size, H_kv);

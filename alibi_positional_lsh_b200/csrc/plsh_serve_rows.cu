@@ -16,11 +16,18 @@
 // e4m3 values become f16 exactly (one conversion per pair) for S, with each row of Q scaled by a power of two into f16's range,
 // and bf16 exactly for P V; the rows' exponents multiply S and P, in fp32.
 //
-// Counts: c_ij = s - popcount(OR of the masks over (j, i]). With p0 the block's first token, the OR splits into
-// (j, p0], which the block holds per key and head of the group, and (p0, i], one word per row. The up to 15 keys
-// above p0 are a last step, counted from the masks directly.
+// Counts: blocks are contiguous, so hash k puts key j with row i >= j exactly if i's block begins at or below j. With p0 the
+// block's first token, the beginning b_k of p0's own block follows from the table in closed form (no mask is read for the window, whose
+// load would be one more trip to memory before K and V), the lowest of them is the window's exact end, and
+//   c_ij = popcount({k : b_k <= j} without the hashes that open a block in (p0, i]),
+// one word per key and head and one word per row. The up to 15 keys above p0 are a step of their own,
+// counted from the masks.
+//
+// What bounds it: a few tokens read so little that the time is the chain of trips to memory (lengths and table; pages;
+// exponents, K and V; the cluster's exchange); a batch reads each window once, 16 keys a step with the next step's rows on their way.
 #include <cooperative_groups.h>
 
+#include "plsh_binid.cuh"
 #include "plsh_serve.cuh"
 
 namespace plsh {
@@ -33,17 +40,45 @@ constexpr int kThreads = 128, kWarps = 4, kRowsMax = 16, kStep = 16;
 constexpr int kChunk = 256;      // keys whose rows, exponents and counts a block holds at a time
 constexpr int kMaxGroup = 16;    // query heads of a block (a larger group takes several blocks)
 
+// Shared memory of a block for `heads` query heads and `rows` rows.
 template <int D, typename MaskT>
-struct RowsSmem {
-  float o[kWarps][kRowsMax][D + 4];
-  float m[kWarps][kRowsMax], l[kWarps][kRowsMax];
-  MaskT suf[kMaxGroup][kChunk];   // OR of the masks over (j, p0], per head and key
-  MaskT carry[kMaxGroup];         // of the keys above the chunk
-  MaskT row_or[kRowsMax];         // OR of the masks over (p0, i]
-  MaskT tail[kMaxGroup][kStep];   // masks of positions p0 + 1 ..
-  long long row[kChunk + kStep];  // the keys' rows in the pages (-1: none)
-  float ks[kChunk + kStep], vs[kChunk + kStep];
+struct Layout {
+  int o, ml, begin, keep, row_off, tail, row, ks, vs, total;
+  __host__ __device__ Layout(int heads, int rows) {
+    int at = 0;
+    auto take = [&](int bytes) {
+      const int here = at;
+      at += (bytes + 15) / 16 * 16;
+      return here;
+    };
+    o = take(kWarps * rows * (D + 4) * 4);         // [warp][row][D + 4]: the warps' rows of O
+    ml = take(2 * kWarps * rows * 4);              // [2][warp][row]: their m and l
+    begin = take(heads * PLSH_MAX_S * 4);          // [head][hash]: where p0's block begins
+    keep = take(heads * kChunk * (int)sizeof(MaskT));   // [head][key]: hashes whose block reaches the key
+    row_off = take(rows * (int)sizeof(MaskT));     // [row]: hashes that open a block in (p0, i]
+    tail = take(heads * kStep * (int)sizeof(MaskT));    // [head][k]: masks of positions p0 + 1 + k
+    row = take((kChunk + kStep) * 8);              // [key]: its row in the pages (-1: none)
+    ks = take((kChunk + kStep) * 4);               // [key]: 2^exponent of K and of V
+    vs = take((kChunk + kStep) * 4);
+    total = at;
+  }
 };
+
+// The first position of the block of hash `b` that holds p.
+__device__ __forceinline__ int block_begin(const Binning& b, int p) {
+  if (!b.ok) return 0;
+  const int32_t id = b.at(p);
+  const double x = ceil((static_cast<double>(id) + b.base) * b.delta - b.u);  // at most a rounding away
+  const int guess = x <= 0.0 ? 0 : x >= static_cast<double>(p) ? p : static_cast<int>(x);
+  if (b.at(guess) == id && (guess == 0 || b.at(guess - 1) != id)) return guess;
+  int good = p, bad = -1;  // ids do not decrease
+  while (good - bad > 1) {
+    const int mid = bad + (good - bad) / 2;
+    if (b.at(mid) == id) good = mid;
+    else bad = mid;
+  }
+  return good;
+}
 
 __device__ __forceinline__ void mma_f16(float (&c)[4], const uint32_t (&a)[4], uint32_t b0, uint32_t b1) {
   asm volatile("mma.sync.aligned.m16n8k16.row.col.f32.f16.f16.f32 {%0, %1, %2, %3}, {%4, %5, %6, %7}, {%8, %9}, {%0, %1, %2, %3};"
@@ -76,9 +111,9 @@ __device__ __forceinline__ float bf16_lo(uint32_t x) { return __uint_as_float(x 
 __device__ __forceinline__ float bf16_hi(uint32_t x) { return __uint_as_float(x & 0xFFFF0000u); }
 
 template <int D, typename MaskT, bool kQuant>
-__global__ void __launch_bounds__(kThreads) serve_rows_kernel(ServeArgs a, int tokens, int heads, int row_blocks, int head_blocks) {
+__global__ void __launch_bounds__(kThreads, D == 128 && !kQuant ? 2 : 3)
+serve_rows_kernel(ServeArgs a, int tokens, int heads, int row_blocks, int head_blocks) {
   extern __shared__ __align__(16) uint8_t smem_raw[];
-  auto& sm = *reinterpret_cast<RowsSmem<D, MaskT>*>(smem_raw);
   cg::cluster_group cluster = cg::this_cluster();
   const int C = static_cast<int>(cluster.num_blocks()), rank = static_cast<int>(cluster.block_rank());
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31, g = lane >> 2, t = lane & 3;
@@ -99,16 +134,33 @@ __global__ void __launch_bounds__(kThreads) serve_rows_kernel(ServeArgs a, int t
   if (nt <= 0 || sq.len > a.few) return;                      // the whole cluster returns
   const int rows = nt * nh, p0 = sq.pos0 + first, c0 = sq.c0 + first;
   const MaskT* bmask = static_cast<const MaskT*>(a.bmask);
+  const int max_rows = tokens * heads;  // of any block of the launch, alike for the whole cluster
+  const Layout<D, MaskT> at_(heads, max_rows);
+  float* const s_o = reinterpret_cast<float*>(smem_raw + at_.o);
+  float* const s_ml = reinterpret_cast<float*>(smem_raw + at_.ml);
+  int* const s_begin = reinterpret_cast<int*>(smem_raw + at_.begin);
+  MaskT* const s_keep = reinterpret_cast<MaskT*>(smem_raw + at_.keep);
+  MaskT* const s_row_off = reinterpret_cast<MaskT*>(smem_raw + at_.row_off);
+  MaskT* const s_tail = reinterpret_cast<MaskT*>(smem_raw + at_.tail);
+  long long* const s_row = reinterpret_cast<long long*>(smem_raw + at_.row);
+  float* const s_ks = reinterpret_cast<float*>(smem_raw + at_.ks);
+  float* const s_vs = reinterpret_cast<float*>(smem_raw + at_.vs);
 
-  // the window: the lowest key with weight for one of the block's rows is in no lower a place than its row tile's
-  const int T128 = (a.sq.max_len + PLSH_TILE - 1) / PLSH_TILE;
+  // where the blocks of p0 begin, and so the window; masks above p0
   int lo = p0;
-  for (int h = lane; h < nh; h += 32) lo = min(lo, a.spans[(static_cast<size_t>(h0 + h) * T128 + (p0 >> 7)) * 2]);
-  lo = max(0, __reduce_min_sync(0xffffffffu, lo));
-  // this block's keys: steps of 16 down from p0, dealt out to the cluster in runs
-  const int steps = (p0 - lo + kStep) / kStep;
-  const int per = (steps + C - 1) / C;
-  const int s0 = rank * per, s1 = min(steps, s0 + per);       // step i: keys p0 - 16 i - 15 .. p0 - 16 i
+  for (int e = tid; e < nh * a.s; e += kThreads) {
+    const int h = e / a.s, k = e % a.s;
+    const int b = block_begin(Binning::from_table(a.table + (static_cast<size_t>(h0 + h) * a.s + k) * 2), p0);
+    s_begin[h * PLSH_MAX_S + k] = b;
+    lo = min(lo, b);
+  }
+  for (int e = tid; e < nh * kStep; e += kThreads) {
+    const int h = e / kStep, k = e % kStep;
+    s_tail[e] = k + 1 < nt ? bmask[static_cast<size_t>(h0 + h) * a.sq.max_len + p0 + 1 + k] : static_cast<MaskT>(0);
+  }
+  __shared__ int s_lo[kWarps];
+  lo = __reduce_min_sync(0xffffffffu, lo);
+  if (lane == 0) s_lo[warp] = lo;
 
   // Q: lane (g, t) holds rows g and g + 8, in K's order of d
   float inv_scale[2] = {1.0f, 1.0f};
@@ -159,26 +211,16 @@ __global__ void __launch_bounds__(kThreads) serve_rows_kernel(ServeArgs a, int t
   const float sc0 = 1.4426950408889634f / sqrtf(static_cast<float>(D));
   const float sc[2] = {sc0 * inv_scale[0], sc0 * inv_scale[1]};
 
-  // masks above p0, and per row the OR over (p0, i]
-  for (int e = tid; e < nh * kStep; e += kThreads) {
-    const int h = e / kStep, k = e % kStep;
-    sm.tail[h][k] = k + 1 < nt ? bmask[static_cast<size_t>(h0 + h) * a.sq.max_len + p0 + 1 + k] : static_cast<MaskT>(0);
-  }
-  // the OR over the keys between p0 and this block's first step, per head: a warp takes heads in turn
-  for (int h = warp; h < nh; h += kWarps) {
-    const MaskT* bm = bmask + static_cast<size_t>(h0 + h) * a.sq.max_len;
-    MaskT v = 0;
-    for (int j = p0 - lane; j > p0 - kStep * s0; j -= 32) v |= bm[j];
-#pragma unroll
-    for (int o = 16; o >= 1; o >>= 1) v |= __shfl_xor_sync(0xffffffffu, v, o);
-    if (lane == 0) sm.carry[h] = v;
-  }
   __syncthreads();
-  if (tid < kRowsMax) {
+  lo = min(min(s_lo[0], s_lo[1]), min(s_lo[2], s_lo[3]));
+  // this block's keys: steps of 16 down from p0, dealt out to the cluster in runs; step i: keys p0 - 16 i - 15 .. p0 - 16 i
+  const int steps = (p0 - lo + kStep) / kStep;
+  const int per = (steps + C - 1) / C;
+  const int s0 = rank * per, s1 = min(steps, s0 + per);
+  if (tid < rows) {
     MaskT v = 0;
-    if (tid < rows)
-      for (int k = 0; k < tid / nh; ++k) v |= sm.tail[tid % nh][k];
-    sm.row_or[tid] = v;
+    for (int k = 0; k < tid / nh; ++k) v |= s_tail[tid % nh * kStep + k];
+    s_row_off[tid] = v;
   }
 
   float o[D / 8][4];
@@ -187,25 +229,26 @@ __global__ void __launch_bounds__(kThreads) serve_rows_kernel(ServeArgs a, int t
 #pragma unroll
     for (int e = 0; e < 4; ++e) o[i][e] = 0.0f;
   float m[2] = {-INFINITY, -INFINITY}, l[2] = {0.0f, 0.0f};
-  MaskT mine[2] = {0, 0};
+  MaskT mine[2] = {0, 0};  // of rows g and g + 8: the hashes that may count, and the row's head in the group
   int hh[2] = {0, 0};
 
   // rows, exponents of keys j(k), k = 0 .. n - 1, into places at ..
   auto describe = [&](int at, int k, int j, bool on) {
     long long row = -1;
     if (on) row = page_row(a.pg, sid, j, kvh, a.err);
-    sm.row[at + k] = row;
+    s_row[at + k] = row;
     if (kQuant) {
-      sm.ks[at + k] = row >= 0 ? pow2(a.pg.k_exp[row]) : 0.0f;
-      sm.vs[at + k] = row >= 0 ? pow2(a.pg.v_exp[row]) : 0.0f;
+      s_ks[at + k] = row >= 0 ? pow2(a.pg.k_exp[row]) : 0.0f;
+      s_vs[at + k] = row >= 0 ? pow2(a.pg.v_exp[row]) : 0.0f;
     }
   };
 
-  // one step: 16 keys at places at .. of sm.row; c[u][n] their counts for rows g and g + 8, keys 2 t, 2 t + 1, 2 t + 8, 2 t + 9
+  // one step: 16 keys at places at .. of sm.row;
+  // byte n of c4[u]: the count of row g + 8 u with key 2 t, 2 t + 1, 2 t + 8 or 2 t + 9
   auto load_k = [&](int at, uint4 (&kr)[2][D / 64][kQuant ? 1 : 2]) {
 #pragma unroll
     for (int n = 0; n < 2; ++n) {
-      const long long row = sm.row[at + 8 * n + g];
+      const long long row = s_row[at + 8 * n + g];
 #pragma unroll
       for (int c = 0; c < D / 64; ++c) {
         if constexpr (kQuant) {
@@ -224,7 +267,7 @@ __global__ void __launch_bounds__(kThreads) serve_rows_kernel(ServeArgs a, int t
   auto load_v = [&](int at, uint32_t (&vr)[4][kVWords]) {
 #pragma unroll
     for (int n = 0; n < 4; ++n) {
-      const long long row = sm.row[at + 2 * t + (n & 1) + 8 * (n >> 1)];
+      const long long row = s_row[at + 2 * t + (n & 1) + 8 * (n >> 1)];
       const uint8_t* src = static_cast<const uint8_t*>(a.pg.v) + row * (kQuant ? D : 2 * D) + (kQuant ? 1 : 2) * (D / 8) * g;
       if constexpr (kVWords % 4 == 0) {
 #pragma unroll
@@ -238,8 +281,9 @@ __global__ void __launch_bounds__(kThreads) serve_rows_kernel(ServeArgs a, int t
       }
     }
   };
-  auto step = [&](int at, const uint4 (&kr)[2][D / 64][kQuant ? 1 : 2], const uint32_t (&vr)[4][kVWords], const int (&c)[2][4]) {
+  auto step = [&](int at, const uint4 (&kr)[2][D / 64][kQuant ? 1 : 2], const uint32_t (&vr)[4][kVWords], const uint32_t (&c4)[2]) {
     float x[2][4];
+    auto count = [&](int u, int n) { return (c4[u] >> (8 * n)) & 0xFFu; };
 #pragma unroll
     for (int n = 0; n < 2; ++n) {
       float acc[4] = {0.0f, 0.0f, 0.0f, 0.0f};
@@ -259,7 +303,7 @@ __global__ void __launch_bounds__(kThreads) serve_rows_kernel(ServeArgs a, int t
       // acc: rows g (0, 1) and g + 8 (2, 3), keys 8 n + 2 t, + 1
 #pragma unroll
       for (int e = 0; e < 2; ++e) {
-        const float ks = kQuant ? sm.ks[at + 8 * n + 2 * t + e] : 1.0f;
+        const float ks = kQuant ? s_ks[at + 8 * n + 2 * t + e] : 1.0f;
         x[0][2 * n + e] = acc[e] * ks * sc[0];
         x[1][2 * n + e] = acc[2 + e] * ks * sc[1];
       }
@@ -269,7 +313,7 @@ __global__ void __launch_bounds__(kThreads) serve_rows_kernel(ServeArgs a, int t
     for (int u = 0; u < 2; ++u) {
       float top = m[u];
 #pragma unroll
-      for (int n = 0; n < 4; ++n) top = c[u][n] > 0 ? fmaxf(top, x[u][n]) : top;
+      for (int n = 0; n < 4; ++n) top = count(u, n) > 0 ? fmaxf(top, x[u][n]) : top;
       top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, 1));
       top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, 2));
       if (top > m[u]) {
@@ -285,9 +329,9 @@ __global__ void __launch_bounds__(kThreads) serve_rows_kernel(ServeArgs a, int t
       float w[4];
 #pragma unroll
       for (int n = 0; n < 4; ++n) {
-        w[n] = c[u][n] > 0 ? static_cast<float>(c[u][n]) * exp2f(x[u][n] - m[u]) : 0.0f;
+        w[n] = count(u, n) > 0 ? static_cast<float>(count(u, n)) * exp2f(x[u][n] - m[u]) : 0.0f;
         l[u] += w[n];
-        if (kQuant) w[n] *= c[u][n] > 0 ? sm.vs[at + 2 * t + (n & 1) + 8 * (n >> 1)] : 0.0f;
+        if (kQuant) w[n] *= count(u, n) > 0 ? s_vs[at + 2 * t + (n & 1) + 8 * (n >> 1)] : 0.0f;
       }
       p[u] = bf16x2(w[0], w[1]);
       p[u + 2] = bf16x2(w[2], w[3]);
@@ -314,8 +358,10 @@ __global__ void __launch_bounds__(kThreads) serve_rows_kernel(ServeArgs a, int t
 #pragma unroll
   for (int u = 0; u < 2; ++u) {
     const int r = g + 8 * u;
-    mine[u] = sm.row_or[r];
-    hh[u] = r < rows ? r % nh : 0;
+    if (r < rows) {
+      mine[u] = static_cast<MaskT>(~s_row_off[r]);
+      hh[u] = r % nh;
+    }
   }
   if (rank == 0 && warp == 0 && nt > 1) {
     if (lane < kStep) describe(kChunk, lane, p0 + 1 + lane, lane + 1 < nt);
@@ -324,18 +370,17 @@ __global__ void __launch_bounds__(kThreads) serve_rows_kernel(ServeArgs a, int t
     uint32_t vr[4][kVWords];
     load_k(kChunk, kr);
     load_v(kChunk, vr);
-    int c[2][4];
+    uint32_t c[2] = {0, 0};
 #pragma unroll
     for (int u = 0; u < 2; ++u) {
       const int r = g + 8 * u, tok = r / nh;  // the row's token: position p0 + tok
 #pragma unroll
       for (int n = 0; n < 4; ++n) {
         const int k = 2 * t + (n & 1) + 8 * (n >> 1);  // key p0 + 1 + k
-        c[u][n] = 0;
         if (r < rows && k + 1 <= tok) {
           MaskT v = 0;
-          for (int y = k + 1; y < tok; ++y) v |= sm.tail[hh[u]][y];
-          c[u][n] = a.s - popc_mask<MaskT>(v);
+          for (int y = k + 1; y < tok; ++y) v |= s_tail[hh[u] * kStep + y];
+          c[u] |= static_cast<uint32_t>(a.s - popc_mask<MaskT>(v)) << (8 * n);
         }
       }
     }
@@ -351,46 +396,55 @@ __global__ void __launch_bounds__(kThreads) serve_rows_kernel(ServeArgs a, int t
       const int j = p0 - kStep * b - k;
       describe(0, k, j, j >= lo);
     }
-    // OR over (j, p0]: an inclusive scan over the masks of j + 1 .. downward, per head
-    for (int h = warp; h < nh; h += kWarps) {
-      const MaskT* bm = bmask + static_cast<size_t>(h0 + h) * a.sq.max_len;
-      MaskT run = sm.carry[h];
-      for (int k0 = 0; k0 < ns * kStep; k0 += 32) {
-        const int k = k0 + lane, j = p0 - kStep * b - k;
-        MaskT v = j >= lo ? bm[j] : static_cast<MaskT>(0);   // of key j: joins the OR below j
-        MaskT inc = v;
-#pragma unroll
-        for (int s = 1; s < 32; s <<= 1) {
-          const MaskT y = __shfl_up_sync(0xffffffffu, inc, s);
-          if (lane >= s) inc |= y;
-        }
-        MaskT exc = __shfl_up_sync(0xffffffffu, inc, 1);
-        if (lane == 0) exc = 0;
-        if (k < ns * kStep) sm.suf[h][k] = static_cast<MaskT>(run | exc);
-        run |= __shfl_sync(0xffffffffu, inc, 31);
+    // the hashes whose block reaches the key, per head
+    for (int k = tid; k < ns * kStep; k += kThreads) {
+      const int j = p0 - kStep * b - k;
+      for (int h = 0; h < nh; ++h) {
+        MaskT v = 0;
+        const int* begin = s_begin + h * PLSH_MAX_S;
+#pragma unroll 4
+        for (int i = 0; i < a.s; ++i) v |= static_cast<MaskT>(begin[i] <= j) << i;
+        s_keep[h * kChunk + k] = v;
       }
-      __syncwarp();
-      if (lane == 0) sm.carry[h] = run;
     }
     __syncthreads();
-    for (int i = warp; i < ns; i += kWarps) {
-      const int at = kStep * i;
-      uint4 kr[2][D / 64][kQuant ? 1 : 2];
-      uint32_t vr[4][kVWords];
-      int c[2][4];
-      bool any = false;
+    // a warp's steps, the next one's rows on their way while this one is computed
+    auto counts = [&](int i, uint32_t (&c)[2]) {
 #pragma unroll
-      for (int u = 0; u < 2; ++u)
+      for (int u = 0; u < 2; ++u) {
+        c[u] = 0;
 #pragma unroll
         for (int n = 0; n < 4; ++n) {
-          const int k = at + 2 * t + (n & 1) + 8 * (n >> 1);
-          c[u][n] = g + 8 * u < rows && sm.row[k] >= 0 ? a.s - popc_mask<MaskT>(static_cast<MaskT>(sm.suf[hh[u]][k] | mine[u])) : 0;
-          any |= c[u][n] > 0;
+          const int k = kStep * i + 2 * t + (n & 1) + 8 * (n >> 1);
+          if (s_row[k] >= 0) c[u] |= static_cast<uint32_t>(popc_mask<MaskT>(static_cast<MaskT>(s_keep[hh[u] * kChunk + k] & mine[u]))) << (8 * n);
         }
-      if (!__any_sync(0xffffffffu, any)) continue;  // nothing has weight here
-      load_k(at, kr);
-      load_v(at, vr);
-      step(at, kr, vr, c);
+      }
+      return __any_sync(0xffffffffu, (c[0] | c[1]) != 0) != 0;  // else nothing has weight there
+    };
+    uint4 kr[2][D / 64][kQuant ? 1 : 2];
+    uint32_t c[2];
+    int i = warp;
+    while (i < ns && !counts(i, c)) i += kWarps;
+    if (i < ns) load_k(kStep * i, kr);
+    while (i < ns) {
+      uint32_t vr[4][kVWords];
+      load_v(kStep * i, vr);
+      int nx = i + kWarps;
+      uint32_t cn[2];
+      while (nx < ns && !counts(nx, cn)) nx += kWarps;
+      uint4 kn[2][D / 64][kQuant ? 1 : 2];
+      if (kQuant && nx < ns) load_k(kStep * nx, kn);
+      step(kStep * i, kr, vr, c);
+      if (!kQuant && nx < ns) load_k(kStep * nx, kn);  // (rows of bf16 take twice the registers)
+      i = nx;
+      c[0] = cn[0];
+      c[1] = cn[1];
+#pragma unroll
+      for (int n = 0; n < 2; ++n)
+#pragma unroll
+        for (int cc = 0; cc < D / 64; ++cc)
+#pragma unroll
+          for (int y = 0; y < (kQuant ? 1 : 2); ++y) kr[n][cc][y] = kn[n][cc][y];
     }
   }
 
@@ -402,14 +456,14 @@ __global__ void __launch_bounds__(kThreads) serve_rows_kernel(ServeArgs a, int t
     const int r = g + 8 * u;
     if (r >= rows) continue;
     if (t == 0) {
-      sm.m[warp][r] = m[u];
-      sm.l[warp][r] = l[u];
+      s_ml[warp * max_rows + r] = m[u];
+      s_ml[(kWarps + warp) * max_rows + r] = l[u];
     }
     // product i's columns n = 2 t, 2 t + 1: V's columns (D/8) (2 t) + i and (D/8) (2 t + 1) + i
 #pragma unroll
     for (int i = 0; i < D / 8; ++i) {
-      sm.o[warp][r][(D / 8) * (2 * t) + i] = o[i][2 * u];
-      sm.o[warp][r][(D / 8) * (2 * t + 1) + i] = o[i][2 * u + 1];
+      s_o[(warp * max_rows + r) * (D + 4) + (D / 8) * (2 * t) + i] = o[i][2 * u];
+      s_o[(warp * max_rows + r) * (D + 4) + (D / 8) * (2 * t + 1) + i] = o[i][2 * u + 1];
     }
   }
   cluster.sync();
@@ -417,19 +471,20 @@ __global__ void __launch_bounds__(kThreads) serve_rows_kernel(ServeArgs a, int t
     const int r = e / (D / 4), col = e % (D / 4) * 4;
     float top = -INFINITY;
     for (int b = 0; b < C; ++b) {
-      const float* pm = &cluster.map_shared_rank(&sm, b)->m[0][0];
+      const float* ml = cluster.map_shared_rank(s_ml, b);
 #pragma unroll
-      for (int w = 0; w < kWarps; ++w) top = fmaxf(top, pm[w * kRowsMax + r]);
+      for (int w = 0; w < kWarps; ++w) top = fmaxf(top, ml[w * max_rows + r]);
     }
     float total = 0.0f, acc[4] = {0.0f, 0.0f, 0.0f, 0.0f};
     for (int b = 0; b < C; ++b) {
-      const auto* rs = cluster.map_shared_rank(&sm, b);
+      const float* ml = cluster.map_shared_rank(s_ml, b);
+      const float* ro = cluster.map_shared_rank(s_o, b);
 #pragma unroll
       for (int w = 0; w < kWarps; ++w) {
-        const float f = exp2f(rs->m[w][r] - top);  // 0 for a warp without keys
+        const float f = exp2f(ml[w * max_rows + r] - top);  // 0 for a warp without keys
         if (f > 0.0f) {
-          total += rs->l[w][r] * f;
-          const float4 v = *reinterpret_cast<const float4*>(&rs->o[w][r][col]);
+          total += ml[(kWarps + w) * max_rows + r] * f;
+          const float4 v = *reinterpret_cast<const float4*>(ro + (w * max_rows + r) * (D + 4) + col);
           acc[0] += v.x * f;
           acc[1] += v.y * f;
           acc[2] += v.z * f;
@@ -450,17 +505,16 @@ template <int D, typename MaskT, bool kQuant>
 int launch(const ServeArgs& a, cudaStream_t st) {
   const int G = a.H / a.H_kv;
   const int heads = G < kMaxGroup ? G : kMaxGroup, head_blocks = ceil_div(G, heads);
-  const int tokens = kRowsMax / heads;
   const int most = a.sq.max_new < a.few ? a.sq.max_new : a.few;
+  const int tokens = most < kRowsMax / heads ? most : kRowsMax / heads;
   const int row_blocks = ceil_div(most, tokens);
   const long long items = static_cast<long long>(a.sq.S) * a.H_kv * head_blocks * row_blocks;
-  // blocks of a window: as many as fill the machine about twice over, up to the portable eight
+  // blocks of a window: up to the portable eight, as long as the machine has room for more, and no more than two steps a warp
   int C = 1;
-  while (C < 8 && items * C < 2 * 148) C *= 2;
-  if (C < 4) C = 4;
+  while (C < 8 && items * C < 4 * 148 && 2 * C * kWarps * kStep < a.max_window) C *= 2;
   if (items * C > 0x7fffffffLL) return fail(PLSH_ERR_RANGE, "plsh_paged_fwd: too many rows");
   auto kern = serve_rows_kernel<D, MaskT, kQuant>;
-  const int smem = static_cast<int>(sizeof(RowsSmem<D, MaskT>));
+  const int smem = Layout<D, MaskT>(heads, tokens * heads).total;
   cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
   if (e != cudaSuccess) return cuda_fail(e, "cudaFuncSetAttribute(serve_rows_kernel)");
   cudaLaunchConfig_t cfg{};

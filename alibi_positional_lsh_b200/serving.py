@@ -261,6 +261,7 @@ class PlshServing(_Errors):
             self.check()  # waits for the plan, so that any stream may use it from here on
             self.max_window = int(self.bmax.max().item())  # the longest block
         self._code, self._err = _CODES[dtype], self.err.data_ptr()
+        self._table = self.table_dev.data_ptr()
         self._plan = self.spans.data_ptr(), self.bmask.data_ptr(), 0 if self.near is None else self.near.data_ptr()
 
     def _outputs(self, T: int, out, stream) -> Tuple[torch.Tensor, torch.Tensor]:
@@ -320,7 +321,7 @@ class PlshServing(_Errors):
                     if need:
                         scratch = _empty((need,), torch.uint8, dev, stream)
                 _check(_lib.plsh_paged_fwd(*qr, self._code, T, S, cu, st, most, self.H, self.H_kv, self.d, *cache._pages, pt, width,
-                                           cache.num_pages, cache.page_size, self.s, self.max_len, *self._plan, self.max_window,
+                                           cache.num_pages, cache.page_size, self.s, self.max_len, self._table, *self._plan, self.max_window,
                                            scratch.data_ptr() if need else 0, need, O.data_ptr(), row_sum.data_ptr(), self._err,
                                            _stream(stream, dev)))
         return O, row_sum

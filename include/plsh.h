@@ -567,6 +567,7 @@ PLSH_API int plsh_cache_read(const void* k_pages, const void* v_pages, const int
  *   max_new   no sequence has more new tokens than this (else
  *             PLSH_DEVERR_SEQUENCE, and it is skipped). The call chooses its kernels by it,
  *             so give the largest length where it is known, or T.
+ *   table_dev the plan's (delta, u), [H][s][2].
  *   near_dev  as plsh_packed_fwd; bf16 with max_new > 16 needs it.
  *   max_window  at least the longest block of the plan (the largest of
  *             plsh_window's bmax_dev), at most max_len.
@@ -579,9 +580,10 @@ PLSH_API size_t plsh_paged_scratch_bytes(int T, int S, int max_new, int H_kv, in
 PLSH_API int plsh_paged_fwd(const void* Q, int64_t q_token, int64_t q_head, int dtype, int T, int S,
                             const int32_t* cu_dev, const int32_t* start_dev, int max_new, int H, int H_kv, int d,
                             const void* k_pages, const void* v_pages, const int8_t* k_exp, const int8_t* v_exp,
-                            const int32_t* page_table_dev, int table_width, int num_pages, int page_size, int s, int max_len,
-                            const int32_t* tile_span_dev, const void* bmask_dev, const uint8_t* near_dev, int max_window, void* scratch_dev,
-                            size_t scratch_bytes, void* O, float* row_sum, uint32_t* err_dev, void* stream);
+                            const int32_t* page_table_dev, int table_width, int num_pages, int page_size, int s,
+                            int max_len, const double* table_dev, const int32_t* tile_span_dev, const void* bmask_dev,
+                            const uint8_t* near_dev, int max_window, void* scratch_dev, size_t scratch_bytes, void* O,
+                            float* row_sum, uint32_t* err_dev, void* stream);
 
 #ifdef __cplusplus
 }
