@@ -99,7 +99,7 @@ def _load() -> ctypes.CDLL:
     lib.plsh_cache_read.argtypes = [vp, vp, vp, vp, vp, i32, i32, i32, i32, i32, vp, vp, i32, i32, i32, vp, vp, vp, vp]
     lib.plsh_paged_fwd.restype = i32
     lib.plsh_paged_fwd.argtypes = [vp, i64, i64, i32, i32, i32, vp, vp, i32, i32, i32, i32, vp, vp, vp, vp, vp, i32, i32,
-                                   i32, i32, i32, vp, vp, vp, vp, i32, vp, ctypes.c_size_t, vp, vp, vp, vp]
+                                   i32, i32, i32, vp, vp, vp, vp, vp, vp, ctypes.c_size_t, vp, vp, vp, vp]
     lib.plsh_paged_scratch_bytes.restype = ctypes.c_size_t
     lib.plsh_paged_scratch_bytes.argtypes = [i32, i32, i32, i32, i32, i32]
     return lib
@@ -322,16 +322,19 @@ def plsh_cache_read(k_pages, v_pages, k_exp, v_exp, page_table_dev, cu_dev, star
 
 
 def plsh_paged_fwd(Q, dtype: int, cu_dev, start_dev, max_new: int, H: int, H_kv: int, d: int, k_pages, v_pages, k_exp,
-                   v_exp, page_table_dev, s: int, max_len: int, table_dev, tile_span_dev, bmask_dev, near_dev, max_window: int,
-                   scratch_dev, O, row_sum, err_dev, stream=None) -> None:
+                   v_exp, page_table_dev, s: int, max_len: int, table_dev, tile_span_dev, bmask_dev, near_dev,
+                   windows_host: np.ndarray, scratch_dev, O, row_sum, err_dev, stream=None) -> None:
     """Q [T][H][d], any strides with contiguous rows, against pages [num_pages][H_kv][page_size][d]."""
     nbytes = 0 if scratch_dev is None else scratch_dev.numel() * scratch_dev.element_size()
+    if windows_host.dtype != np.int32 or windows_host.shape != (H,) or not windows_host.flags.c_contiguous:
+        raise ValueError("windows_host must be a contiguous int32 array [H]")
     _check(_lib.plsh_paged_fwd(*_rows_arg(Q, "Q"), dtype, Q.shape[0], cu_dev.shape[0] - 1, _dev_ptr(cu_dev, "cu_dev"),
                                _dev_ptr(start_dev, "start_dev"), max_new, H, H_kv, d, _dev_ptr(k_pages, "k_pages"),
                                _dev_ptr(v_pages, "v_pages"), _dev_ptr(k_exp, "k_exp"), _dev_ptr(v_exp, "v_exp"),
                                _dev_ptr(page_table_dev, "page_table_dev"), page_table_dev.shape[1], k_pages.shape[0],
                                k_pages.shape[2], s, max_len, _dev_ptr(table_dev, "table_dev"), _dev_ptr(tile_span_dev, "tile_span_dev"),
-                               _dev_ptr(bmask_dev, "bmask_dev"), _dev_ptr(near_dev, "near_dev"), max_window,
+                               _dev_ptr(bmask_dev, "bmask_dev"), _dev_ptr(near_dev, "near_dev"),
+                               windows_host.ctypes.data_as(ctypes.c_void_p),
                                _dev_ptr(scratch_dev, "scratch_dev"), ctypes.c_size_t(nbytes), _dev_ptr(O, "O"),
                                _dev_ptr(row_sum, "row_sum"), _dev_ptr(err_dev, "err_dev"), _stream_ptr(stream)))
 

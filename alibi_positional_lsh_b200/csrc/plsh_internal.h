@@ -124,6 +124,7 @@ struct ServeArgs {
   const double* table;                      // [H][s][2]; the row kernel's
   // paged bf16: sequences with at most this many new tokens are the row kernel's, the others the tile kernel's (0: all theirs)
   int few;
+  const int32_t* windows_host;              // [H], host: the heads' longest blocks
   void* scratch; int max_window;            // e4m3 pages: serve_scratch_bytes for the tile kernel's sequences
   int kv_rows, kv_pad;                      // rows of K and V, set by the launcher
   void* O; float* row_sum; uint32_t* err;

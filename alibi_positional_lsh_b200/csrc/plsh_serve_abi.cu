@@ -154,7 +154,8 @@ extern "C" int plsh_paged_fwd(const void* Q, int64_t q_token, int64_t q_head, in
                               const int32_t* start_dev, int max_new, int H, int H_kv, int d, const void* k_pages,
                               const void* v_pages, const int8_t* k_exp, const int8_t* v_exp, const int32_t* page_table_dev,
                               int table_width, int num_pages, int page_size, int s, int max_len, const double* table_dev,
-                              const int32_t* tile_span_dev, const void* bmask_dev, const uint8_t* near_dev, int max_window,
+                              const int32_t* tile_span_dev, const void* bmask_dev, const uint8_t* near_dev,
+                              const int32_t* windows_host,
                               void* scratch_dev, size_t scratch_bytes, void* O, float* row_sum, uint32_t* err_dev,
                               void* stream) {
   const char* fn = "plsh_paged_fwd";
@@ -164,8 +165,13 @@ extern "C" int plsh_paged_fwd(const void* Q, int64_t q_token, int64_t q_head, in
   if (int rc = plsh::check_pages(fn, k_pages, v_pages, k_exp, v_exp, page_table_dev, table_width, num_pages, page_size)) return rc;
   if (int rc = plsh::check_plan(fn, s, tile_span_dev, bmask_dev, O, row_sum, err_dev)) return rc;
   if (!table_dev || !start_dev) return fail(PLSH_ERR_INVALID_ARG, "%s: null pointer", fn);
-  if (max_window < 1 || max_window > max_len)
-    return fail(PLSH_ERR_INVALID_ARG, "%s: need 1 <= max_window <= max_len (max_window=%d)", fn, max_window);
+  if (!windows_host) return fail(PLSH_ERR_INVALID_ARG, "%s: null pointer", fn);
+  int max_window = 0;
+  for (int h = 0; h < H; ++h) {
+    if (windows_host[h] < 1 || windows_host[h] > max_len)
+      return fail(PLSH_ERR_INVALID_ARG, "%s: need 1 <= windows_host[h] <= max_len (%d for head %d)", fn, windows_host[h], h);
+    if (windows_host[h] > max_window) max_window = windows_host[h];
+  }
   const bool tiles = dtype == PLSH_BF16 && max_new > plsh::kFewTokens;
   if (tiles && (!near_dev || !plsh::aligned16(near_dev)))
     return fail(PLSH_ERR_INVALID_ARG, "%s: bf16 with max_new > %d needs near_dev, 16-byte aligned", fn, plsh::kFewTokens);
@@ -182,6 +188,7 @@ extern "C" int plsh_paged_fwd(const void* Q, int64_t q_token, int64_t q_head, in
   a.table = table_dev;
   a.scratch = scratch_dev;
   a.max_window = max_window;
+  a.windows_host = windows_host;
   a.pg = plsh::pages(k_pages, v_pages, k_exp, v_exp, page_table_dev, table_width, num_pages, page_size, H_kv);
   a.sq = {cu_dev, start_dev, S, T, max_len, max_new};
   a.dtype = dtype; a.H = H; a.H_kv = H_kv; a.d = d; a.s = s;

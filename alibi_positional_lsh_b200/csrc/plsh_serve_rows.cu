@@ -2,13 +2,13 @@
 //
 // Rows are the (token, query head) pairs that share a KV head, up to 16 in a block; their keys are the
 // window below them, so the work is reading K and V once: 2 (d + 1) bytes a key and KV head when the pages
-// hold e4m3. A cluster of blocks shares one window, four warps a block, each taking steps of 16 keys:
-//   S[16 rows][16 keys] = Q K^T   8 d/16 x 2 products mma.m16n8k16 per step, fp32 accumulation
+// hold e4m3. One to eight blocks share a window, by its width, four warps a block, each taking steps of 16 keys on its own:
+//   S[16 rows][16 keys] = Q K^T   d/16 x 2 products mma.m16n8k16 per step, fp32 accumulation
 //   P = c 2^(S sc - m), against the warp's own running maximum m over keys with c > 0
 //   O[16 rows][d] += P V
-// and the partial rows (m, l, O) meet in shared memory at the end, each block of the cluster joining its share
-// of the rows from all blocks' (distributed shared memory): one launch, no scratch, and always in the
-// same order, so results do not depend on timing.
+// and the partial rows (m, l, O) meet at the end, the warps' in shared memory and the blocks' across it (eight blocks
+// are a cluster: one wide window's, or two, four or eight narrower ones'): one launch, no scratch, and always
+// joined in the same order, so results do not depend on timing.
 //
 // K and V go from the pages to registers, 16 bytes at a time, and are not staged: a dot product may take its d in any order, so
 // lane (g, t) of a warp takes bytes 16 t .. 16 t + 15 of each 64 of key g's row as its operand of four products, and Q is
@@ -37,13 +37,23 @@ namespace cg = cooperative_groups;
 using namespace serve;
 
 constexpr int kThreads = 128, kWarps = 4, kRowsMax = 16, kStep = 16;
-constexpr int kChunk = 256;      // keys whose rows, exponents and counts a block holds at a time
+constexpr int kCluster = 8;
+constexpr int kChunkSteps = 64;  // steps whose pages a block holds at a time
+constexpr int kMaxSplitHeads = 64;
 constexpr int kMaxGroup = 16;    // query heads of a block (a larger group takes several blocks)
+
+// How a launch's windows are dealt out: 2^lg[kv head] blocks of each (with more KV heads, lg_all), kv heads from the last.
+struct Split {
+  int tokens, heads, row_blocks, head_blocks;  // of a block; blocks of a sequence's rows and of a group's heads
+  int per_head;                                // windows of a KV head: sequences x row blocks x head blocks
+  int lg_all;
+  uint8_t lg[kMaxSplitHeads];
+};
 
 // Shared memory of a block for `heads` query heads and `rows` rows.
 template <int D, typename MaskT>
 struct Layout {
-  int o, ml, begin, keep, row_off, tail, row, ks, vs, total;
+  int o, ml, begin, keep, row_off, tail, page, row, ks, vs, total;
   __host__ __device__ Layout(int heads, int rows) {
     int at = 0;
     auto take = [&](int bytes) {
@@ -54,12 +64,13 @@ struct Layout {
     o = take(kWarps * rows * (D + 4) * 4);         // [warp][row][D + 4]: the warps' rows of O
     ml = take(2 * kWarps * rows * 4);              // [2][warp][row]: their m and l
     begin = take(heads * PLSH_MAX_S * 4);          // [head][hash]: where p0's block begins
-    keep = take(heads * kChunk * (int)sizeof(MaskT));   // [head][key]: hashes whose block reaches the key
+    keep = take(kWarps * heads * kStep * (int)sizeof(MaskT));  // [warp][head][key]: hashes whose block reaches the key
     row_off = take(rows * (int)sizeof(MaskT));     // [row]: hashes that open a block in (p0, i]
     tail = take(heads * kStep * (int)sizeof(MaskT));    // [head][k]: masks of positions p0 + 1 + k
-    row = take((kChunk + kStep) * 8);              // [key]: its row in the pages (-1: none)
-    ks = take((kChunk + kStep) * 4);               // [key]: 2^exponent of K and of V
-    vs = take((kChunk + kStep) * 4);
+    page = take((kChunkSteps + 2) * 4);            // pages of the chunk's positions (they hold 16 and more)
+    row = take(2 * kWarps * kStep * 8);            // [stage][warp][key]: its row in the pages (-1: none)
+    ks = take(2 * kWarps * kStep * 4);             // the same: 2^exponent of K and of V
+    vs = take(2 * kWarps * kStep * 4);
     total = at;
   }
 };
@@ -112,26 +123,43 @@ __device__ __forceinline__ float bf16_hi(uint32_t x) { return __uint_as_float(x 
 
 template <int D, typename MaskT, bool kQuant>
 __global__ void __launch_bounds__(kThreads, D == 128 && !kQuant ? 2 : 3)
-serve_rows_kernel(ServeArgs a, int tokens, int heads, int row_blocks, int head_blocks) {
+serve_rows_kernel(ServeArgs a, Split sp) {
   extern __shared__ __align__(16) uint8_t smem_raw[];
   cg::cluster_group cluster = cg::this_cluster();
-  const int C = static_cast<int>(cluster.num_blocks()), rank = static_cast<int>(cluster.block_rank());
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31, g = lane >> 2, t = lane & 3;
   if (blockIdx.x == 0) check_seqs(a.sq, a.err);
 
-  // KV heads from the last (with the usual slopes, the widest windows first), then sequences, then row blocks
-  int x = blockIdx.x / C;
-  const int hb = x % head_blocks;
-  x /= head_blocks;
-  const int rb = x % row_blocks;
-  x /= row_blocks;
-  const int sid = x % a.sq.S, kvh = a.H_kv - 1 - x / a.sq.S;
+  // KV heads from the last (with the usual slopes, the widest windows first), a KV head's windows 8 / C to a cluster
+  const int cl = blockIdx.x / kCluster, in_cl = blockIdx.x % kCluster;
+  int kvh, lg = sp.lg_all, x;
+  if (a.H_kv > kMaxSplitHeads) {
+    const int per = (sp.per_head << lg) / kCluster + ((sp.per_head << lg) % kCluster != 0);
+    kvh = a.H_kv - 1 - cl / per;
+    x = cl % per;
+  } else {
+    x = cl;
+    for (kvh = a.H_kv - 1; kvh > 0; --kvh) {
+      lg = sp.lg[kvh];
+      const int per = ((sp.per_head << lg) + kCluster - 1) / kCluster;
+      if (x < per) break;
+      x -= per;
+    }
+    lg = sp.lg[kvh];
+  }
+  const int C = 1 << lg, rank = in_cl & (C - 1), rank0 = in_cl - rank;  // the window's blocks are rank0 .. rank0 + C - 1 of the cluster
+  x = (x << (3 - lg)) + (in_cl >> lg);                                  // the window's number within the KV head
+  const int tokens = sp.tokens, heads = sp.heads;
+  const int hb = x % sp.head_blocks;
+  x /= sp.head_blocks;
+  const int rb = x % sp.row_blocks, sid = x / sp.row_blocks;
   const int G = a.H / a.H_kv, h0 = kvh * G + hb * heads, nh = min(heads, G - hb * heads);
-  const Seq sq = load_seq(a.sq, sid);
+  Seq sq{};
+  if (sid < a.sq.S) sq = load_seq(a.sq, sid);
   const int first = rb * tokens;                              // the block's first token in the sequence
   const int nt = min(tokens, sq.len - first);
-  // (longer sequences are the tile kernel's)
-  if (nt <= 0 || sq.len > a.few) return;                      // the whole cluster returns
+  // nothing here (or a longer sequence, the tile kernel's): the cluster's barriers do not wait for a block that has ended, and
+  // nobody reads its memory
+  if (sid >= a.sq.S || nt <= 0 || sq.len > a.few) return;
   const int rows = nt * nh, p0 = sq.pos0 + first, c0 = sq.c0 + first;
   const MaskT* bmask = static_cast<const MaskT*>(a.bmask);
   const int max_rows = tokens * heads;  // of any block of the launch, alike for the whole cluster
@@ -145,9 +173,12 @@ serve_rows_kernel(ServeArgs a, int tokens, int heads, int row_blocks, int head_b
   long long* const s_row = reinterpret_cast<long long*>(smem_raw + at_.row);
   float* const s_ks = reinterpret_cast<float*>(smem_raw + at_.ks);
   float* const s_vs = reinterpret_cast<float*>(smem_raw + at_.vs);
+  int* const s_page = reinterpret_cast<int*>(smem_raw + at_.page);
 
   // where the blocks of p0 begin, and so the window; masks above p0
   int lo = p0;
+  for (int e = tid; e < nh * PLSH_MAX_S; e += kThreads) s_begin[e] = 0x7fffffff;
+  __syncthreads();
   for (int e = tid; e < nh * a.s; e += kThreads) {
     const int h = e / a.s, k = e % a.s;
     const int b = block_begin(Binning::from_table(a.table + (static_cast<size_t>(h0 + h) * a.s + k) * 2), p0);
@@ -232,17 +263,8 @@ serve_rows_kernel(ServeArgs a, int tokens, int heads, int row_blocks, int head_b
   MaskT mine[2] = {0, 0};  // of rows g and g + 8: the hashes that may count, and the row's head in the group
   int hh[2] = {0, 0};
 
-  // rows, exponents of keys j(k), k = 0 .. n - 1, into places at ..
-  auto describe = [&](int at, int k, int j, bool on) {
-    long long row = -1;
-    if (on) row = page_row(a.pg, sid, j, kvh, a.err);
-    s_row[at + k] = row;
-    if (kQuant) {
-      s_ks[at + k] = row >= 0 ? pow2(a.pg.k_exp[row]) : 0.0f;
-      s_vs[at + k] = row >= 0 ? pow2(a.pg.v_exp[row]) : 0.0f;
-    }
-  };
-
+  // places of this warp's step in flight
+  auto place = [&](int stage) { return (stage * kWarps + warp) * kStep; };
   // one step: 16 keys at places at .. of sm.row;
   // byte n of c4[u]: the count of row g + 8 u with key 2 t, 2 t + 1, 2 t + 8 or 2 t + 9
   auto load_k = [&](int at, uint4 (&kr)[2][D / 64][kQuant ? 1 : 2]) {
@@ -353,7 +375,6 @@ serve_rows_kernel(ServeArgs a, int tokens, int heads, int row_blocks, int head_b
     }
   };
 
-  // ---- the keys above p0, one step of block 0's first warp
   __syncthreads();
 #pragma unroll
   for (int u = 0; u < 2; ++u) {
@@ -363,13 +384,29 @@ serve_rows_kernel(ServeArgs a, int tokens, int heads, int row_blocks, int head_b
       hh[u] = r % nh;
     }
   }
+  // exponents of the rows at places at ..: lanes 0 .. 15 K's, 16 .. 31 V's
+  auto exponents = [&](int at) {
+    if (kQuant) {
+      const long long row = s_row[at + (lane & 15)];
+      return row >= 0 ? pow2((lane < 16 ? a.pg.k_exp : a.pg.v_exp)[row]) : 0.0f;
+    }
+    return 0.0f;
+  };
+  auto put_exponents = [&](int at, float e) {
+    if (kQuant) (lane < 16 ? s_ks : s_vs)[at + (lane & 15)] = e;
+  };
+
+  // ---- the keys above p0, one step of the first block's first warp
   if (rank == 0 && warp == 0 && nt > 1) {
-    if (lane < kStep) describe(kChunk, lane, p0 + 1 + lane, lane + 1 < nt);
+    const int at = place(0);
+    if (lane < kStep) s_row[at + lane] = lane + 1 < nt ? page_row(a.pg, sid, p0 + 1 + lane, kvh, a.err) : -1;
     __syncwarp();
     uint4 kr[2][D / 64][kQuant ? 1 : 2];
     uint32_t vr[4][kVWords];
-    load_k(kChunk, kr);
-    load_v(kChunk, vr);
+    load_k(at, kr);
+    load_v(at, vr);
+    put_exponents(at, exponents(at));
+    __syncwarp();
     uint32_t c[2] = {0, 0};
 #pragma unroll
     for (int u = 0; u < 2; ++u) {
@@ -384,59 +421,91 @@ serve_rows_kernel(ServeArgs a, int tokens, int heads, int row_blocks, int head_b
         }
       }
     }
-    step(kChunk, kr, vr, c);
+    step(at, kr, vr, c);
+    __syncwarp();
   }
 
-  // ---- the window, kChunk keys at a time
-  for (int b = s0; b < s1; b += kChunk / kStep) {
-    const int ns = min(kChunk / kStep, s1 - b);
+  // ---- the window
+  MaskT* const keep = s_keep + warp * heads * kStep;
+  for (int b = s0; b < s1; b += kChunkSteps) {
+    const int ns = min(kChunkSteps, s1 - b);
+    const int slot0 = max(lo, p0 - kStep * (b + ns) + 1) >> a.pg.lg_page, slots = ((p0 - kStep * b) >> a.pg.lg_page) - slot0 + 1;
     __syncthreads();
-    // key at place k of the chunk: p0 - 16 b - k, steps downward; within a step of 16 places ascending order does not matter
-    for (int k = tid; k < ns * kStep; k += kThreads) {
-      const int j = p0 - kStep * b - k;
-      describe(0, k, j, j >= lo);
-    }
-    // the hashes whose block reaches the key, per head
-    for (int k = tid; k < ns * kStep; k += kThreads) {
-      const int j = p0 - kStep * b - k;
-      for (int h = 0; h < nh; ++h) {
-        MaskT v = 0;
-        const int* begin = s_begin + h * PLSH_MAX_S;
-#pragma unroll 4
-        for (int i = 0; i < a.s; ++i) v |= static_cast<MaskT>(begin[i] <= j) << i;
-        s_keep[h * kChunk + k] = v;
+    for (int k = tid; k < slots; k += kThreads) {
+      int page = slot0 + k < a.pg.width ? a.pg.table[static_cast<long long>(sid) * a.pg.width + slot0 + k] : -1;
+      if (page < 0 || page >= a.pg.num_pages) {
+        atomicOr(a.err, PLSH_DEVERR_PAGE);
+        page = -1;
       }
+      s_page[k] = page;
     }
     __syncthreads();
-    // a warp's steps, the next one's rows on their way while this one is computed
-    auto counts = [&](int i, uint32_t (&c)[2]) {
+    // Step i of the chunk: rows and counts of its keys into the stage's places. False: nothing has weight there. Key k of
+    // the step is p0 - 16 (b + i) - k; a lane per hash says which hashes' blocks reach it.
+    auto describe = [&](int i, int stage, uint32_t (&c)[2]) {
+      const int at = place(stage), j0 = p0 - kStep * (b + i);
+      __syncwarp();
+      if (lane < kStep) {
+        const int j = j0 - lane;
+        long long row = -1;
+        if (j >= lo) {
+          const int page = s_page[(j >> a.pg.lg_page) - slot0];
+          if (page >= 0)
+            row = ((static_cast<long long>(page) * a.pg.H_kv + kvh) << a.pg.lg_page) + (j & ((1 << a.pg.lg_page) - 1));
+        }
+        s_row[at + lane] = row;
+      }
+      for (int h = 0; h < nh; ++h) {
+        const int b0 = s_begin[h * PLSH_MAX_S + lane];
+        const int b1 = sizeof(MaskT) == 8 ? s_begin[h * PLSH_MAX_S + 32 + lane] : 0;
+        MaskT v = 0;
+#pragma unroll
+        for (int k = 0; k < kStep; ++k) {
+          MaskT m = static_cast<MaskT>(__ballot_sync(0xffffffffu, b0 <= j0 - k));
+          if (sizeof(MaskT) == 8) m |= static_cast<MaskT>(static_cast<unsigned long long>(__ballot_sync(0xffffffffu, b1 <= j0 - k)) << 32);
+          if (lane == k) v = m;
+        }
+        if (lane < kStep) keep[h * kStep + lane] = v;
+      }
+      __syncwarp();
 #pragma unroll
       for (int u = 0; u < 2; ++u) {
         c[u] = 0;
 #pragma unroll
         for (int n = 0; n < 4; ++n) {
-          const int k = kStep * i + 2 * t + (n & 1) + 8 * (n >> 1);
-          if (s_row[k] >= 0) c[u] |= static_cast<uint32_t>(popc_mask<MaskT>(static_cast<MaskT>(s_keep[hh[u] * kChunk + k] & mine[u]))) << (8 * n);
+          const int k = 2 * t + (n & 1) + 8 * (n >> 1);
+          if (s_row[at + k] >= 0) c[u] |= static_cast<uint32_t>(popc_mask<MaskT>(static_cast<MaskT>(keep[hh[u] * kStep + k] & mine[u]))) << (8 * n);
         }
       }
-      return __any_sync(0xffffffffu, (c[0] | c[1]) != 0) != 0;  // else nothing has weight there
+      return __any_sync(0xffffffffu, (c[0] | c[1]) != 0) != 0;
     };
+    // a warp's steps, the next one's K on its way while this one is computed
     uint4 kr[2][D / 64][kQuant ? 1 : 2];
     uint32_t c[2];
-    int i = warp;
-    while (i < ns && !counts(i, c)) i += kWarps;
-    if (i < ns) load_k(kStep * i, kr);
+    int i = warp, stage = 0;
+    while (i < ns && !describe(i, stage, c)) i += kWarps;
+    float ex = 0.0f;
+    if (i < ns) {
+      load_k(place(stage), kr);
+      ex = exponents(place(stage));
+    }
     while (i < ns) {
       uint32_t vr[4][kVWords];
-      load_v(kStep * i, vr);
+      load_v(place(stage), vr);
+      put_exponents(place(stage), ex);
       int nx = i + kWarps;
       uint32_t cn[2];
-      while (nx < ns && !counts(nx, cn)) nx += kWarps;
+      while (nx < ns && !describe(nx, stage ^ 1, cn)) nx += kWarps;
       uint4 kn[2][D / 64][kQuant ? 1 : 2];
-      if (kQuant && nx < ns) load_k(kStep * nx, kn);
-      step(kStep * i, kr, vr, c);
-      if (!kQuant && nx < ns) load_k(kStep * nx, kn);  // (rows of bf16 take twice the registers)
+      if (kQuant && nx < ns) {
+        load_k(place(stage ^ 1), kn);
+        ex = exponents(place(stage ^ 1));
+      }
+      __syncwarp();
+      step(place(stage), kr, vr, c);
+      if (!kQuant && nx < ns) load_k(place(stage ^ 1), kn);  // (rows of bf16 take twice the registers)
       i = nx;
+      stage ^= 1;
       c[0] = cn[0];
       c[1] = cn[1];
 #pragma unroll
@@ -466,37 +535,60 @@ serve_rows_kernel(ServeArgs a, int tokens, int heads, int row_blocks, int head_b
       s_o[(warp * max_rows + r) * (D + 4) + (D / 8) * (2 * t + 1) + i] = o[i][2 * u + 1];
     }
   }
-  cluster.sync();
-  for (int e = rank * kThreads + tid; e < rows * (D / 4); e += C * kThreads) {
+  __syncthreads();
+  // the block's warps, into the first one's place
+  for (int e = tid; e < rows * (D / 4); e += kThreads) {
     const int r = e / (D / 4), col = e % (D / 4) * 4;
-    float top = -INFINITY;
-    for (int b = 0; b < C; ++b) {
-      const float* ml = cluster.map_shared_rank(s_ml, b);
+    float top = -INFINITY, total = 0.0f, acc[4] = {0.0f, 0.0f, 0.0f, 0.0f};
 #pragma unroll
-      for (int w = 0; w < kWarps; ++w) top = fmaxf(top, ml[w * max_rows + r]);
-    }
-    float total = 0.0f, acc[4] = {0.0f, 0.0f, 0.0f, 0.0f};
-    for (int b = 0; b < C; ++b) {
-      const float* ml = cluster.map_shared_rank(s_ml, b);
-      const float* ro = cluster.map_shared_rank(s_o, b);
+    for (int w = 0; w < kWarps; ++w) top = fmaxf(top, s_ml[w * max_rows + r]);
 #pragma unroll
-      for (int w = 0; w < kWarps; ++w) {
-        const float f = exp2f(ml[w * max_rows + r] - top);  // 0 for a warp without keys
-        if (f > 0.0f) {
-          total += ml[(kWarps + w) * max_rows + r] * f;
-          const float4 v = *reinterpret_cast<const float4*>(ro + (w * max_rows + r) * (D + 4) + col);
-          acc[0] += v.x * f;
-          acc[1] += v.y * f;
-          acc[2] += v.z * f;
-          acc[3] += v.w * f;
-        }
-      }
+    for (int w = 0; w < kWarps; ++w) {
+      const float mw = s_ml[w * max_rows + r];
+      const float f = mw == -INFINITY ? 0.0f : exp2f(mw - top);  // -inf: a warp without keys
+      const float4 v = *reinterpret_cast<const float4*>(s_o + (w * max_rows + r) * (D + 4) + col);
+      total += s_ml[(kWarps + w) * max_rows + r] * f;
+      acc[0] += v.x * f;
+      acc[1] += v.y * f;
+      acc[2] += v.z * f;
+      acc[3] += v.w * f;
     }
+    *reinterpret_cast<float4*>(s_o + r * (D + 4) + col) = make_float4(acc[0], acc[1], acc[2], acc[3]);
+    if (col == 0) *reinterpret_cast<float2*>(s_o + r * (D + 4) + D) = make_float2(top, total);  // behind the row
+  }
+  auto finish = [&](int r, int col, float top, float total, const float (&acc)[4]) {
     const float inv = 1.0f / total;
     const size_t at = static_cast<size_t>(c0 + r / nh) * a.H + h0 + r % nh;
     const float out[4] = {acc[0] * inv, acc[1] * inv, acc[2] * inv, acc[3] * inv};
     store4f(static_cast<__nv_bfloat16*>(a.O) + at * D + col, out);
     if (col == 0) a.row_sum[at] = (log2f(total) + top) * 0.6931471805599453f - logf(static_cast<float>(a.s));
+  };
+  cluster.sync();
+  // the window's blocks, each joining its share of the elements
+  for (int e = rank + C * tid; e < rows * (D / 4); e += C * kThreads) {
+    const int r = e / (D / 4), col = e % (D / 4) * 4;
+    float2 ml[kCluster];
+    float4 v[kCluster];
+    float top = -INFINITY, total = 0.0f, acc[4] = {0.0f, 0.0f, 0.0f, 0.0f};
+#pragma unroll
+    for (int b = 0; b < kCluster; ++b) {
+      if (b >= C) break;
+      const float* ro = cluster.map_shared_rank(s_o, rank0 + b) + r * (D + 4);
+      ml[b] = *reinterpret_cast<const float2*>(ro + D);
+      v[b] = *reinterpret_cast<const float4*>(ro + col);
+      top = fmaxf(top, ml[b].x);
+    }
+#pragma unroll
+    for (int b = 0; b < kCluster; ++b) {
+      if (b >= C) break;
+      const float f = ml[b].x == -INFINITY ? 0.0f : exp2f(ml[b].x - top);
+      total += ml[b].y * f;
+      acc[0] += v[b].x * f;
+      acc[1] += v[b].y * f;
+      acc[2] += v[b].z * f;
+      acc[3] += v[b].w * f;
+    }
+    finish(r, col, top, total, acc);
   }
   cluster.sync();  // the others have read this block's rows
 }
@@ -504,32 +596,54 @@ serve_rows_kernel(ServeArgs a, int tokens, int heads, int row_blocks, int head_b
 template <int D, typename MaskT, bool kQuant>
 int launch(const ServeArgs& a, cudaStream_t st) {
   const int G = a.H / a.H_kv;
-  const int heads = G < kMaxGroup ? G : kMaxGroup, head_blocks = ceil_div(G, heads);
   const int most = a.sq.max_new < a.few ? a.sq.max_new : a.few;
-  const int tokens = most < kRowsMax / heads ? most : kRowsMax / heads;
-  const int row_blocks = ceil_div(most, tokens);
-  const long long items = static_cast<long long>(a.sq.S) * a.H_kv * head_blocks * row_blocks;
-  // blocks of a window: up to the portable eight, as long as the machine has room for more, and no more than two steps a warp
-  int C = 1;
-  while (C < 8 && items * C < 4 * 148 && 2 * C * kWarps * kStep < a.max_window) C *= 2;
-  if (items * C > 0x7fffffffLL) return fail(PLSH_ERR_RANGE, "plsh_paged_fwd: too many rows");
+  Split sp{};
+  sp.heads = G < kMaxGroup ? G : kMaxGroup;
+  sp.head_blocks = ceil_div(G, sp.heads);
+  sp.tokens = most < kRowsMax / sp.heads ? most : kRowsMax / sp.heads;
+  sp.row_blocks = ceil_div(most, sp.tokens);
+  const long long per_head = static_cast<long long>(a.sq.S) * sp.row_blocks * sp.head_blocks;
+  if (per_head * kCluster * a.H_kv > 0x7fffffffLL) return fail(PLSH_ERR_RANGE, "plsh_paged_fwd: too many rows");
+  sp.per_head = static_cast<int>(per_head);
+  // Blocks of a window: one for each `keys` keys of the widest head's longest block, 64 (a step a warp) while the launch then has
+  // up to four blocks an SM, else the fewest doublings that come near it.
+  long long clusters = 0;
+  for (int keys = kWarps * kStep; keys <= 4096; keys *= 2) {
+    clusters = 0;
+    long long blocks = 0;
+    for (int k = 0; k < a.H_kv; ++k) {
+      int w = 1;
+      for (int h = 0; h < G; ++h) {
+        const int x = a.windows_host ? a.windows_host[k * G + h] : a.max_window;
+        w = x > w ? x : w;
+      }
+      int lg = 0;
+      while (lg < 3 && (static_cast<long long>(keys) << lg) < w) ++lg;
+      if (a.H_kv > kMaxSplitHeads) lg = sp.lg_all = lg > sp.lg_all && k > 0 ? lg : k > 0 ? sp.lg_all : lg;
+      else sp.lg[k] = static_cast<uint8_t>(lg);
+      blocks += per_head << lg;
+      clusters += ((per_head << lg) + kCluster - 1) / kCluster;
+    }
+    if (a.H_kv > kMaxSplitHeads) clusters = a.H_kv * (((per_head << sp.lg_all) + kCluster - 1) / kCluster);
+    if (blocks <= 4 * 148) break;
+  }
   auto kern = serve_rows_kernel<D, MaskT, kQuant>;
-  const int smem = Layout<D, MaskT>(heads, tokens * heads).total;
+  const int smem = Layout<D, MaskT>(sp.heads, sp.tokens * sp.heads).total;
   cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
   if (e != cudaSuccess) return cuda_fail(e, "cudaFuncSetAttribute(serve_rows_kernel)");
   cudaLaunchConfig_t cfg{};
-  cfg.gridDim = dim3(static_cast<unsigned>(items * C));
+  cfg.gridDim = dim3(static_cast<unsigned>(clusters * kCluster));
   cfg.blockDim = dim3(kThreads);
   cfg.dynamicSmemBytes = smem;
   cfg.stream = st;
   cudaLaunchAttribute attr{};
   attr.id = cudaLaunchAttributeClusterDimension;
-  attr.val.clusterDim.x = C;
+  attr.val.clusterDim.x = kCluster;
   attr.val.clusterDim.y = 1;
   attr.val.clusterDim.z = 1;
   cfg.attrs = &attr;
   cfg.numAttrs = 1;
-  e = cudaLaunchKernelEx(&cfg, kern, a, tokens, heads, row_blocks, head_blocks);
+  e = cudaLaunchKernelEx(&cfg, kern, a, sp);
   return e == cudaSuccess ? PLSH_OK : cuda_fail(e, "serve_rows_kernel launch");
 }
 

@@ -259,7 +259,9 @@ class PlshServing(_Errors):
                 self.near = torch.empty((H, max_len, 64), dtype=torch.uint8, device=self.device)
                 plsh_near_counts(self.bmask, H, s, max_len, self.near)
             self.check()  # waits for the plan, so that any stream may use it from here on
-            self.max_window = int(self.bmax.max().item())  # the longest block
+            self.windows_host = self.bmax.cpu().numpy()  # the heads' longest blocks
+        self.max_window = int(self.windows_host.max())
+        self._windows = self.windows_host.ctypes.data
         self._code, self._err = _CODES[dtype], self.err.data_ptr()
         self._table = self.table_dev.data_ptr()
         self._plan = self.spans.data_ptr(), self.bmask.data_ptr(), 0 if self.near is None else self.near.data_ptr()
@@ -321,7 +323,7 @@ class PlshServing(_Errors):
                     if need:
                         scratch = _empty((need,), torch.uint8, dev, stream)
                 _check(_lib.plsh_paged_fwd(*qr, self._code, T, S, cu, st, most, self.H, self.H_kv, self.d, *cache._pages, pt, width,
-                                           cache.num_pages, cache.page_size, self.s, self.max_len, self._table, *self._plan, self.max_window,
+                                           cache.num_pages, cache.page_size, self.s, self.max_len, self._table, *self._plan, self._windows,
                                            scratch.data_ptr() if need else 0, need, O.data_ptr(), row_sum.data_ptr(), self._err,
                                            _stream(stream, dev)))
         return O, row_sum

@@ -569,10 +569,10 @@ PLSH_API int plsh_cache_read(const void* k_pages, const void* v_pages, const int
  *             so give the largest length where it is known, or T.
  *   table_dev the plan's (delta, u), [H][s][2].
  *   near_dev  as plsh_packed_fwd; bf16 with max_new > 16 needs it.
- *   max_window  at least the longest block of the plan (the largest of
- *             plsh_window's bmax_dev), at most max_len.
+ *   windows_host  [H] int32 on the host: each head's longest block, plsh_window's
+ *             bmax_dev (a copy, made once with the plan).
  *   scratch_dev, scratch_bytes  device scratch of at least
- *             plsh_paged_scratch_bytes(...) bytes, 16-byte aligned (NULL where that is 0, with pages of the call's dtype, and for fp32):
+ *             plsh_paged_scratch_bytes(.., the largest of windows_host) bytes, 16-byte aligned (NULL where that is 0, with pages of the call's dtype, and for fp32):
  *             bf16 copies of the e4m3 rows that sequences with more than 16
  *             new tokens reach. Nothing in it needs clearing.
  */
@@ -582,8 +582,8 @@ PLSH_API int plsh_paged_fwd(const void* Q, int64_t q_token, int64_t q_head, int 
                             const void* k_pages, const void* v_pages, const int8_t* k_exp, const int8_t* v_exp,
                             const int32_t* page_table_dev, int table_width, int num_pages, int page_size, int s,
                             int max_len, const double* table_dev, const int32_t* tile_span_dev, const void* bmask_dev,
-                            const uint8_t* near_dev, int max_window, void* scratch_dev, size_t scratch_bytes, void* O,
-                            float* row_sum, uint32_t* err_dev, void* stream);
+                            const uint8_t* near_dev, const int32_t* windows_host, void* scratch_dev,
+                            size_t scratch_bytes, void* O, float* row_sum, uint32_t* err_dev, void* stream);
 
 #ifdef __cplusplus
 }

@@ -32,9 +32,9 @@ def _read(kp=FAKE, ke=FAKE, ve=FAKE, width=3, pages=8, page=64, T=10, start=FAKE
 
 
 def _paged(Q=FAKE, qt=512, dtype=0, T=10, S=2, start=FAKE, max_new=10, H=4, H_kv=2, d=128, ke=FAKE, ve=FAKE, page=64, s=20,
-           max_len=100, table=FAKE, near=FAKE, window=50, scratch=FAKE, nbytes=1 << 30, O=FAKE):
+           max_len=100, table=FAKE, near=FAKE, window=50, windows=True, scratch=FAKE, nbytes=1 << 30, O=FAKE):
     return (Q, qt, 128, dtype, T, S, FAKE, start, max_new, H, H_kv, d, FAKE, FAKE, ke, ve, FAKE, 3, 8, page, s, max_len, table, FAKE, FAKE,
-            near, window, scratch, ctypes.c_size_t(nbytes), O, FAKE, FAKE, NULL)
+            near, (ctypes.c_int32 * 8)(window, 9, 9, 9, 9, 9, 9, 9) if windows else NULL, scratch, ctypes.c_size_t(nbytes), O, FAKE, FAKE, NULL)
 
 
 ODD = ctypes.c_void_p((1 << 20) + 8)
@@ -52,7 +52,7 @@ REFUSED = [
                                 (dict(start=NULL), 1), (dict(d=256), 2), (dict(dtype=5), 2), (dict(K=NULL), 1), (dict(K=ODD), 1)]),
     ("plsh_paged_fwd", _paged, [(dict(Q=NULL), 1), (dict(qt=100), 1), (dict(dtype=3), 2), (dict(T=0), 1), (dict(start=NULL), 1), (dict(max_new=0), 1),
                                 (dict(H_kv=3), 1), (dict(d=80), 2), (dict(ve=NULL), 1), (dict(page=20), 2), (dict(s=99), 1), (dict(max_len=0), 1),
-                                (dict(O=NULL), 1), (dict(table=NULL), 1), (dict(max_new=17, near=NULL), 1), (dict(max_new=17, window=101), 1), (dict(max_new=17, window=0), 1),
+                                (dict(O=NULL), 1), (dict(table=NULL), 1), (dict(max_new=17, near=NULL), 1), (dict(window=101), 1), (dict(window=0), 1), (dict(windows=False), 1),
                                 (dict(max_new=17, scratch=NULL), 1), (dict(max_new=17, nbytes=1000), 1)]),
 ]
 
