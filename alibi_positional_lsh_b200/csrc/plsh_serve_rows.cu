@@ -1,18 +1,20 @@
 // T~ of a few new tokens of each sequence (one when decoding) against the paged cache, bf16.
 //
-// Rows are the (token, query head) pairs that share a KV head, up to 16 in a block; their keys are the
+// Rows are the (token, query head) pairs that share a KV head, up to 8 in a block; their keys are the
 // window below them, so the work is reading K and V once: 2 (d + 1) bytes a key and KV head when the pages
-// hold e4m3. One to eight blocks share a window, by its width, four warps a block, each taking steps of 16 keys on its own:
-//   S[16 rows][16 keys] = Q K^T   d/16 x 2 products mma.m16n8k16 per step, fp32 accumulation
+// hold e4m3. One to eight blocks share a window, by its width, eight warps a block, each taking 32 keys at a time, two steps of 16:
+//   S^T[16 keys][8 rows] = K Q^T   d/16 products mma.m16n8k16, fp32 accumulation
 //   P = c 2^(S sc - m), against the warp's own running maximum m over keys with c > 0
-//   O[16 rows][d] += P V
+//   O^T[d][8 rows] += V^T P^T      d/16 products
 // and the partial rows (m, l, O) meet at the end, the warps' in shared memory and the blocks' across it (eight blocks
 // are a cluster: one wide window's, or two, four or eight narrower ones'): one launch, no scratch, and always
 // joined in the same order, so results do not depend on timing.
 //
-// K and V go from the pages to registers, 16 bytes at a time, and are not staged: a dot product may take its d in any order, so
-// lane (g, t) of a warp takes bytes 16 t .. 16 t + 15 of each 64 of key g's row as its operand of four products, and Q is
-// loaded in the same order. For P V it takes columns (d/8) g .. of four keys and pairs them up by key.
+// The rows are the products' narrow side: with them on the wide one (16), half of the products, of O's registers and of
+// the exponentials were padding. K and V go from the pages to registers, 16 bytes at a time, and are not staged: a dot product may
+// take its d in any order, so lane (g, t) of a warp takes bytes 16 t .. 16 t + 15 of each 64 of key g's (and g + 8's) row as
+// its operand of four products, and Q is loaded in the same order. For P V it takes columns (d/8) g .. of four keys and pairs
+// them up by key; P is turned round by a matrix transpose in registers.
 // e4m3 values become f16 exactly (one conversion per pair) for S, with each row of Q scaled by a power of two into f16's range,
 // and bf16 exactly for P V; the rows' exponents multiply S and P, in fp32.
 //
@@ -36,17 +38,19 @@ namespace {
 namespace cg = cooperative_groups;
 using namespace serve;
 
-constexpr int kThreads = 128, kWarps = 4, kRowsMax = 16, kStep = 16;
+constexpr int kThreads = 256, kWarps = 8, kRowsMax = 8, kStep = 32;
 constexpr int kCluster = 8;
-constexpr int kChunkSteps = 64;  // steps whose pages a block holds at a time
+constexpr int kTail = 16;        // places above p0 (a block has at most 8 tokens)
+constexpr int kChunkSteps = 32;  // steps of 32 keys whose pages a block holds at a time
 constexpr int kMaxSplitHeads = 64;
-constexpr int kMaxGroup = 16;    // query heads of a block (a larger group takes several blocks)
+constexpr int kMaxGroup = 8;     // query heads of a block (a larger group takes several blocks)
 
 // How a launch's windows are dealt out: 2^lg[kv head] blocks of each (with more KV heads, lg_all), kv heads from the last.
 struct Split {
   int tokens, heads, row_blocks, head_blocks;  // of a block; blocks of a sequence's rows and of a group's heads
   int per_head;                                // windows of a KV head: sequences x row blocks x head blocks
-  int lg_all;
+  int lg_all, window_all;
+  int window[kMaxSplitHeads];  // the longest block of a KV head's heads
   uint8_t lg[kMaxSplitHeads];
 };
 
@@ -64,10 +68,10 @@ struct Layout {
     o = take(kWarps * rows * (D + 4) * 4);         // [warp][row][D + 4]: the warps' rows of O
     ml = take(2 * kWarps * rows * 4);              // [2][warp][row]: their m and l
     begin = take(heads * PLSH_MAX_S * 4);          // [head][hash]: where p0's block begins
-    keep = take(kWarps * heads * kStep * (int)sizeof(MaskT));  // [warp][head][key]: hashes whose block reaches the key
+    keep = take(2 * kWarps * heads * kStep * (int)sizeof(MaskT));  // [stage][warp][head][key]: hashes whose block reaches the key
     row_off = take(rows * (int)sizeof(MaskT));     // [row]: hashes that open a block in (p0, i]
-    tail = take(heads * kStep * (int)sizeof(MaskT));    // [head][k]: masks of positions p0 + 1 + k
-    page = take((kChunkSteps + 2) * 4);            // pages of the chunk's positions (they hold 16 and more)
+    tail = take(heads * kTail * (int)sizeof(MaskT));    // [head][k]: masks of positions p0 + 1 + k
+    page = take((2 * kChunkSteps + 2) * 4);            // pages of the chunk's positions (they hold 16 and more)
     row = take(2 * kWarps * kStep * 8);            // [stage][warp][key]: its row in the pages (-1: none)
     ks = take(2 * kWarps * kStep * 4);             // the same: 2^exponent of K and of V
     vs = take(2 * kWarps * kStep * 4);
@@ -91,13 +95,24 @@ __device__ __forceinline__ int block_begin(const Binning& b, int p) {
   return good;
 }
 
-__device__ __forceinline__ void mma_f16(float (&c)[4], const uint32_t (&a)[4], uint32_t b0, uint32_t b1) {
+__device__ __forceinline__ void mma_f16(float (&c)[4], uint32_t a0, uint32_t a1, uint32_t a2, uint32_t a3, uint32_t b0, uint32_t b1) {
   asm volatile("mma.sync.aligned.m16n8k16.row.col.f32.f16.f16.f32 {%0, %1, %2, %3}, {%4, %5, %6, %7}, {%8, %9}, {%0, %1, %2, %3};"
-               : "+f"(c[0]), "+f"(c[1]), "+f"(c[2]), "+f"(c[3]) : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b0), "r"(b1));
+               : "+f"(c[0]), "+f"(c[1]), "+f"(c[2]), "+f"(c[3]) : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1));
 }
-__device__ __forceinline__ void mma_bf16(float (&c)[4], const uint32_t (&a)[4], uint32_t b0, uint32_t b1) {
+__device__ __forceinline__ void mma_bf16(float (&c)[4], uint32_t a0, uint32_t a1, uint32_t a2, uint32_t a3, uint32_t b0, uint32_t b1) {
   asm volatile("mma.sync.aligned.m16n8k16.row.col.f32.bf16.bf16.f32 {%0, %1, %2, %3}, {%4, %5, %6, %7}, {%8, %9}, {%0, %1, %2, %3};"
-               : "+f"(c[0]), "+f"(c[1]), "+f"(c[2]), "+f"(c[3]) : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b0), "r"(b1));
+               : "+f"(c[0]), "+f"(c[1]), "+f"(c[2]), "+f"(c[3]) : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1));
+}
+// An 8 x 8 matrix of 16-bit values, lane (g, t) holding row g's columns 2 t, 2 t + 1, transposed.
+__device__ __forceinline__ uint32_t transpose8(uint32_t x) {
+  uint32_t y;
+  asm volatile("movmatrix.sync.aligned.m8n8.trans.b16 %0, %1;" : "=r"(y) : "r"(x));
+  return y;
+}
+__device__ __forceinline__ float ex2(float x) {
+  float y;
+  asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
+  return y;
 }
 __device__ __forceinline__ uint32_t bf16x2(float lo, float hi) {
   const __nv_bfloat162 h = __floats2bfloat162_rn(lo, hi);
@@ -122,7 +137,7 @@ __device__ __forceinline__ float bf16_lo(uint32_t x) { return __uint_as_float(x 
 __device__ __forceinline__ float bf16_hi(uint32_t x) { return __uint_as_float(x & 0xFFFF0000u); }
 
 template <int D, typename MaskT, bool kQuant>
-__global__ void __launch_bounds__(kThreads, D == 128 && !kQuant ? 2 : 3)
+__global__ void __launch_bounds__(kThreads, D == 128 && !kQuant ? 1 : 2)
 serve_rows_kernel(ServeArgs a, Split sp) {
   extern __shared__ __align__(16) uint8_t smem_raw[];
   cg::cluster_group cluster = cg::this_cluster();
@@ -146,6 +161,7 @@ serve_rows_kernel(ServeArgs a, Split sp) {
     }
     lg = sp.lg[kvh];
   }
+  const int window = a.H_kv > kMaxSplitHeads ? sp.window_all : sp.window[kvh];
   const int C = 1 << lg, rank = in_cl & (C - 1), rank0 = in_cl - rank;  // the window's blocks are rank0 .. rank0 + C - 1 of the cluster
   x = (x << (3 - lg)) + (in_cl >> lg);                                  // the window's number within the KV head
   const int tokens = sp.tokens, heads = sp.heads;
@@ -175,6 +191,19 @@ serve_rows_kernel(ServeArgs a, Split sp) {
   float* const s_vs = reinterpret_cast<float*>(smem_raw + at_.vs);
   int* const s_page = reinterpret_cast<int*>(smem_raw + at_.page);
 
+  // This block's keys: steps of 32 down from p0, as many as the longest block can reach, dealt out to the window's blocks in runs (step i:
+  // keys p0 - 32 i - 31 .. p0 - 32 i). Their first pages are looked up before anything else is known.
+  const int steps = (min(window, p0 + 1) + kStep - 1) / kStep;
+  const int per = (steps + C - 1) / C;
+  const int s0 = rank * per;
+  int s1 = min(steps, s0 + per);
+  auto find_pages = [&](int b, int ns) {
+    const int slot0 = max(0, p0 - kStep * (b + ns) + 1) >> a.pg.lg_page, slots = ((p0 - kStep * b) >> a.pg.lg_page) - slot0 + 1;
+    for (int k = tid; k < slots; k += kThreads)
+      s_page[k] = slot0 + k < a.pg.width ? a.pg.table[static_cast<long long>(sid) * a.pg.width + slot0 + k] : -1;
+    return slot0;
+  };
+  int slot0 = s0 < s1 ? find_pages(s0, min(kChunkSteps, s1 - s0)) : 0;
   // where the blocks of p0 begin, and so the window; masks above p0
   int lo = p0;
   for (int e = tid; e < nh * PLSH_MAX_S; e += kThreads) s_begin[e] = 0x7fffffff;
@@ -185,107 +214,98 @@ serve_rows_kernel(ServeArgs a, Split sp) {
     s_begin[h * PLSH_MAX_S + k] = b;
     lo = min(lo, b);
   }
-  for (int e = tid; e < nh * kStep; e += kThreads) {
-    const int h = e / kStep, k = e % kStep;
+  for (int e = tid; e < nh * kTail; e += kThreads) {
+    const int h = e / kTail, k = e % kTail;
     s_tail[e] = k + 1 < nt ? bmask[static_cast<size_t>(h0 + h) * a.sq.max_len + p0 + 1 + k] : static_cast<MaskT>(0);
   }
   __shared__ int s_lo[kWarps];
   lo = __reduce_min_sync(0xffffffffu, lo);
   if (lane == 0) s_lo[warp] = lo;
 
-  // Q: lane (g, t) holds rows g and g + 8, in K's order of d
-  float inv_scale[2] = {1.0f, 1.0f};
-  uint32_t q[D / 16][4];
+  // Q: lane (g, t) holds row g, in K's order of d
+  uint32_t q[D / 16][2];
+  float scale_g = 1.4426950408889634f / sqrtf(static_cast<float>(D));  // of row g: S to the exponent of 2
   {
-    float amax[2] = {0.0f, 0.0f};
+    const bool on = g < rows;
+    const __nv_bfloat16* src = static_cast<const __nv_bfloat16*>(a.Q) +
+        (on ? static_cast<long long>(c0 + g / nh) * a.qs.token + (h0 + g % nh) * a.qs.head : 0);
+    float amax = 0.0f;
 #pragma unroll
-    for (int u = 0; u < 2; ++u) {
-      const int r = g + 8 * u;
-      const bool on = r < rows;
-      const __nv_bfloat16* src = static_cast<const __nv_bfloat16*>(a.Q) +
-          (on ? static_cast<long long>(c0 + r / nh) * a.qs.token + (h0 + r % nh) * a.qs.head : 0);
+    for (int c = 0; c < D / 64; ++c) {
+      uint4 w[2] = {make_uint4(0, 0, 0, 0), make_uint4(0, 0, 0, 0)};
+      if (on) {
+        w[0] = *reinterpret_cast<const uint4*>(src + 64 * c + 16 * t);
+        w[1] = *reinterpret_cast<const uint4*>(src + 64 * c + 16 * t + 8);
+      }
+      const uint32_t ws[8] = {w[0].x, w[0].y, w[0].z, w[0].w, w[1].x, w[1].y, w[1].z, w[1].w};
 #pragma unroll
-      for (int c = 0; c < D / 64; ++c) {
-        uint4 w[2] = {make_uint4(0, 0, 0, 0), make_uint4(0, 0, 0, 0)};
-        if (on) {
-          w[0] = *reinterpret_cast<const uint4*>(src + 64 * c + 16 * t);
-          w[1] = *reinterpret_cast<const uint4*>(src + 64 * c + 16 * t + 8);
-        }
-        const uint32_t ws[8] = {w[0].x, w[0].y, w[0].z, w[0].w, w[1].x, w[1].y, w[1].z, w[1].w};
-#pragma unroll
-        for (int k = 0; k < 4; ++k) {
-          q[4 * c + k][u] = ws[2 * k];
-          q[4 * c + k][u + 2] = ws[2 * k + 1];
-        }
-        if (kQuant) {
-#pragma unroll
-          for (int k = 0; k < 8; ++k) amax[u] = fmaxf(amax[u], fmaxf(fabsf(bf16_lo(ws[k])), fabsf(bf16_hi(ws[k]))));
-        }
+      for (int k = 0; k < 8; ++k) {
+        q[4 * c + k / 2][k & 1] = ws[k];
+        if (kQuant) amax = fmaxf(amax, fmaxf(fabsf(bf16_lo(ws[k])), fabsf(bf16_hi(ws[k]))));
       }
     }
     if (kQuant) {  // rows scaled to a largest magnitude in [1, 2): f16 then holds bf16's eight bits down to 2^-14 of it
+      amax = fmaxf(amax, __shfl_xor_sync(0xffffffffu, amax, 1));
+      amax = fmaxf(amax, __shfl_xor_sync(0xffffffffu, amax, 2));
+      const int e = min(126, max(-126, static_cast<int>(__float_as_uint(amax) >> 23) - 127));
+      scale_g *= pow2(e);
+      const float sc = pow2(-e);
 #pragma unroll
-      for (int u = 0; u < 2; ++u) {
-        amax[u] = fmaxf(amax[u], __shfl_xor_sync(0xffffffffu, amax[u], 1));
-        amax[u] = fmaxf(amax[u], __shfl_xor_sync(0xffffffffu, amax[u], 2));
-        const int e = min(126, max(-126, static_cast<int>(__float_as_uint(amax[u]) >> 23) - 127));
-        inv_scale[u] = pow2(e);
-        const float sc = pow2(-e);
-#pragma unroll
-        for (int k = 0; k < D / 16; ++k) {
-          q[k][u] = f16x2(bf16_lo(q[k][u]) * sc, bf16_hi(q[k][u]) * sc);
-          q[k][u + 2] = f16x2(bf16_lo(q[k][u + 2]) * sc, bf16_hi(q[k][u + 2]) * sc);
-        }
+      for (int k = 0; k < D / 16; ++k) {
+        q[k][0] = f16x2(bf16_lo(q[k][0]) * sc, bf16_hi(q[k][0]) * sc);
+        q[k][1] = f16x2(bf16_lo(q[k][1]) * sc, bf16_hi(q[k][1]) * sc);
       }
     }
   }
-  const float sc0 = 1.4426950408889634f / sqrtf(static_cast<float>(D));
-  const float sc[2] = {sc0 * inv_scale[0], sc0 * inv_scale[1]};
+  // of rows 2 t and 2 t + 1, whose columns of S^T the lane has
+  const float sc[2] = {__shfl_sync(0xffffffffu, scale_g, 8 * t), __shfl_sync(0xffffffffu, scale_g, 8 * t + 4)};
 
   __syncthreads();
-  lo = min(min(s_lo[0], s_lo[1]), min(s_lo[2], s_lo[3]));
-  // this block's keys: steps of 16 down from p0, dealt out to the cluster in runs; step i: keys p0 - 16 i - 15 .. p0 - 16 i
-  const int steps = (p0 - lo + kStep) / kStep;
-  const int per = (steps + C - 1) / C;
-  const int s0 = rank * per, s1 = min(steps, s0 + per);
+#pragma unroll
+  for (int w = 0; w < kWarps; ++w) lo = min(lo, s_lo[w]);
+  s1 = min(s1, (p0 - lo + kStep) / kStep);  // the window's exact end
   if (tid < rows) {
     MaskT v = 0;
-    for (int k = 0; k < tid / nh; ++k) v |= s_tail[tid % nh * kStep + k];
+    for (int k = 0; k < tid / nh; ++k) v |= s_tail[tid % nh * kTail + k];
     s_row_off[tid] = v;
   }
 
-  float o[D / 8][4];
+  // O^T: product i has columns (d/8) g + 2 i (0, 1) and (d/8) g + 2 i + 1 (2, 3) of rows 2 t (0, 2) and 2 t + 1 (1, 3)
+  float o[D / 16][4];
 #pragma unroll
-  for (int i = 0; i < D / 8; ++i)
+  for (int i = 0; i < D / 16; ++i)
 #pragma unroll
     for (int e = 0; e < 4; ++e) o[i][e] = 0.0f;
-  float m[2] = {-INFINITY, -INFINITY}, l[2] = {0.0f, 0.0f};
-  MaskT mine[2] = {0, 0};  // of rows g and g + 8: the hashes that may count, and the row's head in the group
+  float m[2] = {-INFINITY, -INFINITY}, l[2] = {0.0f, 0.0f};  // of rows 2 t and 2 t + 1; l: this lane's keys only
+  __syncthreads();
+  MaskT mine[2] = {0, 0};  // the hashes that may count for the two rows, and the rows' heads in the group
   int hh[2] = {0, 0};
+#pragma unroll
+  for (int u = 0; u < 2; ++u)
+    if (2 * t + u < rows) {
+      mine[u] = static_cast<MaskT>(~s_row_off[2 * t + u]);
+      hh[u] = (2 * t + u) % nh;
+    }
 
-  // places of this warp's step in flight
+  // places of this warp's keys in flight
   auto place = [&](int stage) { return (stage * kWarps + warp) * kStep; };
-  // one step: 16 keys at places at .. of sm.row;
-  // byte n of c4[u]: the count of row g + 8 u with key 2 t, 2 t + 1, 2 t + 8 or 2 t + 9
-  auto load_k = [&](int at, uint4 (&kr)[2][D / 64][kQuant ? 1 : 2]) {
+  // K of the 16 keys at places at ..: keys g and g + 8
+  constexpr int kKWords = D / 64 * (kQuant ? 4 : 8);
+  auto load_k = [&](int at, uint32_t (&kr)[2][kKWords]) {
 #pragma unroll
     for (int n = 0; n < 2; ++n) {
       const long long row = s_row[at + 8 * n + g];
 #pragma unroll
-      for (int c = 0; c < D / 64; ++c) {
-        if constexpr (kQuant) {
-          kr[n][c][0] = row >= 0 ? __ldg(reinterpret_cast<const uint4*>(static_cast<const uint8_t*>(a.pg.k) + row * D + 64 * c + 16 * t))
-                                 : make_uint4(0, 0, 0, 0);
-        } else {
-          const uint4* src = reinterpret_cast<const uint4*>(static_cast<const __nv_bfloat16*>(a.pg.k) + row * D + 64 * c + 16 * t);
-          kr[n][c][0] = row >= 0 ? __ldg(src) : make_uint4(0, 0, 0, 0);
-          kr[n][c][1] = row >= 0 ? __ldg(src + 1) : make_uint4(0, 0, 0, 0);
-        }
+      for (int i = 0; i < kKWords / 4; ++i) {
+        const uint8_t* src = static_cast<const uint8_t*>(a.pg.k) + row * (kQuant ? D : 2 * D) +
+                             (kQuant ? 64 * i + 16 * t : 128 * (i >> 1) + 32 * t + 16 * (i & 1));
+        const uint4 w = row >= 0 ? __ldg(reinterpret_cast<const uint4*>(src)) : make_uint4(0, 0, 0, 0);
+        kr[n][4 * i] = w.x; kr[n][4 * i + 1] = w.y; kr[n][4 * i + 2] = w.z; kr[n][4 * i + 3] = w.w;
       }
     }
   };
-  // V's columns (D/8) g .. of keys 2 t, 2 t + 1, 2 t + 8, 2 t + 9: D/8 values each
-  constexpr int kVWords = kQuant ? D / 32 : D / 16;  // 32-bit words
+  // V's columns (d/8) g .. of keys 2 t, 2 t + 1, 2 t + 8, 2 t + 9
+  constexpr int kVWords = kQuant ? D / 32 : D / 16;
   auto load_v = [&](int at, uint32_t (&vr)[4][kVWords]) {
 #pragma unroll
     for (int n = 0; n < 4; ++n) {
@@ -303,237 +323,189 @@ serve_rows_kernel(ServeArgs a, Split sp) {
       }
     }
   };
-  auto step = [&](int at, const uint4 (&kr)[2][D / 64][kQuant ? 1 : 2], const uint32_t (&vr)[4][kVWords], const uint32_t (&c4)[2]) {
-    float x[2][4];
-    auto count = [&](int u, int n) { return (c4[u] >> (8 * n)) & 0xFFu; };
+  // The 16 keys at places at ..; byte 2 n + u of c4: the count of key g + 8 n with row 2 t + u.
+  auto step = [&](int at, const uint32_t (&kr)[2][kKWords], uint32_t c4) {
+    uint32_t vr[4][kVWords];
+    load_v(at, vr);  // lands while S is computed
+    float acc[2][4] = {};  // two chains of products
+#pragma unroll
+    for (int k = 0; k < D / 16; ++k) {
+      if constexpr (kQuant)
+        mma_f16(acc[k & 1], e4m3_f16x2(kr[0][k]), e4m3_f16x2(kr[1][k]), e4m3_f16x2(kr[0][k] >> 16), e4m3_f16x2(kr[1][k] >> 16), q[k][0], q[k][1]);
+      else
+        mma_bf16(acc[k & 1], kr[0][2 * k], kr[1][2 * k], kr[0][2 * k + 1], kr[1][2 * k + 1], q[k][0], q[k][1]);
+    }
+    float x[2][2], top[2] = {-INFINITY, -INFINITY};  // [key][row]
+    uint32_t c[2][2];
 #pragma unroll
     for (int n = 0; n < 2; ++n) {
-      float acc[4] = {0.0f, 0.0f, 0.0f, 0.0f};
+      const float ks = kQuant ? s_ks[at + 8 * n + g] : 1.0f;
 #pragma unroll
-      for (int cc = 0; cc < D / 64; ++cc) {
-        if constexpr (kQuant) {
-          const uint32_t w[4] = {kr[n][cc][0].x, kr[n][cc][0].y, kr[n][cc][0].z, kr[n][cc][0].w};
-#pragma unroll
-          for (int k = 0; k < 4; ++k) mma_f16(acc, q[4 * cc + k], e4m3_f16x2(w[k]), e4m3_f16x2(w[k] >> 16));
-        } else {
-          const uint32_t w[8] = {kr[n][cc][0].x, kr[n][cc][0].y, kr[n][cc][0].z, kr[n][cc][0].w,
-                                 kr[n][cc][1].x, kr[n][cc][1].y, kr[n][cc][1].z, kr[n][cc][1].w};
-#pragma unroll
-          for (int k = 0; k < 4; ++k) mma_bf16(acc, q[4 * cc + k], w[2 * k], w[2 * k + 1]);
-        }
-      }
-      // acc: rows g (0, 1) and g + 8 (2, 3), keys 8 n + 2 t, + 1
-#pragma unroll
-      for (int e = 0; e < 2; ++e) {
-        const float ks = kQuant ? s_ks[at + 8 * n + 2 * t + e] : 1.0f;
-        x[0][2 * n + e] = acc[e] * ks * sc[0];
-        x[1][2 * n + e] = acc[2 + e] * ks * sc[1];
+      for (int u = 0; u < 2; ++u) {
+        c[n][u] = (c4 >> (8 * (2 * n + u))) & 0xFFu;
+        x[n][u] = (acc[0][2 * n + u] + acc[1][2 * n + u]) * ks * sc[u];
+        if (c[n][u]) top[u] = fmaxf(top[u], x[n][u]);
       }
     }
-    uint32_t p[4];
+    if (__any_sync(0xffffffffu, top[0] > m[0] || top[1] > m[1])) {
 #pragma unroll
-    for (int u = 0; u < 2; ++u) {
-      float top = m[u];
+      for (int u = 0; u < 2; ++u) {
 #pragma unroll
-      for (int n = 0; n < 4; ++n) top = count(u, n) > 0 ? fmaxf(top, x[u][n]) : top;
-      top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, 1));
-      top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, 2));
-      if (top > m[u]) {
-        const float alpha = exp2f(m[u] - top);  // 0 the first time
+        for (int s = 4; s <= 16; s <<= 1) top[u] = fmaxf(top[u], __shfl_xor_sync(0xffffffffu, top[u], s));
+        const float now = fmaxf(m[u], top[u]);
+        const float alpha = now == -INFINITY ? 1.0f : ex2(m[u] - now);  // 0 the first time
+        m[u] = now;
         l[u] *= alpha;
 #pragma unroll
-        for (int i = 0; i < D / 8; ++i) {
-          o[i][2 * u] *= alpha;
-          o[i][2 * u + 1] *= alpha;
+        for (int i = 0; i < D / 16; ++i) {
+          o[i][u] *= alpha;
+          o[i][2 + u] *= alpha;
         }
-        m[u] = top;
       }
-      float w[4];
+    }
+    uint32_t b[2];
 #pragma unroll
-      for (int n = 0; n < 4; ++n) {
-        w[n] = count(u, n) > 0 ? static_cast<float>(count(u, n)) * exp2f(x[u][n] - m[u]) : 0.0f;
-        l[u] += w[n];
-        if (kQuant) w[n] *= count(u, n) > 0 ? s_vs[at + 2 * t + (n & 1) + 8 * (n >> 1)] : 0.0f;
+    for (int n = 0; n < 2; ++n) {
+      float w[2];
+      const float vs = kQuant ? s_vs[at + 8 * n + g] : 1.0f;
+#pragma unroll
+      for (int u = 0; u < 2; ++u) {
+        w[u] = c[n][u] ? static_cast<float>(c[n][u]) * ex2(x[n][u] - m[u]) : 0.0f;
+        l[u] += w[u];
+        if (kQuant) w[u] = c[n][u] ? w[u] * vs : 0.0f;
       }
-      p[u] = bf16x2(w[0], w[1]);
-      p[u + 2] = bf16x2(w[2], w[3]);
+      b[n] = transpose8(bf16x2(w[0], w[1]));  // row g, keys 8 n + 2 t, + 1
     }
-    // O += P V: column (D/8) g + i of V is n = g of product i
+    // column (d/8) g + j of keys 2 t, 2 t + 1 (n = 0) and 2 t + 8, 2 t + 9 (n = 1)
+    auto pair = [&](int j, int n) {
+      if constexpr (kQuant) return e4m3_bf16x2(__byte_perm(vr[2 * n][j >> 2], vr[2 * n + 1][j >> 2], 0x0040u + 0x0011u * (j & 3)));
+      else return __byte_perm(vr[2 * n][j >> 1], vr[2 * n + 1][j >> 1], (j & 1) ? 0x7632u : 0x5410u);
+    };
 #pragma unroll
-    for (int i = 0; i < D / 8; ++i) {
-      uint32_t b0, b1;
-      if constexpr (kQuant) {
-        const uint32_t sel = 0x0040u + 0x0011u * (i & 3);  // byte i & 3 of both
-        b0 = e4m3_bf16x2(__byte_perm(vr[0][i >> 2], vr[1][i >> 2], sel));
-        b1 = e4m3_bf16x2(__byte_perm(vr[2][i >> 2], vr[3][i >> 2], sel));
-      } else {
-        const uint32_t sel = (i & 1) ? 0x7632u : 0x5410u;
-        b0 = __byte_perm(vr[0][i >> 1], vr[1][i >> 1], sel);
-        b1 = __byte_perm(vr[2][i >> 1], vr[3][i >> 1], sel);
-      }
-      mma_bf16(o[i], p, b0, b1);
-    }
-  };
-
-  __syncthreads();
-#pragma unroll
-  for (int u = 0; u < 2; ++u) {
-    const int r = g + 8 * u;
-    if (r < rows) {
-      mine[u] = static_cast<MaskT>(~s_row_off[r]);
-      hh[u] = r % nh;
-    }
-  }
-  // exponents of the rows at places at ..: lanes 0 .. 15 K's, 16 .. 31 V's
-  auto exponents = [&](int at) {
-    if (kQuant) {
-      const long long row = s_row[at + (lane & 15)];
-      return row >= 0 ? pow2((lane < 16 ? a.pg.k_exp : a.pg.v_exp)[row]) : 0.0f;
-    }
-    return 0.0f;
-  };
-  auto put_exponents = [&](int at, float e) {
-    if (kQuant) (lane < 16 ? s_ks : s_vs)[at + (lane & 15)] = e;
+    for (int i = 0; i < D / 16; ++i) mma_bf16(o[i], pair(2 * i, 0), pair(2 * i + 1, 0), pair(2 * i, 1), pair(2 * i + 1, 1), b[0], b[1]);
   };
 
   // ---- the keys above p0, one step of the first block's first warp
   if (rank == 0 && warp == 0 && nt > 1) {
     const int at = place(0);
-    if (lane < kStep) s_row[at + lane] = lane + 1 < nt ? page_row(a.pg, sid, p0 + 1 + lane, kvh, a.err) : -1;
+    if (lane < kTail) {
+      const long long row = lane + 1 < nt ? page_row(a.pg, sid, p0 + 1 + lane, kvh, a.err) : -1;
+      s_row[at + lane] = row;
+      if (kQuant) {
+        s_ks[at + lane] = row >= 0 ? pow2(a.pg.k_exp[row]) : 0.0f;
+        s_vs[at + lane] = row >= 0 ? pow2(a.pg.v_exp[row]) : 0.0f;
+      }
+    }
     __syncwarp();
-    uint4 kr[2][D / 64][kQuant ? 1 : 2];
-    uint32_t vr[4][kVWords];
+    uint32_t kr[2][kKWords];
     load_k(at, kr);
-    load_v(at, vr);
-    put_exponents(at, exponents(at));
-    __syncwarp();
-    uint32_t c[2] = {0, 0};
+    uint32_t c4 = 0;
 #pragma unroll
     for (int u = 0; u < 2; ++u) {
-      const int r = g + 8 * u, tok = r / nh;  // the row's token: position p0 + tok
+      const int r = 2 * t + u, tok = r / nh;  // the row's token: position p0 + tok
 #pragma unroll
-      for (int n = 0; n < 4; ++n) {
-        const int k = 2 * t + (n & 1) + 8 * (n >> 1);  // key p0 + 1 + k
+      for (int n = 0; n < 2; ++n) {
+        const int k = g + 8 * n;              // key p0 + 1 + k
         if (r < rows && k + 1 <= tok) {
           MaskT v = 0;
-          for (int y = k + 1; y < tok; ++y) v |= s_tail[hh[u] * kStep + y];
-          c[u] |= static_cast<uint32_t>(a.s - popc_mask<MaskT>(v)) << (8 * n);
+          for (int y = k + 1; y < tok; ++y) v |= s_tail[hh[u] * kTail + y];
+          c4 |= static_cast<uint32_t>(a.s - popc_mask<MaskT>(v)) << (8 * (2 * n + u));
         }
       }
     }
-    step(at, kr, vr, c);
+    step(at, kr, c4);
     __syncwarp();
   }
 
   // ---- the window
-  MaskT* const keep = s_keep + warp * heads * kStep;
   for (int b = s0; b < s1; b += kChunkSteps) {
     const int ns = min(kChunkSteps, s1 - b);
-    const int slot0 = max(lo, p0 - kStep * (b + ns) + 1) >> a.pg.lg_page, slots = ((p0 - kStep * b) >> a.pg.lg_page) - slot0 + 1;
-    __syncthreads();
-    for (int k = tid; k < slots; k += kThreads) {
-      int page = slot0 + k < a.pg.width ? a.pg.table[static_cast<long long>(sid) * a.pg.width + slot0 + k] : -1;
-      if (page < 0 || page >= a.pg.num_pages) {
-        atomicOr(a.err, PLSH_DEVERR_PAGE);
-        page = -1;
-      }
-      s_page[k] = page;
+    if (b > s0) {
+      __syncthreads();
+      slot0 = find_pages(b, ns);
+      __syncthreads();
     }
-    __syncthreads();
-    // Step i of the chunk: rows and counts of its keys into the stage's places. False: nothing has weight there. Key k of
-    // the step is p0 - 16 (b + i) - k; a lane per hash says which hashes' blocks reach it.
-    auto describe = [&](int i, int stage, uint32_t (&c)[2]) {
-      const int at = place(stage), j0 = p0 - kStep * (b + i);
-      __syncwarp();
-      if (lane < kStep) {
-        const int j = j0 - lane;
-        long long row = -1;
-        if (j >= lo) {
-          const int page = s_page[(j >> a.pg.lg_page) - slot0];
-          if (page >= 0)
-            row = ((static_cast<long long>(page) * a.pg.H_kv + kvh) << a.pg.lg_page) + (j & ((1 << a.pg.lg_page) - 1));
-        }
-        s_row[at + lane] = row;
+    // Step i of the chunk, a lane per key (lane k: key p0 - 32 (b + i) - k): its row, exponents and the hashes whose blocks
+    // reach it, into the stage's places. Returns which keys have weight for some row.
+    auto describe = [&](int i, int stage) -> uint32_t {
+      const int at = place(stage), j = p0 - kStep * (b + i) - lane;
+      MaskT* const keep = s_keep + (stage * kWarps + warp) * heads * kStep;
+      long long row = -1;
+      if (i < ns && j >= lo) {
+        const int page = s_page[(j >> a.pg.lg_page) - slot0];
+        if (page < 0 || page >= a.pg.num_pages) atomicOr(a.err, PLSH_DEVERR_PAGE);
+        else row = ((static_cast<long long>(page) * a.pg.H_kv + kvh) << a.pg.lg_page) + (j & ((1 << a.pg.lg_page) - 1));
       }
+      int8_t ek = 0, ev = 0;
+      if (kQuant && row >= 0) {
+        ek = a.pg.k_exp[row];
+        ev = a.pg.v_exp[row];
+      }
+      MaskT all = 0;
       for (int h = 0; h < nh; ++h) {
-        const int b0 = s_begin[h * PLSH_MAX_S + lane];
-        const int b1 = sizeof(MaskT) == 8 ? s_begin[h * PLSH_MAX_S + 32 + lane] : 0;
+        const int4* begin = reinterpret_cast<const int4*>(s_begin + h * PLSH_MAX_S);
         MaskT v = 0;
-#pragma unroll
-        for (int k = 0; k < kStep; ++k) {
-          MaskT m = static_cast<MaskT>(__ballot_sync(0xffffffffu, b0 <= j0 - k));
-          if (sizeof(MaskT) == 8) m |= static_cast<MaskT>(static_cast<unsigned long long>(__ballot_sync(0xffffffffu, b1 <= j0 - k)) << 32);
-          if (lane == k) v = m;
+        for (int k = 0; k < (a.s + 3) / 4; ++k) {  // places past the last hash hold the largest position
+          const int4 b4 = begin[k];
+          const uint32_t n4 = (b4.x <= j ? 1u : 0u) | (b4.y <= j ? 2u : 0u) | (b4.z <= j ? 4u : 0u) | (b4.w <= j ? 8u : 0u);
+          v |= static_cast<MaskT>(n4) << (4 * k);
         }
-        if (lane < kStep) keep[h * kStep + lane] = v;
+        keep[h * kStep + lane] = v;
+        all |= v;
       }
+      s_row[at + lane] = row;
+      if (kQuant) {
+        s_ks[at + lane] = pow2(ek);
+        s_vs[at + lane] = pow2(ev);
+      }
+      const uint32_t live = __ballot_sync(0xffffffffu, row >= 0 && all != 0);
       __syncwarp();
-#pragma unroll
-      for (int u = 0; u < 2; ++u) {
-        c[u] = 0;
-#pragma unroll
-        for (int n = 0; n < 4; ++n) {
-          const int k = 2 * t + (n & 1) + 8 * (n >> 1);
-          if (s_row[at + k] >= 0) c[u] |= static_cast<uint32_t>(popc_mask<MaskT>(static_cast<MaskT>(keep[hh[u] * kStep + k] & mine[u]))) << (8 * n);
-        }
-      }
-      return __any_sync(0xffffffffu, (c[0] | c[1]) != 0) != 0;
+      return live;
     };
-    // a warp's steps, the next one's K on its way while this one is computed
-    uint4 kr[2][D / 64][kQuant ? 1 : 2];
-    uint32_t c[2];
-    int i = warp, stage = 0;
-    while (i < ns && !describe(i, stage, c)) i += kWarps;
-    float ex = 0.0f;
-    if (i < ns) {
-      load_k(place(stage), kr);
-      ex = exponents(place(stage));
-    }
-    while (i < ns) {
-      uint32_t vr[4][kVWords];
-      load_v(place(stage), vr);
-      put_exponents(place(stage), ex);
-      int nx = i + kWarps;
-      uint32_t cn[2];
-      while (nx < ns && !describe(nx, stage ^ 1, cn)) nx += kWarps;
-      uint4 kn[2][D / 64][kQuant ? 1 : 2];
-      if (kQuant && nx < ns) {
-        load_k(place(stage ^ 1), kn);
-        ex = exponents(place(stage ^ 1));
-      }
-      __syncwarp();
-      step(place(stage), kr, vr, c);
-      if (!kQuant && nx < ns) load_k(place(stage ^ 1), kn);  // (rows of bf16 take twice the registers)
-      i = nx;
-      stage ^= 1;
-      c[0] = cn[0];
-      c[1] = cn[1];
+    // the counts of half h's keys g and g + 8 with rows 2 t and 2 t + 1
+    auto counts = [&](int stage, int h) -> uint32_t {
+      const MaskT* const keep = s_keep + (stage * kWarps + warp) * heads * kStep + 16 * h;
+      const long long* const row = s_row + place(stage) + 16 * h;
+      uint32_t c4 = 0;
 #pragma unroll
       for (int n = 0; n < 2; ++n)
+        if (row[g + 8 * n] >= 0) {
 #pragma unroll
-        for (int cc = 0; cc < D / 64; ++cc)
-#pragma unroll
-          for (int y = 0; y < (kQuant ? 1 : 2); ++y) kr[n][cc][y] = kn[n][cc][y];
+          for (int u = 0; u < 2; ++u)
+            c4 |= static_cast<uint32_t>(popc_mask<MaskT>(static_cast<MaskT>(keep[hh[u] * kStep + g + 8 * n] & mine[u]))) << (8 * (2 * n + u));
+        }
+      return c4;
+    };
+    // a warp's steps; the next half's K is on its way while one is computed
+    int stage = 0;
+    uint32_t live = describe(warp, 0);
+    uint32_t ka[2][kKWords], kb[2][kKWords];
+    if (live & 0xFFFFu) load_k(place(0), ka);
+    for (int i = warp; i < ns; i += kWarps) {
+      if (live >> 16) load_k(place(stage) + 16, kb);
+      if (live & 0xFFFFu) step(place(stage), ka, counts(stage, 0));
+      const uint32_t next = describe(i + kWarps, stage ^ 1);
+      if (next & 0xFFFFu) load_k(place(stage ^ 1), ka);
+      if (live >> 16) step(place(stage) + 16, kb, counts(stage, 1));
+      live = next;
+      stage ^= 1;
     }
   }
 
   // ---- join: the warps' rows of every block of the cluster
 #pragma unroll
   for (int u = 0; u < 2; ++u) {
-    l[u] += __shfl_xor_sync(0xffffffffu, l[u], 1);
-    l[u] += __shfl_xor_sync(0xffffffffu, l[u], 2);
-    const int r = g + 8 * u;
+#pragma unroll
+    for (int s = 4; s <= 16; s <<= 1) l[u] += __shfl_xor_sync(0xffffffffu, l[u], s);
+    const int r = 2 * t + u;
     if (r >= rows) continue;
-    if (t == 0) {
+    if (g == 0) {
       s_ml[warp * max_rows + r] = m[u];
       s_ml[(kWarps + warp) * max_rows + r] = l[u];
     }
-    // product i's columns n = 2 t, 2 t + 1: V's columns (D/8) (2 t) + i and (D/8) (2 t + 1) + i
 #pragma unroll
-    for (int i = 0; i < D / 8; ++i) {
-      s_o[(warp * max_rows + r) * (D + 4) + (D / 8) * (2 * t) + i] = o[i][2 * u];
-      s_o[(warp * max_rows + r) * (D + 4) + (D / 8) * (2 * t + 1) + i] = o[i][2 * u + 1];
-    }
+    for (int i = 0; i < D / 16; ++i)
+      *reinterpret_cast<float2*>(s_o + (warp * max_rows + r) * (D + 4) + (D / 8) * g + 2 * i) = make_float2(o[i][u], o[i][2 + u]);
   }
   __syncthreads();
   // the block's warps, into the first one's place
@@ -605,7 +577,7 @@ int launch(const ServeArgs& a, cudaStream_t st) {
   const long long per_head = static_cast<long long>(a.sq.S) * sp.row_blocks * sp.head_blocks;
   if (per_head * kCluster * a.H_kv > 0x7fffffffLL) return fail(PLSH_ERR_RANGE, "plsh_paged_fwd: too many rows");
   sp.per_head = static_cast<int>(per_head);
-  // Blocks of a window: one for each `keys` keys of the widest head's longest block, 64 (a step a warp) while the launch then has
+  // Blocks of a window: one for each `keys` keys of the widest head's longest block, 256 (a step a warp) while the launch then has
   // up to four blocks an SM, else the fewest doublings that come near it.
   long long clusters = 0;
   for (int keys = kWarps * kStep; keys <= 4096; keys *= 2) {
@@ -621,6 +593,7 @@ int launch(const ServeArgs& a, cudaStream_t st) {
       while (lg < 3 && (static_cast<long long>(keys) << lg) < w) ++lg;
       if (a.H_kv > kMaxSplitHeads) lg = sp.lg_all = lg > sp.lg_all && k > 0 ? lg : k > 0 ? sp.lg_all : lg;
       else sp.lg[k] = static_cast<uint8_t>(lg);
+      (a.H_kv > kMaxSplitHeads ? sp.window_all : sp.window[k]) = a.H_kv > kMaxSplitHeads && sp.window_all > w ? sp.window_all : w;
       blocks += per_head << lg;
       clusters += ((per_head << lg) + kCluster - 1) / kCluster;
     }
