@@ -2,13 +2,15 @@
 //
 // Rows are the (token, query head) pairs that share a KV head, up to 8 in a block; their keys are the
 // window below them, so the work is reading K and V once: 2 (d + 1) bytes a key and KV head when the pages
-// hold e4m3. One to eight blocks share a window, by its width, eight warps a block, each taking 32 keys at a time, two steps of 16:
+// hold e4m3. A team of 1 to 64 warps shares a window, by its width: some of the eight of a block, or up to eight whole blocks (a
+// cluster). A warp takes 32 keys at a time, two steps of 16:
 //   S^T[16 keys][8 rows] = K Q^T   d/16 products mma.m16n8k16, fp32 accumulation
 //   P = c 2^(S sc - m), against the warp's own running maximum m over keys with c > 0
 //   O^T[d][8 rows] += V^T P^T      d/16 products
-// and the partial rows (m, l, O) meet at the end, the warps' in shared memory and the blocks' across it (eight blocks
-// are a cluster: one wide window's, or two, four or eight narrower ones'): one launch, no scratch, and always
-// joined in the same order, so results do not depend on timing.
+// and the partial rows (m, l, O) meet at the end, the warps' in shared memory and the blocks' across it (distributed shared
+// memory): one launch, no scratch, and always joined in the same order, so results do not depend on timing. Teams are
+// sized so that the launch fits the machine at once: narrow windows with a block each left a second wave of blocks whose
+// time is all trips to memory (64 sequences, 16/8 heads, d 128, e4m3: 39 us).
 //
 // The rows are the products' narrow side: with them on the wide one (16), half of the products, of O's registers and of
 // the exponentials were padding. K and V go from the pages to registers, 16 bytes at a time, and are not staged: a dot product may
@@ -31,6 +33,7 @@
 
 #include "plsh_binid.cuh"
 #include "plsh_serve.cuh"
+#include "plsh_tile_common.cuh"
 
 namespace plsh {
 namespace {
@@ -45,14 +48,16 @@ constexpr int kChunkSteps = 32;  // steps of 32 keys whose pages a block holds a
 constexpr int kMaxSplitHeads = 64;
 constexpr int kMaxGroup = 8;     // query heads of a block (a larger group takes several blocks)
 
-// How a launch's windows are dealt out: 2^lg[kv head] blocks of each (with more KV heads, lg_all), kv heads from the last.
+// How a launch's windows are dealt out: 2^lg warps to each (with more KV heads, lg_all), KV heads from the last.
 struct Split {
-  int tokens, heads, row_blocks, head_blocks;  // of a block; blocks of a sequence's rows and of a group's heads
+  int tokens, heads, row_blocks, head_blocks;  // of a team; teams of a sequence's rows and of a group's heads
   int per_head;                                // windows of a KV head: sequences x row blocks x head blocks
   int lg_all, window_all;
   int window[kMaxSplitHeads];  // the longest block of a KV head's heads
   uint8_t lg[kMaxSplitHeads];
 };
+// Clusters of eight blocks (64 warps) for `windows` windows of 2^lg warps.
+__host__ __device__ inline int clusters_of(int windows, int lg) { return static_cast<int>(((static_cast<long long>(windows) << lg) + 63) >> 6); }
 
 // Shared memory of a block for `heads` query heads and `rows` rows.
 template <int D, typename MaskT>
@@ -67,11 +72,11 @@ struct Layout {
     };
     o = take(kWarps * rows * (D + 4) * 4);         // [warp][row][D + 4]: the warps' rows of O
     ml = take(2 * kWarps * rows * 4);              // [2][warp][row]: their m and l
-    begin = take(heads * PLSH_MAX_S * 4);          // [head][hash]: where p0's block begins
+    begin = take(kWarps * heads * PLSH_MAX_S * 4); // [team, at its first warp][head][hash]: where p0's block begins
     keep = take(2 * kWarps * heads * kStep * (int)sizeof(MaskT));  // [stage][warp][head][key]: hashes whose block reaches the key
-    row_off = take(rows * (int)sizeof(MaskT));     // [row]: hashes that open a block in (p0, i]
-    tail = take(heads * kTail * (int)sizeof(MaskT));    // [head][k]: masks of positions p0 + 1 + k
-    page = take((2 * kChunkSteps + 2) * 4);            // pages of the chunk's positions (they hold 16 and more)
+    row_off = take(kWarps * rows * (int)sizeof(MaskT));  // [team][row]: hashes that open a block in (p0, i]
+    tail = take(kWarps * heads * kTail * (int)sizeof(MaskT));  // [team][head][k]: masks of positions p0 + 1 + k
+    page = take(kWarps * (2 * kChunkSteps + 4) * 4);   // [team]: pages of the chunk's positions (they hold 16 and more)
     row = take(2 * kWarps * kStep * 8);            // [stage][warp][key]: its row in the pages (-1: none)
     ks = take(2 * kWarps * kStep * 4);             // the same: 2^exponent of K and of V
     vs = take(2 * kWarps * kStep * 4);
@@ -144,26 +149,27 @@ serve_rows_kernel(ServeArgs a, Split sp) {
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31, g = lane >> 2, t = lane & 3;
   if (blockIdx.x == 0) check_seqs(a.sq, a.err);
 
-  // KV heads from the last (with the usual slopes, the widest windows first), a KV head's windows 8 / C to a cluster
-  const int cl = blockIdx.x / kCluster, in_cl = blockIdx.x % kCluster;
-  int kvh, lg = sp.lg_all, x;
+  // KV heads from the last (with the usual slopes, the widest windows first)
+  int x = blockIdx.x / kCluster, kvh, lg = sp.lg_all;  // x: the cluster's number within the KV head
   if (a.H_kv > kMaxSplitHeads) {
-    const int per = (sp.per_head << lg) / kCluster + ((sp.per_head << lg) % kCluster != 0);
-    kvh = a.H_kv - 1 - cl / per;
-    x = cl % per;
+    const int per = clusters_of(sp.per_head, lg);
+    kvh = a.H_kv - 1 - x / per;
+    x %= per;
   } else {
-    x = cl;
     for (kvh = a.H_kv - 1; kvh > 0; --kvh) {
-      lg = sp.lg[kvh];
-      const int per = ((sp.per_head << lg) + kCluster - 1) / kCluster;
+      const int per = clusters_of(sp.per_head, sp.lg[kvh]);
       if (x < per) break;
       x -= per;
     }
     lg = sp.lg[kvh];
   }
   const int window = a.H_kv > kMaxSplitHeads ? sp.window_all : sp.window[kvh];
-  const int C = 1 << lg, rank = in_cl & (C - 1), rank0 = in_cl - rank;  // the window's blocks are rank0 .. rank0 + C - 1 of the cluster
-  x = (x << (3 - lg)) + (in_cl >> lg);                                  // the window's number within the KV head
+  // the team: W warps of each of C blocks; this block's part is warps w0 .. w0 + W - 1
+  const int W = min(kWarps, 1 << lg), C = max(1, (1 << lg) / kWarps), in_cl = blockIdx.x % kCluster;
+  const int rank = in_cl & (C - 1), rank0 = in_cl - rank;  // blocks rank0 .. rank0 + C - 1 of the cluster
+  const int w0 = warp & ~(W - 1), team_tid = tid - 32 * w0, team_threads = 32 * W;
+  auto team_sync = [&]() { asm volatile("bar.sync %0, %1;" ::"r"(1 + w0), "r"(team_threads) : "memory"); };
+  x = ((x * kCluster + in_cl) * kWarps + warp) >> lg;      // the window's number within the KV head
   const int tokens = sp.tokens, heads = sp.heads;
   const int hb = x % sp.head_blocks;
   x /= sp.head_blocks;
@@ -173,8 +179,8 @@ serve_rows_kernel(ServeArgs a, Split sp) {
   if (sid < a.sq.S) sq = load_seq(a.sq, sid);
   const int first = rb * tokens;                              // the block's first token in the sequence
   const int nt = min(tokens, sq.len - first);
-  // nothing here (or a longer sequence, the tile kernel's): the cluster's barriers do not wait for a block that has ended, and
-  // nobody reads its memory
+  // nothing here (or a longer sequence, the tile kernel's): the cluster's barriers do not wait for warps that have ended, and
+  // nobody reads their memory
   if (sid >= a.sq.S || nt <= 0 || sq.len > a.few) return;
   const int rows = nt * nh, p0 = sq.pos0 + first, c0 = sq.c0 + first;
   const MaskT* bmask = static_cast<const MaskT*>(a.bmask);
@@ -182,14 +188,14 @@ serve_rows_kernel(ServeArgs a, Split sp) {
   const Layout<D, MaskT> at_(heads, max_rows);
   float* const s_o = reinterpret_cast<float*>(smem_raw + at_.o);
   float* const s_ml = reinterpret_cast<float*>(smem_raw + at_.ml);
-  int* const s_begin = reinterpret_cast<int*>(smem_raw + at_.begin);
+  int* const s_begin = reinterpret_cast<int*>(smem_raw + at_.begin) + w0 * heads * PLSH_MAX_S;
   MaskT* const s_keep = reinterpret_cast<MaskT*>(smem_raw + at_.keep);
-  MaskT* const s_row_off = reinterpret_cast<MaskT*>(smem_raw + at_.row_off);
-  MaskT* const s_tail = reinterpret_cast<MaskT*>(smem_raw + at_.tail);
+  MaskT* const s_row_off = reinterpret_cast<MaskT*>(smem_raw + at_.row_off) + w0 * max_rows;
+  MaskT* const s_tail = reinterpret_cast<MaskT*>(smem_raw + at_.tail) + w0 * heads * kTail;
   long long* const s_row = reinterpret_cast<long long*>(smem_raw + at_.row);
   float* const s_ks = reinterpret_cast<float*>(smem_raw + at_.ks);
   float* const s_vs = reinterpret_cast<float*>(smem_raw + at_.vs);
-  int* const s_page = reinterpret_cast<int*>(smem_raw + at_.page);
+  int* const s_page = reinterpret_cast<int*>(smem_raw + at_.page) + w0 * (2 * kChunkSteps + 4);
 
   // This block's keys: steps of 32 down from p0, as many as the longest block can reach, dealt out to the window's blocks in runs (step i:
   // keys p0 - 32 i - 31 .. p0 - 32 i). Their first pages are looked up before anything else is known.
@@ -199,22 +205,22 @@ serve_rows_kernel(ServeArgs a, Split sp) {
   int s1 = min(steps, s0 + per);
   auto find_pages = [&](int b, int ns) {
     const int slot0 = max(0, p0 - kStep * (b + ns) + 1) >> a.pg.lg_page, slots = ((p0 - kStep * b) >> a.pg.lg_page) - slot0 + 1;
-    for (int k = tid; k < slots; k += kThreads)
+    for (int k = team_tid; k < slots; k += team_threads)
       s_page[k] = slot0 + k < a.pg.width ? a.pg.table[static_cast<long long>(sid) * a.pg.width + slot0 + k] : -1;
     return slot0;
   };
   int slot0 = s0 < s1 ? find_pages(s0, min(kChunkSteps, s1 - s0)) : 0;
   // where the blocks of p0 begin, and so the window; masks above p0
   int lo = p0;
-  for (int e = tid; e < nh * PLSH_MAX_S; e += kThreads) s_begin[e] = 0x7fffffff;
-  __syncthreads();
-  for (int e = tid; e < nh * a.s; e += kThreads) {
+  for (int e = team_tid; e < nh * PLSH_MAX_S; e += team_threads)
+    if (e % PLSH_MAX_S >= a.s) s_begin[e] = 0x7fffffff;
+  for (int e = team_tid; e < nh * a.s; e += team_threads) {
     const int h = e / a.s, k = e % a.s;
     const int b = block_begin(Binning::from_table(a.table + (static_cast<size_t>(h0 + h) * a.s + k) * 2), p0);
     s_begin[h * PLSH_MAX_S + k] = b;
     lo = min(lo, b);
   }
-  for (int e = tid; e < nh * kTail; e += kThreads) {
+  for (int e = team_tid; e < nh * kTail; e += team_threads) {
     const int h = e / kTail, k = e % kTail;
     s_tail[e] = k + 1 < nt ? bmask[static_cast<size_t>(h0 + h) * a.sq.max_len + p0 + 1 + k] : static_cast<MaskT>(0);
   }
@@ -260,14 +266,13 @@ serve_rows_kernel(ServeArgs a, Split sp) {
   // of rows 2 t and 2 t + 1, whose columns of S^T the lane has
   const float sc[2] = {__shfl_sync(0xffffffffu, scale_g, 8 * t), __shfl_sync(0xffffffffu, scale_g, 8 * t + 4)};
 
-  __syncthreads();
-#pragma unroll
-  for (int w = 0; w < kWarps; ++w) lo = min(lo, s_lo[w]);
+  team_sync();
+  for (int w = 0; w < W; ++w) lo = min(lo, s_lo[w0 + w]);
   s1 = min(s1, (p0 - lo + kStep) / kStep);  // the window's exact end
-  if (tid < rows) {
+  if (team_tid < rows) {
     MaskT v = 0;
-    for (int k = 0; k < tid / nh; ++k) v |= s_tail[tid % nh * kTail + k];
-    s_row_off[tid] = v;
+    for (int k = 0; k < team_tid / nh; ++k) v |= s_tail[team_tid % nh * kTail + k];
+    s_row_off[team_tid] = v;
   }
 
   // O^T: product i has columns (d/8) g + 2 i (0, 1) and (d/8) g + 2 i + 1 (2, 3) of rows 2 t (0, 2) and 2 t + 1 (1, 3)
@@ -277,7 +282,7 @@ serve_rows_kernel(ServeArgs a, Split sp) {
 #pragma unroll
     for (int e = 0; e < 4; ++e) o[i][e] = 0.0f;
   float m[2] = {-INFINITY, -INFINITY}, l[2] = {0.0f, 0.0f};  // of rows 2 t and 2 t + 1; l: this lane's keys only
-  __syncthreads();
+  team_sync();
   MaskT mine[2] = {0, 0};  // the hashes that may count for the two rows, and the rows' heads in the group
   int hh[2] = {0, 0};
 #pragma unroll
@@ -386,7 +391,7 @@ serve_rows_kernel(ServeArgs a, Split sp) {
   };
 
   // ---- the keys above p0, one step of the first block's first warp
-  if (rank == 0 && warp == 0 && nt > 1) {
+  if (rank == 0 && warp == w0 && nt > 1) {
     const int at = place(0);
     if (lane < kTail) {
       const long long row = lane + 1 < nt ? page_row(a.pg, sid, p0 + 1 + lane, kvh, a.err) : -1;
@@ -421,23 +426,31 @@ serve_rows_kernel(ServeArgs a, Split sp) {
   for (int b = s0; b < s1; b += kChunkSteps) {
     const int ns = min(kChunkSteps, s1 - b);
     if (b > s0) {
-      __syncthreads();
+      team_sync();
       slot0 = find_pages(b, ns);
-      __syncthreads();
+      team_sync();
     }
     // Step i of the chunk, a lane per key (lane k: key p0 - 32 (b + i) - k): its row, exponents and the hashes whose blocks
     // reach it, into the stage's places. Returns which keys have weight for some row.
+    int8_t ek = 0, ev = 0;
+    auto put_exponents = [&](int stage) {
+      if (kQuant) {
+        s_ks[place(stage) + lane] = pow2(ek);
+        s_vs[place(stage) + lane] = pow2(ev);
+        __syncwarp();
+      }
+    };
     auto describe = [&](int i, int stage) -> uint32_t {
       const int at = place(stage), j = p0 - kStep * (b + i) - lane;
       MaskT* const keep = s_keep + (stage * kWarps + warp) * heads * kStep;
+      __syncwarp();  // the stage's last reader is done
       long long row = -1;
       if (i < ns && j >= lo) {
         const int page = s_page[(j >> a.pg.lg_page) - slot0];
         if (page < 0 || page >= a.pg.num_pages) atomicOr(a.err, PLSH_DEVERR_PAGE);
         else row = ((static_cast<long long>(page) * a.pg.H_kv + kvh) << a.pg.lg_page) + (j & ((1 << a.pg.lg_page) - 1));
       }
-      int8_t ek = 0, ev = 0;
-      if (kQuant && row >= 0) {
+      if (kQuant && row >= 0) {  // stored when they have come, before the step
         ek = a.pg.k_exp[row];
         ev = a.pg.v_exp[row];
       }
@@ -454,10 +467,6 @@ serve_rows_kernel(ServeArgs a, Split sp) {
         all |= v;
       }
       s_row[at + lane] = row;
-      if (kQuant) {
-        s_ks[at + lane] = pow2(ek);
-        s_vs[at + lane] = pow2(ev);
-      }
       const uint32_t live = __ballot_sync(0xffffffffu, row >= 0 && all != 0);
       __syncwarp();
       return live;
@@ -478,15 +487,17 @@ serve_rows_kernel(ServeArgs a, Split sp) {
     };
     // a warp's steps; the next half's K is on its way while one is computed
     int stage = 0;
-    uint32_t live = describe(warp, 0);
+    uint32_t live = describe(warp - w0, 0);
     uint32_t ka[2][kKWords], kb[2][kKWords];
     if (live & 0xFFFFu) load_k(place(0), ka);
-    for (int i = warp; i < ns; i += kWarps) {
+    put_exponents(0);
+    for (int i = warp - w0; i < ns; i += W) {
       if (live >> 16) load_k(place(stage) + 16, kb);
       if (live & 0xFFFFu) step(place(stage), ka, counts(stage, 0));
-      const uint32_t next = describe(i + kWarps, stage ^ 1);
+      const uint32_t next = describe(i + W, stage ^ 1);
       if (next & 0xFFFFu) load_k(place(stage ^ 1), ka);
       if (live >> 16) step(place(stage) + 16, kb, counts(stage, 1));
+      put_exponents(stage ^ 1);
       live = next;
       stage ^= 1;
     }
@@ -507,27 +518,7 @@ serve_rows_kernel(ServeArgs a, Split sp) {
     for (int i = 0; i < D / 16; ++i)
       *reinterpret_cast<float2*>(s_o + (warp * max_rows + r) * (D + 4) + (D / 8) * g + 2 * i) = make_float2(o[i][u], o[i][2 + u]);
   }
-  __syncthreads();
-  // the block's warps, into the first one's place
-  for (int e = tid; e < rows * (D / 4); e += kThreads) {
-    const int r = e / (D / 4), col = e % (D / 4) * 4;
-    float top = -INFINITY, total = 0.0f, acc[4] = {0.0f, 0.0f, 0.0f, 0.0f};
-#pragma unroll
-    for (int w = 0; w < kWarps; ++w) top = fmaxf(top, s_ml[w * max_rows + r]);
-#pragma unroll
-    for (int w = 0; w < kWarps; ++w) {
-      const float mw = s_ml[w * max_rows + r];
-      const float f = mw == -INFINITY ? 0.0f : exp2f(mw - top);  // -inf: a warp without keys
-      const float4 v = *reinterpret_cast<const float4*>(s_o + (w * max_rows + r) * (D + 4) + col);
-      total += s_ml[(kWarps + w) * max_rows + r] * f;
-      acc[0] += v.x * f;
-      acc[1] += v.y * f;
-      acc[2] += v.z * f;
-      acc[3] += v.w * f;
-    }
-    *reinterpret_cast<float4*>(s_o + r * (D + 4) + col) = make_float4(acc[0], acc[1], acc[2], acc[3]);
-    if (col == 0) *reinterpret_cast<float2*>(s_o + r * (D + 4) + D) = make_float2(top, total);  // behind the row
-  }
+  team_sync();
   auto finish = [&](int r, int col, float top, float total, const float (&acc)[4]) {
     const float inv = 1.0f / total;
     const size_t at = static_cast<size_t>(c0 + r / nh) * a.H + h0 + r % nh;
@@ -535,6 +526,31 @@ serve_rows_kernel(ServeArgs a, Split sp) {
     store4f(static_cast<__nv_bfloat16*>(a.O) + at * D + col, out);
     if (col == 0) a.row_sum[at] = (log2f(total) + top) * 0.6931471805599453f - logf(static_cast<float>(a.s));
   };
+  // the block's warps, into the first one's place, or straight into the result
+  float* const o0 = s_o + w0 * max_rows * (D + 4);
+  for (int e = team_tid; e < rows * (D / 4); e += team_threads) {
+    const int r = e / (D / 4), col = e % (D / 4) * 4;
+    float top = -INFINITY, total = 0.0f, acc[4] = {0.0f, 0.0f, 0.0f, 0.0f};
+    for (int w = w0; w < w0 + W; ++w) top = fmaxf(top, s_ml[w * max_rows + r]);
+#pragma unroll 4
+    for (int w = w0; w < w0 + W; ++w) {
+      const float mw = s_ml[w * max_rows + r];
+      const float f = mw == -INFINITY ? 0.0f : ex2(mw - top);  // -inf: a warp without keys
+      const float4 v = *reinterpret_cast<const float4*>(s_o + (w * max_rows + r) * (D + 4) + col);
+      total += s_ml[(kWarps + w) * max_rows + r] * f;
+      acc[0] += v.x * f;
+      acc[1] += v.y * f;
+      acc[2] += v.z * f;
+      acc[3] += v.w * f;
+    }
+    if (C == 1) {
+      finish(r, col, top, total, acc);
+    } else {
+      *reinterpret_cast<float4*>(o0 + r * (D + 4) + col) = make_float4(acc[0], acc[1], acc[2], acc[3]);
+      if (col == 0) *reinterpret_cast<float2*>(o0 + r * (D + 4) + D) = make_float2(top, total);  // behind the row
+    }
+  }
+  if (C == 1) return;  // (alike for the whole cluster)
   cluster.sync();
   // the window's blocks, each joining its share of the elements
   for (int e = rank + C * tid; e < rows * (D / 4); e += C * kThreads) {
@@ -544,16 +560,15 @@ serve_rows_kernel(ServeArgs a, Split sp) {
     float top = -INFINITY, total = 0.0f, acc[4] = {0.0f, 0.0f, 0.0f, 0.0f};
 #pragma unroll
     for (int b = 0; b < kCluster; ++b) {
-      if (b >= C) break;
-      const float* ro = cluster.map_shared_rank(s_o, rank0 + b) + r * (D + 4);
+      const float* ro = cluster.map_shared_rank(s_o, rank0 + (b & (C - 1))) + r * (D + 4);
       ml[b] = *reinterpret_cast<const float2*>(ro + D);
       v[b] = *reinterpret_cast<const float4*>(ro + col);
+      if (b >= C) ml[b] = make_float2(-INFINITY, 0.0f);
       top = fmaxf(top, ml[b].x);
     }
 #pragma unroll
     for (int b = 0; b < kCluster; ++b) {
-      if (b >= C) break;
-      const float f = ml[b].x == -INFINITY ? 0.0f : exp2f(ml[b].x - top);
+      const float f = ml[b].x == -INFINITY ? 0.0f : ex2(ml[b].x - top);
       total += ml[b].y * f;
       acc[0] += v[b].x * f;
       acc[1] += v[b].y * f;
@@ -575,31 +590,37 @@ int launch(const ServeArgs& a, cudaStream_t st) {
   sp.tokens = most < kRowsMax / sp.heads ? most : kRowsMax / sp.heads;
   sp.row_blocks = ceil_div(most, sp.tokens);
   const long long per_head = static_cast<long long>(a.sq.S) * sp.row_blocks * sp.head_blocks;
-  if (per_head * kCluster * a.H_kv > 0x7fffffffLL) return fail(PLSH_ERR_RANGE, "plsh_paged_fwd: too many rows");
+  if (per_head > 0x7fffffffLL / 64) return fail(PLSH_ERR_RANGE, "plsh_paged_fwd: too many rows");
   sp.per_head = static_cast<int>(per_head);
-  // Blocks of a window: one for each `keys` keys of the widest head's longest block, 256 (a step a warp) while the launch then has
-  // up to four blocks an SM, else the fewest doublings that come near it.
+  // Warps of a window: enough that each has `each` turns of 32 keys of its heads' longest block, the fewest turns with which the
+  // launch's blocks are on the machine at once.
+  const int room = tiles::sm_count() * (D == 128 && !kQuant ? 1 : 2);
   long long clusters = 0;
-  for (int keys = kWarps * kStep; keys <= 4096; keys *= 2) {
-    clusters = 0;
+  for (int each = 1; each <= 1 << 20; each += each < 8 ? 1 : each / 2) {
     long long blocks = 0;
+    clusters = 0;
+    sp.lg_all = 0;
     for (int k = 0; k < a.H_kv; ++k) {
-      int w = 1;
-      for (int h = 0; h < G; ++h) {
-        const int x = a.windows_host ? a.windows_host[k * G + h] : a.max_window;
-        w = x > w ? x : w;
+      int w = 1, lg = 0;
+      for (int h = 0; h < G; ++h) w = a.windows_host[k * G + h] > w ? a.windows_host[k * G + h] : w;
+      while (lg < 6 && (static_cast<long long>(kStep) * each << lg) < w) ++lg;
+      if (a.H_kv > kMaxSplitHeads) {
+        sp.window_all = sp.window_all > w ? sp.window_all : w;
+        sp.lg_all = sp.lg_all > lg ? sp.lg_all : lg;
+        continue;
       }
-      int lg = 0;
-      while (lg < 3 && (static_cast<long long>(keys) << lg) < w) ++lg;
-      if (a.H_kv > kMaxSplitHeads) lg = sp.lg_all = lg > sp.lg_all && k > 0 ? lg : k > 0 ? sp.lg_all : lg;
-      else sp.lg[k] = static_cast<uint8_t>(lg);
-      (a.H_kv > kMaxSplitHeads ? sp.window_all : sp.window[k]) = a.H_kv > kMaxSplitHeads && sp.window_all > w ? sp.window_all : w;
-      blocks += per_head << lg;
-      clusters += ((per_head << lg) + kCluster - 1) / kCluster;
+      sp.window[k] = w;
+      sp.lg[k] = static_cast<uint8_t>(lg);
+      blocks += ((per_head << lg) + kWarps - 1) / kWarps;
+      clusters += clusters_of(sp.per_head, lg);
     }
-    if (a.H_kv > kMaxSplitHeads) clusters = a.H_kv * (((per_head << sp.lg_all) + kCluster - 1) / kCluster);
-    if (blocks <= 4 * 148) break;
+    if (a.H_kv > kMaxSplitHeads) {
+      blocks = a.H_kv * (((per_head << sp.lg_all) + kWarps - 1) / kWarps);
+      clusters = static_cast<long long>(a.H_kv) * clusters_of(sp.per_head, sp.lg_all);
+    }
+    if (blocks <= room) break;
   }
+  if (clusters * kCluster > 0x7fffffffLL) return fail(PLSH_ERR_RANGE, "plsh_paged_fwd: too many rows");
   auto kern = serve_rows_kernel<D, MaskT, kQuant>;
   const int smem = Layout<D, MaskT>(sp.heads, sp.tokens * sp.heads).total;
   cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
