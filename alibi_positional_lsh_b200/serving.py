@@ -25,6 +25,7 @@ _CODES = {torch.bfloat16: PLSH_BF16, torch.float32: PLSH_F32}
 
 
 _EMPTY = (0, 0, 0)
+_FEW = 16  # plsh_paged_fwd needs scratch for more new tokens than this
 
 
 def _stream(stream: Optional[torch.cuda.Stream], device: torch.device) -> int:
@@ -104,12 +105,12 @@ class _On:
             torch.cuda.set_device(self.back)
 
 
-def _empty(shape, dtype: torch.dtype, device: torch.device, stream: Optional[torch.cuda.Stream]) -> torch.Tensor:
-    """A new tensor for work on `stream` (None: the current one)."""
+def _empty(like: torch.Tensor, stream: Optional[torch.cuda.Stream], *shape: int) -> torch.Tensor:
+    """A new tensor of like's type and device for work on `stream` (None: the current one)."""
     if stream is None:
-        return torch.empty(shape, dtype=dtype, device=device)
+        return like.new_empty(*shape)
     with torch.cuda.stream(stream):
-        return torch.empty(shape, dtype=dtype, device=device)
+        return like.new_empty(*shape)
 
 
 class _Errors:
@@ -161,6 +162,7 @@ class PagedCache(_Errors):
                 raise ValueError(f"{nm} must be int8 [num_pages][H_kv][page_size]")
         self.k_pages, self.v_pages, self.k_exp, self.v_exp = k_pages, v_pages, k_exp, v_exp
         self.err = torch.zeros((4,), dtype=torch.int32, device=self.device)
+        self._like = {t: torch.empty((0,), dtype=t, device=self.device) for t in _CODES}  # what new tensors are made from
         self._pages = tuple(0 if x is None else x.data_ptr() for x in (k_pages, v_pages, k_exp, v_exp))
 
     @classmethod
@@ -205,13 +207,14 @@ class PagedCache(_Errors):
             raise ValueError("total must be >= 0")
         with _On(dev.index):
             if out is None:
-                shape = (total, self.H_kv, self.d)
-                out = _empty(shape, dtype, dev, stream), _empty(shape, dtype, dev, stream)
-            K, V = out
-            for x, nm in ((K, "K"), (V, "V")):
-                _rows(x, nm, total, self.H_kv, self.d, dtype, dev)
-                if not x.is_contiguous():
-                    raise ValueError(f"{nm} must be contiguous")
+                like = self._like[dtype]
+                K, V = _empty(like, stream, total, self.H_kv, self.d), _empty(like, stream, total, self.H_kv, self.d)
+            else:
+                K, V = out
+                for x, nm in ((K, "K"), (V, "V")):
+                    _rows(x, nm, total, self.H_kv, self.d, dtype, dev)
+                    if not x.is_contiguous():
+                        raise ValueError(f"{nm} must be contiguous")
             if S and total:
                 _check(_lib.plsh_cache_read(*self._pages, pt, width, self.num_pages, self.page_size, total, S, cu, st, self.H_kv,
                                             self.d, _CODES[dtype], K.data_ptr(), V.data_ptr(), self.err.data_ptr(), _stream(stream, dev)))
@@ -262,14 +265,14 @@ class PlshServing(_Errors):
             self.windows_host = self.bmax.cpu().numpy()  # the heads' longest blocks
         self.max_window = int(self.windows_host.max())
         self._windows = self.windows_host.ctypes.data
+        self._like = tuple(torch.empty((0,), dtype=t, device=self.device) for t in (dtype, torch.float32, torch.uint8))
         self._code, self._err = _CODES[dtype], self.err.data_ptr()
         self._table = self.table_dev.data_ptr()
         self._plan = self.spans.data_ptr(), self.bmask.data_ptr(), 0 if self.near is None else self.near.data_ptr()
 
     def _outputs(self, T: int, out, stream) -> Tuple[torch.Tensor, torch.Tensor]:
         if out is None:
-            return (_empty((T, self.H, self.d), self.dtype, self.device, stream),
-                    _empty((T, self.H), torch.float32, self.device, stream))
+            return _empty(self._like[0], stream, T, self.H, self.d), _empty(self._like[1], stream, T, self.H)
         O, row_sum = out
         _rows(O, "O", T, self.H, self.d, self.dtype, self.device)
         if row_sum.shape != (T, self.H) or row_sum.dtype != torch.float32 or row_sum.device != self.device \
@@ -318,10 +321,10 @@ class PlshServing(_Errors):
             O, row_sum = self._outputs(T, out, stream)
             if S and T:
                 scratch, need = None, 0
-                if cache.quantised and self.near is not None:
+                if most > _FEW and cache.quantised and self.near is not None:
                     need = _lib.plsh_paged_scratch_bytes(T, S, most, self.H_kv, self.d, self.max_window)
                     if need:
-                        scratch = _empty((need,), torch.uint8, dev, stream)
+                        scratch = _empty(self._like[2], stream, need)
                 _check(_lib.plsh_paged_fwd(*qr, self._code, T, S, cu, st, most, self.H, self.H_kv, self.d, *cache._pages, pt, width,
                                            cache.num_pages, cache.page_size, self.s, self.max_len, self._table, *self._plan, self._windows,
                                            scratch.data_ptr() if need else 0, need, O.data_ptr(), row_sum.data_ptr(), self._err,
