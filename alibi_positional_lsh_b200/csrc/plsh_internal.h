@@ -131,7 +131,7 @@ struct ServeArgs {
 };
 constexpr int kFewTokens = 16;
 int launch_serve_rows(const ServeArgs& a, cudaStream_t st);
-int launch_serve_simt(const ServeArgs& a, cudaStream_t st);
+int launch_serve_simt(const ServeArgs& a, cudaStream_t st);  // fp32
 int launch_near(const void* bmask, int H, int s, int n, uint8_t* near, cudaStream_t st);
 size_t serve_scratch_bytes(int T, int S, int H_kv, int d, int max_window);
 int launch_serve_tc(const ServeArgs& a, cudaStream_t st);  // bf16

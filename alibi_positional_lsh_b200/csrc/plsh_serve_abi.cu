@@ -97,8 +97,7 @@ extern "C" int plsh_packed_fwd(const void* Q, int64_t q_token, int64_t q_head, c
   if (int rc = plsh::check_rows(fn, "K", K, dtype, d, H_kv, T, k_token, k_head)) return rc;
   if (int rc = plsh::check_rows(fn, "V", V, dtype, d, H_kv, T, v_token, v_head)) return rc;
   if (int rc = plsh::check_plan(fn, s, tile_span_dev, bmask_dev, O, row_sum, err_dev)) return rc;
-  if (dtype == PLSH_BF16 && (!near_dev || !plsh::aligned16(near_dev)))
-    return fail(PLSH_ERR_INVALID_ARG, "%s: bf16 needs near_dev, 16-byte aligned", fn);
+  if (!near_dev || !plsh::aligned16(near_dev)) return fail(PLSH_ERR_INVALID_ARG, "%s: near_dev must be given, 16-byte aligned", fn);
   plsh::ServeArgs a{};
   a.near = near_dev;
   a.Q = Q; a.qs = {q_token, q_head};
@@ -173,8 +172,7 @@ extern "C" int plsh_paged_fwd(const void* Q, int64_t q_token, int64_t q_head, in
     if (windows_host[h] > max_window) max_window = windows_host[h];
   }
   const bool tiles = dtype == PLSH_BF16 && max_new > plsh::kFewTokens;
-  if (tiles && (!near_dev || !plsh::aligned16(near_dev)))
-    return fail(PLSH_ERR_INVALID_ARG, "%s: bf16 with max_new > %d needs near_dev, 16-byte aligned", fn, plsh::kFewTokens);
+  if (!near_dev || !plsh::aligned16(near_dev)) return fail(PLSH_ERR_INVALID_ARG, "%s: near_dev must be given, 16-byte aligned", fn);
   if (tiles && k_exp) {
     const size_t need = plsh_paged_scratch_bytes(T, S, max_new, H_kv, d, max_window);
     if (!scratch_dev || !plsh::aligned16(scratch_dev) || scratch_bytes < need)

@@ -1,83 +1,129 @@
-// T~ for packed prompts and for chunks against the paged cache, in fp32 on the CUDA cores: the kernel
-// for fp32 inputs (whose tolerance rules the tensor cores out).
+// T~ for packed prompts and against the paged cache, fp32: on the CUDA cores, because its tolerance rules the tensor
+// cores out.
 //
 //   O_i = sum_{j <= i} c_ij e^{S_ij} V_j / sum_{j <= i} c_ij e^{S_ij},  row_sum_i = ln sum_{j <= i} (c_ij / s) e^{S_ij},
 // with c_ij = s - popcount(OR of the boundary masks over (j, i]) (blocks are contiguous).
 //
-// One block per (tile of 64 positions, query head): 64 rows against 64 keys at a time, from the
-// diagonal down to the window's end, with a running maximum and sum. Tiles lie on the grid of
-// absolute positions, so that the counts need one carry per row (the OR from the tile's end to the
-// row) and one suffix OR per key; the diagonal tile's counts are scanned row by row.
+// A cluster of one to four blocks takes a tile of 32 positions of one query head, each block a run of the window's 64-key tiles,
+// from the diagonal down, with a running maximum and sum; the blocks' rows then meet across their shared memory, each
+// block joining a share of the elements, always in the same order. Tiles lie on the grid of absolute positions, so that the counts need
+// one word per row (the OR from the key tile's end to the row) and one suffix OR per key; those of the row's own key
+// tile are the plan's near counts (scanned here, they were a chain of up to 64 dependent steps a block). A thread holds 2 rows x 4 keys of S and 2 rows x d/16 columns of O (4 rows and half
+// as many warps: a key tile took twice as long, for want of warps to hide its trips to shared memory).
+//
+// What bounds it: 4 d multiply-adds a weighted pair at 128 a clock and SM, and for short prompts the length of the longest
+// window, which is why blocks share one (one block a tile of 64 rows: 110 us for three prompts of 1,024, 301 and 699 tokens, 4/2
+// heads, d 64).
+#include <cooperative_groups.h>
+
 #include "plsh_serve.cuh"
+#include "plsh_tile_common.cuh"
 
 namespace plsh {
 namespace {
 
+namespace cg = cooperative_groups;
 using namespace serve;
 
-constexpr int kRows = 64, kKeys = 64, kThreads = 256;
+constexpr int kRows = 32, kKeys = 64, kThreads = 256, kCluster = 4;
+constexpr int kR = kRows / (kThreads / 16);  // rows of a thread
 
 template <int D, typename MaskT>
 struct SimtSmem {
   float q[kRows][D + 4];
-  float k[kKeys][D + 4];
+  float k[kKeys][D + 4];  // in the end the block's rows, with m and l behind each
   float v[kKeys][D];
   float p[kRows][kKeys + 4];
-  MaskT suf[kKeys];      // OR of the masks after key c, up to the tile's last key
-  MaskT bm[kKeys];
-  MaskT carry[kRows];    // OR of the masks from the tile's end (exclusive) to the row
-  uint8_t c[kRows][kKeys];
+  MaskT suf[kKeys];       // OR of the masks after key c, up to the key tile's last
+  MaskT own[kRows];       // OR of the masks from the row's own key tile's first key to the row
+  MaskT gap[kThreads / 32];
+  alignas(16) uint8_t c[kRows][kKeys];
   int sid;
 };
 
-template <typename T, int D, typename MaskT, bool kPaged, bool kQuant>
-__global__ void __launch_bounds__(kThreads) serve_simt_kernel(ServeArgs a) {
+template <int D, typename MaskT, bool kPaged, bool kQuant>
+__global__ void __launch_bounds__(kThreads) serve_simt_kernel(ServeArgs a, int C) {
   extern __shared__ __align__(16) uint8_t smem_raw[];
   auto& sm = *reinterpret_cast<SimtSmem<D, MaskT>*>(smem_raw);
+  cg::cluster_group cluster = cg::this_cluster();  // heads from the last: with the usual slopes, the widest windows first
   if (blockIdx.x == 0 && blockIdx.y == 0) check_seqs(a.sq, a.err);
-  const int tid = threadIdx.x, tx = tid & 15, ty = tid >> 4;
-  const int mult = a.sq.start ? 2 : 1;
-  if (tid < 32) {
-    const int s = warp_find(a.sq.cu, a.sq.S, 6, mult, blockIdx.x);
-    if (tid == 0) sm.sid = s;
+  const int tid = threadIdx.x, tx = tid & 15, ty = tid >> 4, warp = tid >> 5, lane = tid & 31;
+  const int mult = a.sq.start ? 2 : 1, slot = blockIdx.x / C, rank = blockIdx.x % C;
+  if (warp == 0) {
+    const int s = warp_find(a.sq.cu, a.sq.S, kRows == 64 ? 6 : 5, mult, slot);
+    if (lane == 0) sm.sid = s;
   }
   __syncthreads();
   const Seq sq = load_seq(a.sq, sm.sid);
-  const int tile = (sq.pos0 >> 6) + static_cast<int>(blockIdx.x) - ((a.sq.cu[sm.sid] >> 6) + mult * sm.sid);
+  const int tile = (sq.pos0 / kRows) + slot - ((a.sq.cu[sm.sid] / kRows) + mult * sm.sid);
   const int end = sq.pos0 + sq.len;
   const int i0 = tile * kRows;
-  if (tile < 0 || sq.len <= a.few || i0 >= end) return;
-  const int h = blockIdx.y, kvh = h / (a.H / a.pg.H_kv);
+  if (tile < 0 || sq.len == 0 || i0 >= end) return;  // the whole cluster
+  const int h = a.H - 1 - blockIdx.y, kvh = h / (a.H / a.pg.H_kv);
   const MaskT* bm = static_cast<const MaskT*>(a.bmask) + static_cast<size_t>(h) * a.sq.max_len;
   const float sc = 1.4426950408889634f / sqrtf(static_cast<float>(D));
 
+  const int T128 = (a.sq.max_len + PLSH_TILE - 1) / PLSH_TILE;
+  int lo = a.spans[(static_cast<size_t>(h) * T128 + (i0 >> 7)) * 2];
+  if (lo < 0 || lo > i0) {
+    if (tid == 0) atomicOr(a.err, PLSH_DEVERR_WINDOW);
+    lo = i0;
+  }
+  // key tiles diag, diag - 1, ..; this block's run of them
+  const int diag = i0 >> 6, tiles = diag - (lo >> 6) + 1;
+  const int per = (tiles + C - 1) / C, t0 = min(tiles, rank * per), t1 = min(tiles, t0 + per);
   // the row of the packed token at a position, or -1 where the position holds none of the new tokens
   auto token = [&](int p) { return (p >= sq.pos0 && p < end) ? sq.c0 + p - sq.pos0 : -1; };
   for (int e = tid; e < kRows * (D / 4); e += kThreads) {
     const int r = e / (D / 4), c = e % (D / 4) * 4;
     const int t = token(i0 + r);
     float x[4] = {0.0f, 0.0f, 0.0f, 0.0f};
-    if (t >= 0) load4f(static_cast<const T*>(a.Q) + t * a.qs.token + h * a.qs.head + c, x);
-#pragma unroll
-    for (int u = 0; u < 4; ++u) sm.q[r][c + u] = x[u];
+    if (t >= 0) load4f(static_cast<const float*>(a.Q) + t * a.qs.token + h * a.qs.head + c, x);
+    store4f(&sm.q[r][c], x);
   }
 
-  const int T128 = (a.sq.max_len + PLSH_TILE - 1) / PLSH_TILE;
-  int lo = a.spans[(static_cast<size_t>(h) * T128 + (i0 >> 7)) * 2];
-  if (lo < 0 || lo > i0) {
-    if (lo < 0 && tid == 0) atomicOr(a.err, PLSH_DEVERR_WINDOW);
-    lo = lo < 0 ? 0 : i0;
-  }
-  float m[4], l[4] = {0.0f, 0.0f, 0.0f, 0.0f}, acc[4][D / 16];
+  // the OR of the tiles between the diagonal one and the run
+  MaskT gap = 0;
+  for (int j = kKeys * (diag - t0 + 1) + tid; j < kKeys * diag; j += kThreads) gap |= bm[j];
 #pragma unroll
-  for (int r = 0; r < 4; ++r) {
+  for (int o = 16; o >= 1; o >>= 1) gap |= __shfl_xor_sync(0xffffffffu, gap, o);
+  if (lane == 0) sm.gap[warp] = gap;
+  if (warp == 0) {  // ORs from the diagonal tile's first key to each row
+    const MaskT b0 = kKeys * diag + lane < end ? bm[kKeys * diag + lane] : static_cast<MaskT>(0);
+    const MaskT b1 = kKeys * diag + 32 + lane < end ? bm[kKeys * diag + 32 + lane] : static_cast<MaskT>(0);
+    const MaskT u = tiles::warp_prefix_or<MaskT>(b0, lane), v = tiles::warp_prefix_or<MaskT>(b1, lane);
+    const MaskT w = static_cast<MaskT>(__shfl_sync(0xffffffffu, u, 31) | v);
+    if (kRows == 64) {
+      sm.own[lane] = u;
+      sm.own[kRows - 32 + lane] = w;
+    } else {
+      sm.own[lane] = i0 & 32 ? w : u;
+    }
+  }
+  if (t0 == 0)  // the counts in the diagonal tile are the plan's
+    for (int e = tid; e < kRows * (kKeys / 16); e += kThreads) {
+      const int r = e / (kKeys / 16), p = i0 + r;
+      reinterpret_cast<uint4*>(sm.c[r])[e % (kKeys / 16)] =
+          p < end ? __ldg(reinterpret_cast<const uint4*>(a.near + (static_cast<size_t>(h) * a.sq.max_len + p) * kKeys) + e % (kKeys / 16))
+                  : make_uint4(0, 0, 0, 0);
+    }
+  __syncthreads();
+  gap = 0;
+#pragma unroll
+  for (int w = 0; w < kThreads / 32; ++w) gap |= sm.gap[w];
+  float m[kR], l[kR], acc[kR][D / 16];
+#pragma unroll
+  for (int r = 0; r < kR; ++r) {
     m[r] = -INFINITY;
+    l[r] = 0.0f;
 #pragma unroll
     for (int e = 0; e < D / 16; ++e) acc[r][e] = 0.0f;
   }
 
-  for (int j0 = i0; j0 > lo - kKeys && j0 >= 0; j0 -= kKeys) {
-    __syncthreads();  // the previous tile has been read
+  for (int t = t0; t < t1; ++t) {
+    const int j0 = kKeys * (diag - t);
+    __syncthreads();  // the tile before has been read
+#pragma unroll (D == 64 ? 8 : 4)
     for (int e = tid; e < kKeys * (D / 4); e += kThreads) {
       const int r = e / (D / 4), c = e % (D / 4) * 4;
       const int p = j0 + r;
@@ -96,69 +142,61 @@ __global__ void __launch_bounds__(kThreads) serve_simt_kernel(ServeArgs a) {
                 y[u] *= sv;
               }
             } else {
-              load4f(static_cast<const T*>(a.pg.k) + row * D + c, x);
-              load4f(static_cast<const T*>(a.pg.v) + row * D + c, y);
+              load4f(static_cast<const float*>(a.pg.k) + row * D + c, x);
+              load4f(static_cast<const float*>(a.pg.v) + row * D + c, y);
             }
           }
         } else {
-          const long long t = sq.c0 + p;
-          load4f(static_cast<const T*>(a.K) + t * a.ks.token + kvh * a.ks.head + c, x);
-          load4f(static_cast<const T*>(a.V) + t * a.vs.token + kvh * a.vs.head + c, y);
+          const long long tk = sq.c0 + p;
+          load4f(static_cast<const float*>(a.K) + tk * a.ks.token + kvh * a.ks.head + c, x);
+          load4f(static_cast<const float*>(a.V) + tk * a.vs.token + kvh * a.vs.head + c, y);
         }
       }
-#pragma unroll
-      for (int u = 0; u < 4; ++u) {
-        sm.k[r][c + u] = x[u];
-        sm.v[r][c + u] = y[u];
-      }
+      store4f(&sm.k[r][c], x);
+      store4f(&sm.v[r][c], y);
     }
-    if (tid < kKeys) sm.bm[tid] = j0 + tid < end ? bm[j0 + tid] : static_cast<MaskT>(0);
-    __syncthreads();
-    if (tid < kRows) {
-      if (j0 == i0) {  // scan the row's keys from the row down
-        MaskT R = 0;
-        for (int c = kKeys - 1; c >= 0; --c) {
-          if (c > tid) { sm.c[tid][c] = 0; continue; }
-          sm.c[tid][c] = static_cast<uint8_t>(a.s - popc_mask<MaskT>(R));
-          R |= sm.bm[c];
-        }
-        sm.carry[tid] = R;
-      } else {  // suffix ORs of the tile's keys; thread c scans the keys after c
-        MaskT R = 0;
-        for (int c = tid + 1; c < kKeys; ++c) R |= sm.bm[c];
-        sm.suf[tid] = R;
+    MaskT all = 0;  // every mask of the tile (a later tile's gap)
+    if (t > 0) {    // suffix ORs over the tile's keys, two a lane; every warp for itself, the first one for all
+      const MaskT b0 = bm[j0 + 2 * lane], b1 = bm[j0 + 2 * lane + 1];
+      const MaskT inc = tiles::warp_suffix_or<MaskT>(static_cast<MaskT>(b0 | b1), lane);
+      MaskT after = __shfl_down_sync(0xffffffffu, inc, 1);
+      if (lane == 31) after = 0;
+      all = __shfl_sync(0xffffffffu, inc, 0);
+      if (warp == 0) {
+        sm.suf[2 * lane] = static_cast<MaskT>(after | b1 | gap);
+        sm.suf[2 * lane + 1] = static_cast<MaskT>(after | gap);
       }
     }
     __syncthreads();
 
-    float x[4][4];
+    float x[kR][4];
 #pragma unroll
-    for (int r = 0; r < 4; ++r)
+    for (int r = 0; r < kR; ++r)
 #pragma unroll
       for (int e = 0; e < 4; ++e) x[r][e] = 0.0f;
 #pragma unroll 4
     for (int c = 0; c < D; c += 4) {
-      float4 qa[4], ka[4];
+      float4 qa[kR], ka[4];
 #pragma unroll
-      for (int r = 0; r < 4; ++r) qa[r] = *reinterpret_cast<const float4*>(&sm.q[4 * ty + r][c]);
+      for (int r = 0; r < kR; ++r) qa[r] = *reinterpret_cast<const float4*>(&sm.q[kR * ty + r][c]);
 #pragma unroll
       for (int e = 0; e < 4; ++e) ka[e] = *reinterpret_cast<const float4*>(&sm.k[tx + 16 * e][c]);
 #pragma unroll
-      for (int r = 0; r < 4; ++r)
+      for (int r = 0; r < kR; ++r)
 #pragma unroll
         for (int e = 0; e < 4; ++e)
           x[r][e] = fmaf(qa[r].x, ka[e].x, fmaf(qa[r].y, ka[e].y, fmaf(qa[r].z, ka[e].z, fmaf(qa[r].w, ka[e].w, x[r][e]))));
     }
-    float alpha[4];
+    float alpha[kR];
 #pragma unroll
-    for (int r = 0; r < 4; ++r) {
-      const int row = 4 * ty + r;
+    for (int r = 0; r < kR; ++r) {
+      const int row = kR * ty + r;
       int cn[4];
       float top = m[r];
 #pragma unroll
       for (int e = 0; e < 4; ++e) {
         const int key = tx + 16 * e;
-        cn[e] = j0 == i0 ? sm.c[row][key] : a.s - popc_mask<MaskT>(sm.carry[row] | sm.suf[key]);
+        cn[e] = t == 0 ? sm.c[row][key] : a.s - popc_mask<MaskT>(static_cast<MaskT>(sm.own[row] | sm.suf[key]));
         x[r][e] *= sc;
         if (cn[e] > 0) top = fmaxf(top, x[r][e]);
       }
@@ -176,77 +214,119 @@ __global__ void __launch_bounds__(kThreads) serve_simt_kernel(ServeArgs a) {
       m[r] = top;
     }
 #pragma unroll
-    for (int r = 0; r < 4; ++r)
+    for (int r = 0; r < kR; ++r)
 #pragma unroll
       for (int e = 0; e < D / 16; ++e) acc[r][e] *= alpha[r];
-    __syncthreads();
-    if (tid < kRows && j0 != i0) sm.carry[tid] |= static_cast<MaskT>(sm.suf[0] | sm.bm[0]);
-#pragma unroll 2
-    for (int k = 0; k < kKeys; ++k) {
-      float pr[4];
+    __syncwarp();  // a warp's rows of P are its own
+    gap = static_cast<MaskT>(gap | all);
+#pragma unroll 4
+    for (int k = 0; k < kKeys; k += 4) {
+      float4 pr[kR];
 #pragma unroll
-      for (int r = 0; r < 4; ++r) pr[r] = sm.p[4 * ty + r][k];
+      for (int r = 0; r < kR; ++r) pr[r] = *reinterpret_cast<const float4*>(&sm.p[kR * ty + r][k]);
 #pragma unroll
-      for (int e = 0; e < D / 64; ++e) {
-        const float4 vv = *reinterpret_cast<const float4*>(&sm.v[k][64 * e + 4 * tx]);
+      for (int kk = 0; kk < 4; ++kk) {
 #pragma unroll
-        for (int r = 0; r < 4; ++r) {
-          acc[r][4 * e + 0] = fmaf(pr[r], vv.x, acc[r][4 * e + 0]);
-          acc[r][4 * e + 1] = fmaf(pr[r], vv.y, acc[r][4 * e + 1]);
-          acc[r][4 * e + 2] = fmaf(pr[r], vv.z, acc[r][4 * e + 2]);
-          acc[r][4 * e + 3] = fmaf(pr[r], vv.w, acc[r][4 * e + 3]);
+        for (int e = 0; e < D / 64; ++e) {
+          const float4 vv = *reinterpret_cast<const float4*>(&sm.v[k + kk][64 * e + 4 * tx]);
+#pragma unroll
+          for (int r = 0; r < kR; ++r) {
+            const float p = kk == 0 ? pr[r].x : kk == 1 ? pr[r].y : kk == 2 ? pr[r].z : pr[r].w;
+            acc[r][4 * e + 0] = fmaf(p, vv.x, acc[r][4 * e + 0]);
+            acc[r][4 * e + 1] = fmaf(p, vv.y, acc[r][4 * e + 1]);
+            acc[r][4 * e + 2] = fmaf(p, vv.z, acc[r][4 * e + 2]);
+            acc[r][4 * e + 3] = fmaf(p, vv.w, acc[r][4 * e + 3]);
+          }
         }
       }
     }
   }
 
+  auto finish = [&](int t, int col, float top, float total, const float (&o)[4]) {
+    const float inv = 1.0f / total;
+    const float out[4] = {o[0] * inv, o[1] * inv, o[2] * inv, o[3] * inv};
+    store4f(static_cast<float*>(a.O) + (static_cast<size_t>(t) * a.H + h) * D + col, out);
+    if (col == 0)
+      a.row_sum[static_cast<size_t>(t) * a.H + h] = (log2f(total) + top) * 0.6931471805599453f - logf(static_cast<float>(a.s));
+  };
+  if (C > 1) __syncthreads();  // K has been read
 #pragma unroll
-  for (int r = 0; r < 4; ++r) {
+  for (int r = 0; r < kR; ++r) {
     float total = l[r];
 #pragma unroll
     for (int o = 8; o >= 1; o >>= 1) total += __shfl_xor_sync(0xffffffffu, total, o);
-    const int t = token(i0 + 4 * ty + r);
-    if (t < 0) continue;
-    const float inv = 1.0f / total;
+    const int row = kR * ty + r, t = token(i0 + row);
 #pragma unroll
     for (int e = 0; e < D / 64; ++e) {
-      const float o[4] = {acc[r][4 * e] * inv, acc[r][4 * e + 1] * inv, acc[r][4 * e + 2] * inv, acc[r][4 * e + 3] * inv};
-      store4f(static_cast<T*>(a.O) + (static_cast<size_t>(t) * a.H + h) * D + 64 * e + 4 * tx, o);
+      const float o[4] = {acc[r][4 * e], acc[r][4 * e + 1], acc[r][4 * e + 2], acc[r][4 * e + 3]};
+      if (C > 1) store4f(&sm.k[row][64 * e + 4 * tx], o);
+      else if (t >= 0) finish(t, 64 * e + 4 * tx, m[r], total, o);
     }
-    if (tx == 0)
-      a.row_sum[static_cast<size_t>(t) * a.H + h] =
-          (log2f(total) + m[r]) * 0.6931471805599453f - logf(static_cast<float>(a.s));
+    if (C > 1 && tx == 0) {
+      sm.k[row][D] = m[r];
+      sm.k[row][D + 1] = total;
+    }
   }
+  if (C == 1) return;
+  cluster.sync();
+  for (int e = rank + C * tid; e < kRows * (D / 4); e += C * kThreads) {
+    const int row = e / (D / 4), col = e % (D / 4) * 4, t = token(i0 + row);
+    if (t < 0) continue;
+    float top = -INFINITY, total = 0.0f, o[4] = {0.0f, 0.0f, 0.0f, 0.0f};
+    for (int b = 0; b < C; ++b) top = fmaxf(top, cluster.map_shared_rank(&sm.k[row][0], b)[D]);
+    for (int b = 0; b < C; ++b) {
+      const float* ro = cluster.map_shared_rank(&sm.k[row][0], b);
+      const float f = ro[D] == -INFINITY ? 0.0f : exp2f(ro[D] - top);  // -inf: no keys with weight
+      const float4 v = *reinterpret_cast<const float4*>(ro + col);
+      total += ro[D + 1] * f;
+      o[0] += v.x * f;
+      o[1] += v.y * f;
+      o[2] += v.z * f;
+      o[3] += v.w * f;
+    }
+    finish(t, col, top, total, o);
+  }
+  cluster.sync();  // the others have read this block's rows
 }
 
-template <typename T, int D, typename MaskT, bool kPaged, bool kQuant>
+template <int D, typename MaskT, bool kPaged, bool kQuant>
 int launch(const ServeArgs& a, cudaStream_t st) {
-  auto kern = serve_simt_kernel<T, D, MaskT, kPaged, kQuant>;
+  auto kern = serve_simt_kernel<D, MaskT, kPaged, kQuant>;
   const int smem = static_cast<int>(sizeof(SimtSmem<D, MaskT>));
   cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
   if (e != cudaSuccess) return cuda_fail(e, "cudaFuncSetAttribute(serve_simt_kernel)");
-  const dim3 grid(static_cast<unsigned>((a.sq.T >> 6) + (a.sq.start ? 2 : 1) * a.sq.S), a.H);
-  kern<<<grid, kThreads, smem, st>>>(a);
-  e = cudaGetLastError();
+  const long long slots = a.sq.T / kRows + static_cast<long long>(a.sq.start ? 2 : 1) * a.sq.S;
+  // blocks of a row tile: up to four while the launch has fewer than four an SM, and no more than the longest window has key tiles
+  int C = 1;
+  while (C < kCluster && slots * a.H * C < 4 * tiles::sm_count() && C * kKeys < a.sq.max_len) C *= 2;
+  if (slots * C > 0x7fffffffLL) return fail(PLSH_ERR_RANGE, "too many row tiles");
+  cudaLaunchConfig_t cfg{};
+  cfg.gridDim = dim3(static_cast<unsigned>(slots * C), a.H);
+  cfg.blockDim = dim3(kThreads);
+  cfg.dynamicSmemBytes = smem;
+  cfg.stream = st;
+  cudaLaunchAttribute attr{};
+  attr.id = cudaLaunchAttributeClusterDimension;
+  attr.val.clusterDim.x = C;
+  attr.val.clusterDim.y = 1;
+  attr.val.clusterDim.z = 1;
+  cfg.attrs = &attr;
+  cfg.numAttrs = 1;
+  e = cudaLaunchKernelEx(&cfg, kern, a, C);
   return e == cudaSuccess ? PLSH_OK : cuda_fail(e, "serve_simt_kernel launch");
 }
 
-template <typename T, int D, typename MaskT>
+template <int D, typename MaskT>
 int launch_src(const ServeArgs& a, cudaStream_t st) {
-  if (!a.paged) return launch<T, D, MaskT, false, false>(a, st);
-  return a.pg.k_exp ? launch<T, D, MaskT, true, true>(a, st) : launch<T, D, MaskT, true, false>(a, st);
-}
-
-template <typename T>
-int launch_type(const ServeArgs& a, cudaStream_t st) {
-  if (a.d == 128) return a.s <= 32 ? launch_src<T, 128, uint32_t>(a, st) : launch_src<T, 128, unsigned long long>(a, st);
-  return a.s <= 32 ? launch_src<T, 64, uint32_t>(a, st) : launch_src<T, 64, unsigned long long>(a, st);
+  if (!a.paged) return launch<D, MaskT, false, false>(a, st);
+  return a.pg.k_exp ? launch<D, MaskT, true, true>(a, st) : launch<D, MaskT, true, false>(a, st);
 }
 
 }  // namespace
 
 int launch_serve_simt(const ServeArgs& a, cudaStream_t st) {
-  return a.dtype == PLSH_BF16 ? launch_type<__nv_bfloat16>(a, st) : launch_type<float>(a, st);
+  if (a.d == 128) return a.s <= 32 ? launch_src<128, uint32_t>(a, st) : launch_src<128, unsigned long long>(a, st);
+  return a.s <= 32 ? launch_src<64, uint32_t>(a, st) : launch_src<64, unsigned long long>(a, st);
 }
 
 }  // namespace plsh

@@ -257,10 +257,8 @@ class PlshServing(_Errors):
             self.spans = torch.empty((H, -(-max_len // PLSH_TILE), 2), dtype=torch.int32, device=self.device)
             self.bmask = torch.empty((H, max_len), dtype=torch.int32 if s <= 32 else torch.int64, device=self.device)
             plsh_window_from_table(self.table_dev, H, s, max_len, 1, self.bmax, self.spans, self.bmask, self.err)
-            self.near = None  # counts of each position's own 64-key tile: H * max_len * 64 bytes
-            if dtype == torch.bfloat16:
-                self.near = torch.empty((H, max_len, 64), dtype=torch.uint8, device=self.device)
-                plsh_near_counts(self.bmask, H, s, max_len, self.near)
+            self.near = torch.empty((H, max_len, 64), dtype=torch.uint8, device=self.device)  # each position's counts in its own key tile
+            plsh_near_counts(self.bmask, H, s, max_len, self.near)
             self.check()  # waits for the plan, so that any stream may use it from here on
             self.windows_host = self.bmax.cpu().numpy()  # the heads' longest blocks
         self.max_window = int(self.windows_host.max())
@@ -268,7 +266,7 @@ class PlshServing(_Errors):
         self._like = tuple(torch.empty((0,), dtype=t, device=self.device) for t in (dtype, torch.float32, torch.uint8))
         self._code, self._err = _CODES[dtype], self.err.data_ptr()
         self._table = self.table_dev.data_ptr()
-        self._plan = self.spans.data_ptr(), self.bmask.data_ptr(), 0 if self.near is None else self.near.data_ptr()
+        self._plan = self.spans.data_ptr(), self.bmask.data_ptr(), self.near.data_ptr()
 
     def _outputs(self, T: int, out, stream) -> Tuple[torch.Tensor, torch.Tensor]:
         if out is None:
@@ -321,7 +319,7 @@ class PlshServing(_Errors):
             O, row_sum = self._outputs(T, out, stream)
             if S and T:
                 scratch, need = None, 0
-                if most > _FEW and cache.quantised and self.near is not None:
+                if most > _FEW and cache.quantised and self.dtype == torch.bfloat16:
                     need = _lib.plsh_paged_scratch_bytes(T, S, most, self.H_kv, self.d, self.max_window)
                     if need:
                         scratch = _empty(self._like[2], stream, need)

@@ -516,7 +516,7 @@ PLSH_API int plsh_attention_bwd_tc(const void* Q, const void* K, const void* V, 
  *   O[t][h]       = sum_{j <= i} c_ij e^{S_ij} V_j / sum_{j <= i} c_ij e^{S_ij},
  *   row_sum[t][h] = ln( sum_{j <= i} (c_ij / s) e^{S_ij} ),
  * j over the sequence's own positions.
- *   near_dev [H][max_len][64] from plsh_near_counts; bf16 needs it, fp32 takes NULL.
+ *   near_dev [H][max_len][64] from plsh_near_counts.
  *   O        [T][H][d] out, row_sum [T][H] float32 out.
  */
 PLSH_API int plsh_packed_fwd(const void* Q, int64_t q_token, int64_t q_head, const void* K, int64_t k_token,
@@ -568,7 +568,7 @@ PLSH_API int plsh_cache_read(const void* k_pages, const void* v_pages, const int
  *             PLSH_DEVERR_SEQUENCE, and it is skipped). The call chooses its kernels by it,
  *             so give the largest length where it is known, or T.
  *   table_dev the plan's (delta, u), [H][s][2].
- *   near_dev  as plsh_packed_fwd; bf16 with max_new > 16 needs it.
+ *   near_dev  as plsh_packed_fwd.
  *   windows_host  [H] int32 on the host: each head's longest block, plsh_window's
  *             bmax_dev (a copy, made once with the plan).
  *   scratch_dev, scratch_bytes  device scratch of at least
