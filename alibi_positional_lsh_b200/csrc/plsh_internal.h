@@ -130,6 +130,7 @@ struct ServeArgs {
   void* O; float* row_sum; uint32_t* err;
 };
 constexpr int kFewTokens = 16;
+int rows_block_tokens(int group);
 int launch_serve_rows(const ServeArgs& a, cudaStream_t st);
 int launch_serve_simt(const ServeArgs& a, cudaStream_t st);  // fp32
 int launch_near(const void* bmask, int H, int s, int n, uint8_t* near, cudaStream_t st);

@@ -194,7 +194,7 @@ extern "C" int plsh_paged_fwd(const void* Q, int64_t q_token, int64_t q_head, in
   a.O = O; a.row_sum = row_sum; a.err = err_dev;
   const cudaStream_t st = static_cast<cudaStream_t>(stream);
   if (dtype == PLSH_BF16) {
-    a.few = plsh::kFewTokens;
+    a.few = tiles ? plsh::rows_block_tokens(H / H_kv) : plsh::kFewTokens;
     if (int rc = plsh::launch_serve_rows(a, st)) return rc;
     return tiles ? plsh::launch_serve_tc(a, st) : PLSH_OK;
   }
