@@ -28,6 +28,10 @@
 // full relative precision, so no maximum is taken otherwise; the tile is then done again
 // with m = the maximum over its keys with c > 0. No score of a key without weight can push a row's weights out of range.
 //
+// P is rounded to bf16 for the second product. O is divided by the sum of the rounded P over the row's own 32 keys (a block of the warp's) and of P
+// before them, which takes back most of that rounding where few keys carry the weight (a row's only key then gives its V exactly) and
+// costs nothing outside those tiles; row_sum is of P itself.
+//
 // Rows past a sequence's end hold another sequence's data: their K and V rows are cleared in shared memory before the
 // products, so that nothing there, not even a NaN, meets a zero weight: a sequence's result has the same bits whatever it is packed with.
 //
@@ -66,6 +70,16 @@ struct Item {
   int valid, h, i0, c0, pos0, end, s, top, low;
   int kv0;  // row of K and V that holds position 0
 };
+
+// The sum of 32 bf16, in fp32.
+__device__ __forceinline__ float sum_bf16(const uint32_t (&w)[16]) {
+  float s[4] = {0.0f, 0.0f, 0.0f, 0.0f};
+#pragma unroll
+  for (int i = 0; i < 16; ++i)
+    asm("{.reg .b16 lo, hi;\n mov.b32 {lo, hi}, %2;\n add.rn.f32.bf16 %0, lo, %0;\n add.rn.f32.bf16 %1, hi, %1;}"
+        : "+f"(s[2 * (i & 1)]), "+f"(s[2 * (i & 1) + 1]) : "r"(w[i]));
+  return (s[0] + s[1]) + (s[2] + s[3]);
+}
 
 template <int D, typename MaskT>
 struct __align__(1024) TcSmem {
@@ -296,7 +310,7 @@ serve_tc_kernel(const __grid_constant__ CUtensorMap tmap_q, const __grid_constan
     const float sc = 1.4426950408889634f / sqrtf(static_cast<float>(D));
     int g = 0, items = 0;
     int d_at = -1;  // the finished item's row of O (-1: none) and its sum and reference, until its epilogue
-    float d_l = 1.0f, d_m = 0.0f;
+    float d_l = 1.0f, d_m = 0.0f, d_norm = 1.0f;
     bool pending = false;
     bool ok = true;
     for (int k = 0; ok; ++k) {
@@ -310,7 +324,7 @@ serve_tc_kernel(const __grid_constant__ CUtensorMap tmap_q, const __grid_constan
       const uint4* near = reinterpret_cast<const uint4*>(prm.near + (static_cast<size_t>(item.h) * max_len + (at >= 0 ? i0 + r : 0)) * kKeys);
       __syncwarp();
       if (lane == 0) mbar_arrive(&sm.item_empty[k % kItems]);
-      float m2 = 0.0f, l = 0.0f;
+      float m2 = 0.0f, l = 0.0f, dl = 0.0f;  // dl: what rounding P to bf16 adds to l, in the row's own 32 keys
       MaskT pre = 0, mid = 0;
       for (int u = first; done ? pending : u >= low; --u, ++g) {
         if (!done) {
@@ -412,6 +426,7 @@ serve_tc_kernel(const __grid_constant__ CUtensorMap tmap_q, const __grid_constan
                   m2 = m_new;
                 }
                 l *= alpha;
+                dl *= alpha;
                 lsum *= alpha;
                 tmem_wait_st();
                 const uint32_t alpha2 = pack_bf16x2(alpha, alpha);
@@ -446,6 +461,7 @@ serve_tc_kernel(const __grid_constant__ CUtensorMap tmap_q, const __grid_constan
                 hsum = (ls[0] + ls[1]) + (ls[2] + ls[3]);
               }
               lsum += hsum;
+              if (own && hf == (rg & 1)) dl += sum_bf16(pk) - hsum;
             }
             tmem_st16(base + kColC + 16u * hf, pk);
           };
@@ -469,7 +485,7 @@ serve_tc_kernel(const __grid_constant__ CUtensorMap tmap_q, const __grid_constan
         if (!wait_all(&sm.o_full, items - 1)) { ok = false; break; }
         tc_fence_after();
         {
-          const float inv = 1.0f / d_l;
+          const float inv = 1.0f / d_norm;
           uint32_t o[D / 2];
 #pragma unroll
           for (int c = 0; c < D; c += 32) {
@@ -493,6 +509,7 @@ serve_tc_kernel(const __grid_constant__ CUtensorMap tmap_q, const __grid_constan
       if (done) break;
       d_at = at;
       d_l = l;
+      d_norm = l + dl;
       d_m = m2;
       pending = true;
       ++items;
