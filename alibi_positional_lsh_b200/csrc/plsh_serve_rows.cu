@@ -7,7 +7,9 @@
 //   S^T[16 keys][8 rows] = K Q^T   d/16 products mma.m16n8k16, fp32 accumulation
 //   P = c 2^(S sc - m), against the warp's own running maximum m over keys with c > 0
 //   O^T[d][8 rows] += V^T P^T      d/16 products
-// and the partial rows (m, l, O) meet at the end, the warps' in shared memory and the blocks' across it (distributed shared
+// O is divided by the sum of the P that it was made with, rounded to bf16 (a row's only key then gives its V exactly; with few
+// keys it takes back most of that rounding); row_sum is of P itself.
+// The partial rows (m, the sums, O) meet at the end, the warps' in shared memory and the blocks' across it (distributed shared
 // memory): one launch, no scratch, and always joined in the same order, so results do not depend on timing. Teams are
 // sized so that the launch fits the machine at once: narrow windows with a block each left a second wave of blocks whose
 // time is all trips to memory (64 sequences, 16/8 heads, d 128, e4m3: 39 us).
@@ -71,7 +73,7 @@ struct Layout {
       return here;
     };
     o = take(kWarps * rows * (D + 4) * 4);         // [warp][row][D + 4]: the warps' rows of O
-    ml = take(2 * kWarps * rows * 4);              // [2][warp][row]: their m and l
+    ml = take(3 * kWarps * rows * 4);              // [3][warp][row]: their m, l and lr
     begin = take(kWarps * heads * PLSH_MAX_S * 4); // [team, at its first warp][head][hash]: where p0's block begins
     keep = take(2 * kWarps * heads * kStep * (int)sizeof(MaskT));  // [stage][warp][head][key]: hashes whose block reaches the key
     row_off = take(kWarps * rows * (int)sizeof(MaskT));  // [team][row]: hashes that open a block in (p0, i]
@@ -281,7 +283,7 @@ serve_rows_kernel(ServeArgs a, Split sp) {
   for (int i = 0; i < D / 16; ++i)
 #pragma unroll
     for (int e = 0; e < 4; ++e) o[i][e] = 0.0f;
-  float m[2] = {-INFINITY, -INFINITY}, l[2] = {0.0f, 0.0f};  // of rows 2 t and 2 t + 1; l: this lane's keys only
+  float m[2] = {-INFINITY, -INFINITY}, l[2] = {0.0f, 0.0f}, lr[2] = {0.0f, 0.0f};  // of rows 2 t and 2 t + 1; l, and lr of the rounded weights: this lane's keys only
   team_sync();
   MaskT mine[2] = {0, 0};  // the hashes that may count for the two rows, and the rows' heads in the group
   int hh[2] = {0, 0};
@@ -361,6 +363,7 @@ serve_rows_kernel(ServeArgs a, Split sp) {
         const float alpha = now == -INFINITY ? 1.0f : ex2(m[u] - now);  // 0 the first time
         m[u] = now;
         l[u] *= alpha;
+        lr[u] *= alpha;
 #pragma unroll
         for (int i = 0; i < D / 16; ++i) {
           o[i][u] *= alpha;
@@ -377,7 +380,13 @@ serve_rows_kernel(ServeArgs a, Split sp) {
       for (int u = 0; u < 2; ++u) {
         w[u] = c[n][u] ? static_cast<float>(c[n][u]) * ex2(x[n][u] - m[u]) : 0.0f;
         l[u] += w[u];
-        if (kQuant) w[u] = c[n][u] ? w[u] * vs : 0.0f;
+      }
+      const uint32_t wr = bf16x2(w[0], w[1]);
+      lr[0] += bf16_lo(wr);
+      lr[1] += bf16_hi(wr);
+      if (kQuant) {
+#pragma unroll
+        for (int u = 0; u < 2; ++u) w[u] = c[n][u] ? w[u] * vs : 0.0f;
       }
       b[n] = transpose8(bf16x2(w[0], w[1]));  // row g, keys 8 n + 2 t, + 1
     }
@@ -507,20 +516,24 @@ serve_rows_kernel(ServeArgs a, Split sp) {
 #pragma unroll
   for (int u = 0; u < 2; ++u) {
 #pragma unroll
-    for (int s = 4; s <= 16; s <<= 1) l[u] += __shfl_xor_sync(0xffffffffu, l[u], s);
+    for (int s = 4; s <= 16; s <<= 1) {
+      l[u] += __shfl_xor_sync(0xffffffffu, l[u], s);
+      lr[u] += __shfl_xor_sync(0xffffffffu, lr[u], s);
+    }
     const int r = 2 * t + u;
     if (r >= rows) continue;
     if (g == 0) {
       s_ml[warp * max_rows + r] = m[u];
       s_ml[(kWarps + warp) * max_rows + r] = l[u];
+      s_ml[(2 * kWarps + warp) * max_rows + r] = lr[u];
     }
 #pragma unroll
     for (int i = 0; i < D / 16; ++i)
       *reinterpret_cast<float2*>(s_o + (warp * max_rows + r) * (D + 4) + (D / 8) * g + 2 * i) = make_float2(o[i][u], o[i][2 + u]);
   }
   team_sync();
-  auto finish = [&](int r, int col, float top, float total, const float (&acc)[4]) {
-    const float inv = 1.0f / total;
+  auto finish = [&](int r, int col, float top, float total, float norm, const float (&acc)[4]) {
+    const float inv = 1.0f / norm;
     const size_t at = static_cast<size_t>(c0 + r / nh) * a.H + h0 + r % nh;
     const float out[4] = {acc[0] * inv, acc[1] * inv, acc[2] * inv, acc[3] * inv};
     store4f(static_cast<__nv_bfloat16*>(a.O) + at * D + col, out);
@@ -530,7 +543,7 @@ serve_rows_kernel(ServeArgs a, Split sp) {
   float* const o0 = s_o + w0 * max_rows * (D + 4);
   for (int e = team_tid; e < rows * (D / 4); e += team_threads) {
     const int r = e / (D / 4), col = e % (D / 4) * 4;
-    float top = -INFINITY, total = 0.0f, acc[4] = {0.0f, 0.0f, 0.0f, 0.0f};
+    float top = -INFINITY, total = 0.0f, norm = 0.0f, acc[4] = {0.0f, 0.0f, 0.0f, 0.0f};
     for (int w = w0; w < w0 + W; ++w) top = fmaxf(top, s_ml[w * max_rows + r]);
 #pragma unroll 4
     for (int w = w0; w < w0 + W; ++w) {
@@ -538,16 +551,17 @@ serve_rows_kernel(ServeArgs a, Split sp) {
       const float f = mw == -INFINITY ? 0.0f : ex2(mw - top);  // -inf: a warp without keys
       const float4 v = *reinterpret_cast<const float4*>(s_o + (w * max_rows + r) * (D + 4) + col);
       total += s_ml[(kWarps + w) * max_rows + r] * f;
+      norm += s_ml[(2 * kWarps + w) * max_rows + r] * f;
       acc[0] += v.x * f;
       acc[1] += v.y * f;
       acc[2] += v.z * f;
       acc[3] += v.w * f;
     }
     if (C == 1) {
-      finish(r, col, top, total, acc);
+      finish(r, col, top, total, norm, acc);
     } else {
       *reinterpret_cast<float4*>(o0 + r * (D + 4) + col) = make_float4(acc[0], acc[1], acc[2], acc[3]);
-      if (col == 0) *reinterpret_cast<float2*>(o0 + r * (D + 4) + D) = make_float2(top, total);  // behind the row
+      if (col == 0) *reinterpret_cast<float4*>(o0 + r * (D + 4) + D) = make_float4(top, total, norm, 0.0f);  // behind the row
     }
   }
   if (C == 1) return;  // (alike for the whole cluster)
@@ -555,27 +569,28 @@ serve_rows_kernel(ServeArgs a, Split sp) {
   // the window's blocks, each joining its share of the elements
   for (int e = rank + C * tid; e < rows * (D / 4); e += C * kThreads) {
     const int r = e / (D / 4), col = e % (D / 4) * 4;
-    float2 ml[kCluster];
+    float4 ml[kCluster];
     float4 v[kCluster];
-    float top = -INFINITY, total = 0.0f, acc[4] = {0.0f, 0.0f, 0.0f, 0.0f};
+    float top = -INFINITY, total = 0.0f, norm = 0.0f, acc[4] = {0.0f, 0.0f, 0.0f, 0.0f};
 #pragma unroll
     for (int b = 0; b < kCluster; ++b) {
       const float* ro = cluster.map_shared_rank(s_o, rank0 + (b & (C - 1))) + r * (D + 4);
-      ml[b] = *reinterpret_cast<const float2*>(ro + D);
+      ml[b] = *reinterpret_cast<const float4*>(ro + D);
       v[b] = *reinterpret_cast<const float4*>(ro + col);
-      if (b >= C) ml[b] = make_float2(-INFINITY, 0.0f);
+      if (b >= C) ml[b].x = -INFINITY;
       top = fmaxf(top, ml[b].x);
     }
 #pragma unroll
     for (int b = 0; b < kCluster; ++b) {
       const float f = ml[b].x == -INFINITY ? 0.0f : ex2(ml[b].x - top);
       total += ml[b].y * f;
+      norm += ml[b].z * f;
       acc[0] += v[b].x * f;
       acc[1] += v[b].y * f;
       acc[2] += v[b].z * f;
       acc[3] += v[b].w * f;
     }
-    finish(r, col, top, total, acc);
+    finish(r, col, top, total, norm, acc);
   }
   cluster.sync();  // the others have read this block's rows
 }
