@@ -63,9 +63,6 @@ __device__ __forceinline__ int warp_find(const int32_t* cu, int S, int lg_tile, 
   return lo;
 }
 
-// The sequence of packed token t.
-__device__ __forceinline__ int warp_find_token(const int32_t* cu, int S, int t) { return warp_find(cu, S, 0, 0, t); }
-
 // ---------------------------------------------------------------- pages
 
 // The row (page, head, place in the page) of position p, or -1 (and PLSH_DEVERR_PAGE) where the page table has none.

@@ -937,7 +937,7 @@ int launch(const ServeArgs& a, cudaStream_t st) {
   prm.items = prm.slots * a.H;
   prm.spans = a.spans;
   prm.near = a.near;
-  prm.wait_limit = static_cast<uint32_t>(wait_limit_ns() >> 20);
+  prm.wait_limit = static_cast<uint32_t>(wait_limit_ns() >> 20) + 1;  // rounded up: a wait never ends before the limit
   prm.log_s = std::log(static_cast<float>(a.s));
   prm.withhold_mma = withhold_mma() ? 1 : 0;
   auto kern = serve_tc_kernel<D, MaskT, kPaged>;

@@ -85,9 +85,10 @@ PLSH_API int plsh_version(void);
  *
  * Every wait of the tensor-core attention kernel (plsh_attention_fwd,
  * plsh_attention_varlen_fwd[_static], plsh_alibi_banded_fwd with bf16,
- * d = 128), of the tensor-core backward (plsh_attention_bwd_tc) and of the
- * decode kernels (plsh_decode_fwd) on one of its roles is bounded in
- * wall-clock time. A wait that runs out sets PLSH_DEVERR_TIMEOUT in err_dev;
+ * d = 128), of the tensor-core backward (plsh_attention_bwd_tc), of the
+ * serving tile kernel (plsh_packed_fwd, and plsh_paged_fwd's longer
+ * sequences, with bf16) and of the decode kernels (plsh_decode_fwd) on one of
+ * its roles is bounded in wall-clock time. A wait that runs out sets PLSH_DEVERR_TIMEOUT in err_dev;
  * every role then leaves its loop, copies and tensor-core operations already
  * in flight are drained (with a separate limit of 0.1 s), Tensor Memory is
  * freed and the kernel returns, so the context stays usable. The outputs of
@@ -507,7 +508,7 @@ PLSH_API int plsh_attention_bwd_tc(const void* Q, const void* K, const void* V, 
  *   - K and V must be finite: a NaN or an infinity may reach any row of
  *     its own sequence near it, weighted or not, but no other sequence.
  *   - Two sequences that share pages may read them in one call; a call in
- *     which two tokens are written to one place leaves either.
+ *     which two tokens are written to one place leaves that row undefined.
  *
  * plsh_packed_fwd -- T~ of whole prompts.
  *
@@ -572,9 +573,11 @@ PLSH_API int plsh_cache_read(const void* k_pages, const void* v_pages, const int
  *   windows_host  [H] int32 on the host: each head's longest block, plsh_window's
  *             bmax_dev (a copy, made once with the plan).
  *   scratch_dev, scratch_bytes  device scratch of at least
- *             plsh_paged_scratch_bytes(.., the largest of windows_host) bytes, 16-byte aligned (NULL where that is 0, with pages of the call's dtype, and for fp32):
- *             bf16 copies of the e4m3 rows that sequences with more than 16
- *             new tokens reach. Nothing in it needs clearing.
+ *             plsh_paged_scratch_bytes(.., the largest of
+ *             windows_host) bytes, 16-byte aligned (NULL where that is 0, with
+ *             pages of the call's dtype, and for fp32): bf16 copies of the
+ *             e4m3 rows that the longer sequences of a call with max_new > 16
+ *             reach. Nothing in it needs clearing.
  */
 PLSH_API size_t plsh_paged_scratch_bytes(int T, int S, int max_new, int H_kv, int d, int max_window);
 PLSH_API int plsh_paged_fwd(const void* Q, int64_t q_token, int64_t q_head, int dtype, int T, int S,

@@ -3,7 +3,8 @@
 Tolerances (derived; eps/2 is the largest relative error of one rounding):
   scores   a dot of d products in fp32 with any order and truncation: |dS| <= (d + 4) 2^-23 sum|q k| / sqrt d =: e
   row_sum  a mean of exponents: e, plus the exponential, logarithm and sums in fp32: 2^-20 + 2^-22 |row_sum|
-  O        weights P / l move by 2 e + 2^-19 relatively, and by 2^-8 when P is rounded to bf16 for the tensor cores (bf16 inputs);
+  O        weights P / l move by 2 e + 2^-19 relatively; with bf16 inputs by 2^-8 more as P is rounded to bf16 for the tensor cores,
+           and by up to 2^-8 again as l may be a sum of rounded P (a mean of factors within 2^-8 of 1);
            the result is rounded once (2^-8 of bf16, 2^-24 of fp32); sums of n terms in fp32 move by n 2^-24; all relative to
            sum_j w_j |V_j|
 """
@@ -42,7 +43,7 @@ def check(O, R, want, dtype, what=""):
     wO, wR, A, E = want
     d, n = O.shape[-1], 4096
     e = (d + 4) * 2.0 ** -23 * E
-    rel = 2 * e + 2.0 ** -19 + n * 2.0 ** -24 + (2 * 2.0 ** -8 if dtype == torch.bfloat16 else 2.0 ** -24)
+    rel = 2 * e + 2.0 ** -19 + n * 2.0 ** -24 + (3 * 2.0 ** -8 if dtype == torch.bfloat16 else 2.0 ** -24)
     off = ((O.double() - wO).abs() - rel[..., None] * A - 1e-30).max().item()
     assert off <= 0, f"{what}: O is {off} over its tolerance"
     roff = ((R.double() - wR).abs() - e - 2.0 ** -20 - 2.0 ** -22 * wR.abs()).max().item()

@@ -610,3 +610,203 @@ def test_refusals_of_the_python_layer():
     with pytest.raises(ValueError):
         _cache(2, 2, 16, 128, BF16).append(k.float(), k.float(), pt, cu, st)
     plan.check()
+
+
+# ---------------------------------------------------------------- at the edges
+
+
+@pytest.mark.parametrize("d,dtype", [(128, BF16), (64, BF16), (64, F32)])
+def test_a_rows_only_key_gives_its_value_exactly(d, dtype):
+    """One key: O is its V, whatever the score (the weight and the sum are rounded alike), and row_sum the score."""
+    H, H_kv, S = 6, 3, 40
+    plan, g = _plan(H, H_kv, 64, d, 20, dtype), _gen(60)
+    q, k, v = _randn(g, S, H, d, dtype=dtype), *_randn(g, 2, S, H_kv, d, dtype=dtype)
+    want = v.repeat_interleave(2, 1)
+    # one product p V, one quotient (p V) (1 / p): 2^-24 each and the reciprocal's 2^-23, far inside half a step of bf16
+    near = 2.0 ** -22 if dtype == F32 else 0.0
+    cu, zero = _cu([1] * S), torch.zeros(S, dtype=torch.int32, device="cuda:0")
+    O, R = plan.attend_packed(q, k, v, cu)
+    score = (q.double() * k.double().repeat_interleave(2, 1)).sum(-1) / d ** 0.5
+    e = (d + 4) * 2.0 ** -23 * (q.double() * k.double().repeat_interleave(2, 1)).abs().sum(-1) / d ** 0.5
+    assert ((O.double() - want.double()).abs() <= near * want.double().abs()).all()
+    assert ((R.double() - score).abs() <= e + 2.0 ** -20 + 2.0 ** -22 * score.abs()).all()
+    pt = torch.arange(S, dtype=torch.int32, device="cuda:0").view(S, 1)
+    cache = _cache(S, H_kv, 16, d, dtype)
+    cache.append(k, v, pt, cu, zero)
+    for most in (1, None):
+        O, R = plan.attend_paged(q, cache, pt, cu, zero, max_new=most)
+        assert ((O.double() - want.double()).abs() <= near * want.double().abs()).all()
+        assert ((R.double() - score).abs() <= e + 2.0 ** -20 + 2.0 ** -22 * score.abs()).all()
+    plan.check()
+    cache.check()
+
+
+@pytest.mark.parametrize("H,H_kv,lens,starts", [
+    (72, 72, [1, 2], [100, 0]),            # more KV heads than the rows kernel splits one by one
+    (80, 80, [40, 1, 3], [7, 130, 64]),
+    (24, 2, [1, 5], [300, 64]),            # twelve query heads to a KV head: two blocks of them
+    (24, 2, [70, 1, 2], [30, 200, 5]),
+    (264, 8, [150, 1], [0, 90]),           # more heads than the tile kernel sorts
+])
+def test_paged_many_heads(H, H_kv, lens, starts):
+    d, page = 64, 32
+    ends = [a + b for a, b in zip(lens, starts)]
+    plan, g = _plan(H, H_kv, max(ends) + 3, d, 12, BF16), _gen(61)
+    pt, num = _table_of(ends, page)
+    cache = _cache(num, H_kv, page, d, E4M3)
+    K, V = _fill(cache, ends, pt, g, H_kv, d, BF16)
+    q, st = _randn(g, sum(lens), H, d), torch.tensor(starts, dtype=torch.int32, device="cuda:0")
+    O, R = plan.attend_paged(q, cache, pt, _cu(lens), st, max_new=max(lens))
+    plan.check()
+    t = at = 0
+    for n, (L, a) in enumerate(zip(lens, starts)):
+        want = plain.sequence(q[t:t + L].double(), K[at:at + a + L], V[at:at + a + L], plan.table_host, a)
+        plain.check(O[t:t + L], R[t:t + L], want, BF16, f"sequence {n}")
+        t, at = t + L, at + ends[n]
+    T = sum(ends)
+    q = _randn(g, T, H, d)
+    O, R = plan.attend_packed(q, K.to(BF16), V.to(BF16), _cu(ends))
+    plan.check()
+    _check_packed(plan, O, R, q, K.to(BF16), V.to(BF16), ends)
+
+
+@pytest.mark.parametrize("lens", [[1, 4, 5, 16, 17], [16, 1, 16], [3, 17, 2, 4]])
+def test_sequences_on_either_side_of_the_kernels_limits(lens):
+    # 8 rows, here 4 tokens, of a block; 16 tokens of the rows kernel's longest call
+    H, H_kv, d, page, starts = 4, 2, 128, 16, [90, 0, 33, 15, 64][:len(lens)]
+    ends = [a + b for a, b in zip(lens, starts)]
+    plan, g = _plan(H, H_kv, 200, d, 20, BF16), _gen(62)
+    pt, num = _table_of(ends, page)
+    cache = _cache(num, H_kv, page, d, E4M3)
+    K, V = _fill(cache, ends, pt, g, H_kv, d, BF16)
+    q, st = _randn(g, sum(lens), H, d), torch.tensor(starts, dtype=torch.int32, device="cuda:0")
+    for most in (max(lens), None):
+        O, R = plan.attend_paged(q, cache, pt, _cu(lens), st, max_new=most)
+        plan.check()
+        t = at = 0
+        for n, (L, a) in enumerate(zip(lens, starts)):
+            want = plain.sequence(q[t:t + L].double(), K[at:at + a + L], V[at:at + a + L], plan.table_host, a)
+            plain.check(O[t:t + L], R[t:t + L], want, BF16, f"sequence {n}")
+            t, at = t + L, at + ends[n]
+
+
+@pytest.mark.parametrize("kind", [E4M3, BF16])
+def test_a_pool_past_32_bit_offsets(kind):
+    """Pages whose first element lies past 2^32 elements of the pool."""
+    from alibi_positional_lsh_b200 import PagedCache
+    H, H_kv, d, page = 4, 1, 128, 256
+    num = (1 << 32) // (page * H_kv * d) + 4
+    cache = PagedCache.empty(num, H_kv, page, d, kind, "cuda:0")
+    pt = torch.tensor([[num - 1, num - 3], [num - 2, num - 4]], dtype=torch.int32, device="cuda:0")
+    plan, g = _plan(H, H_kv, 512, d, 20, BF16), _gen(63)
+    ends, zero = [400, 290], torch.zeros(2, dtype=torch.int32, device="cuda:0")
+    k, v = _randn(g, 2, 690, H_kv, d)
+    cache.append(k, v, pt, _cu(ends), zero)
+    K, V = cache.read(pt, _cu(ends), zero, 690)
+    cache.check()
+    if kind == BF16:
+        assert torch.equal(K, k) and torch.equal(V, v)
+    else:  # half a step of e4m3 relative to the row's scale: 2^-4 of a value, 2^-10 of 2^e below its normal numbers
+        assert ((K.double() - k.double()).abs() <= 2.0 ** -4 * k.double().abs() + 2.0 ** -10 * k.double().abs().amax(-1, keepdim=True) / 224).all()
+    for n in (1, 30):
+        q, st = _randn(g, 2 * n, H, d), torch.tensor([400 - n, 290 - n], dtype=torch.int32, device="cuda:0")
+        O, R = plan.attend_paged(q, cache, pt, _cu([n, n]), st, max_new=n)
+        plan.check()
+        for s, (a, b) in enumerate(((0, 400), (400, 690))):
+            want = plain.sequence(q[n * s:n * s + n].double(), K[a:b].double(), V[a:b].double(), plan.table_host, b - a - n)
+            plain.check(O[n * s:n * s + n], R[n * s:n * s + n], want, BF16, f"{n} tokens, sequence {s}")
+
+
+@pytest.mark.parametrize("bad", [float("nan"), float("inf")])
+def test_a_query_that_is_not_finite_spoils_its_own_row_only(bad):
+    H, H_kv, d, page = 4, 2, 128, 64
+    plan, g = _plan(H, H_kv, 300, d, 20, BF16), _gen(64)
+    pt, num = _table_of([250], page)
+    cache = _cache(num, H_kv, page, d, E4M3)
+    K, V = _fill(cache, [250], pt, g, H_kv, d, BF16)
+    for n in (3, 100, 250):
+        q, st = _randn(g, n, H, d), torch.tensor([250 - n], dtype=torch.int32, device="cuda:0")
+        call = (lambda: plan.attend_packed(q, K.to(BF16), V.to(BF16), _cu([n]))) if n == 250 else \
+               (lambda: plan.attend_paged(q, cache, pt, _cu([n]), st, max_new=n))
+        O, R = call()
+        q[1, 2, 5] = bad
+        O2, R2 = call()
+        plan.check()
+        keep = torch.ones((n, H), dtype=torch.bool, device="cuda:0")
+        keep[1, 2] = False
+        assert torch.equal(O[keep], O2[keep]) and torch.equal(R[keep], R2[keep]), n
+        assert not torch.isfinite(O2[1, 2]).all()
+
+
+def test_near_counts_against_the_bins():
+    H, n = 3, 200
+    for s in (1, 20, 64):
+        plan = _plan(H, 1, n, 64, s, BF16, sigma=[1.0, 9.0, 200.0])
+        ids = oracle.bin_ids(plan.table_host, n)
+        near = plan.near.cpu().numpy()
+        for h in range(H):
+            c = (ids[h][:, :, None] == ids[h][:, None, :]).sum(0)  # [n][n], over the hashes
+            for p in range(n):
+                row = np.zeros(64, dtype=np.int64)
+                j = np.arange(p // 64 * 64, p + 1)
+                row[j % 64] = c[p, j]
+                assert (near[h, p] == row).all(), (s, h, p)
+
+
+def test_the_plain_entry_points_give_the_same_bits():
+    import alibi_positional_lsh_b200 as m
+    H, H_kv, d, s, page, lens = 4, 2, 128, 20, 64, [40, 1, 30]
+    plan, g, T = _plan(H, H_kv, 100, d, s, BF16), _gen(65), 71
+    q, k, v = _randn(g, T, H, d), *_randn(g, 2, T, H_kv, d)
+    cu, zero = _cu(lens), torch.zeros(3, dtype=torch.int32, device="cuda:0")
+    err = torch.zeros(4, dtype=torch.int32, device="cuda:0")
+    near = torch.empty_like(plan.near)
+    m.plsh_near_counts(plan.bmask, H, s, 100, near)
+    assert torch.equal(near, plan.near)
+    O, R = torch.empty_like(q), torch.empty((T, H), device="cuda:0")
+    m.plsh_packed_fwd(q, k, v, m.PLSH_BF16, cu, H, H_kv, d, s, 100, plan.spans, plan.bmask, near, O, R, err)
+    assert all(torch.equal(a, b) for a, b in zip((O, R), plan.attend_packed(q, k, v, cu)))
+    pt, num = _table_of(lens, page)
+    a, b = _cache(num, H_kv, page, d, E4M3), _cache(num, H_kv, page, d, E4M3)
+    a.append(k, v, pt, cu, zero)
+    m.plsh_cache_append(k, v, m.PLSH_BF16, cu, zero, H_kv, d, b.k_pages, b.v_pages, b.k_exp, b.v_exp, pt, err)
+    for x, y in zip((a.k_pages, a.v_pages, a.k_exp, a.v_exp), (b.k_pages, b.v_pages, b.k_exp, b.v_exp)):
+        assert torch.equal(x.view(torch.uint8), y.view(torch.uint8))
+    K, V = torch.empty_like(k), torch.empty_like(v)
+    m.plsh_cache_read(b.k_pages, b.v_pages, b.k_exp, b.v_exp, pt, cu, zero, H_kv, d, m.PLSH_BF16, K, V, err)
+    assert all(torch.equal(x, y) for x, y in zip((K, V), a.read(pt, cu, zero, T)))
+    scratch = torch.empty(m.plsh_paged_scratch_bytes(T, 3, T, H_kv, d, plan.max_window), dtype=torch.uint8, device="cuda:0")
+    m.plsh_paged_fwd(q, m.PLSH_BF16, cu, zero, T, H, H_kv, d, b.k_pages, b.v_pages, b.k_exp, b.v_exp, pt, s, 100, plan.table_dev,
+                     plan.spans, plan.bmask, near, plan.windows_host, scratch, O, R, err)
+    assert all(torch.equal(x, y) for x, y in zip((O, R), plan.attend_paged(q, a, pt, cu, zero)))
+    assert int(err.abs().max()) == 0
+
+
+@pytest.mark.parametrize("paged", [False, True])
+def test_a_bounded_wait_runs_out_and_the_next_call_is_correct(paged):
+    """The tile kernel's issuer of tensor-core products told to issue none: every wait for scores runs out after the limit, the
+    launch reports it and returns, and the next call on the same context is right."""
+    from alibi_positional_lsh_b200 import plsh_set_wait_limit_ns, plsh_test_withhold_mma
+    H, H_kv, d, page, lens = 2, 1, 128, 64, [300, 90]
+    plan, g = _plan(H, H_kv, 300, d, 12, BF16), _gen(66)
+    q, k, v = _randn(g, 390, H, d), *_randn(g, 2, 390, H_kv, d)
+    cu, zero = _cu(lens), torch.zeros(2, dtype=torch.int32, device="cuda:0")
+    pt, num = _table_of(lens, page)
+    cache = _cache(num, H_kv, page, d, BF16)
+    cache.append(k, v, pt, cu, zero)
+    call = (lambda: plan.attend_paged(q, cache, pt, cu, zero)) if paged else (lambda: plan.attend_packed(q, k, v, cu))
+    call()
+    plan.check()
+    plsh_set_wait_limit_ns(1_000_000)
+    plsh_test_withhold_mma(True)
+    try:
+        call()
+        torch.cuda.synchronize()
+    finally:
+        plsh_test_withhold_mma(False)
+        plsh_set_wait_limit_ns(0)
+    assert "TIMEOUT" in plan.device_errors()
+    plan.reset_errors()
+    O, R = call()
+    plan.check()
+    _check_packed(plan, O, R, q, k, v, lens)
