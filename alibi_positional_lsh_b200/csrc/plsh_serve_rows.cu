@@ -110,6 +110,17 @@ __device__ __forceinline__ void mma_bf16(float (&c)[4], uint32_t a0, uint32_t a1
   asm volatile("mma.sync.aligned.m16n8k16.row.col.f32.bf16.bf16.f32 {%0, %1, %2, %3}, {%4, %5, %6, %7}, {%8, %9}, {%0, %1, %2, %3};"
                : "+f"(c[0]), "+f"(c[1]), "+f"(c[2]), "+f"(c[3]) : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1));
 }
+// A 32 x 32 matrix of bits, lane i holding row i, transposed: blocks of 16, 8, .. change places across the diagonal.
+__device__ __forceinline__ uint32_t transpose_bits(uint32_t x, int lane) {
+  uint32_t m = 0x0000FFFFu;
+#pragma unroll
+  for (int j = 16; j >= 1; j >>= 1) {
+    const uint32_t y = __shfl_xor_sync(0xffffffffu, x, j);
+    x = lane & j ? (x & ~m) | ((y >> j) & m) : (x & m) | ((y & m) << j);
+    m ^= m << (j >> 1);
+  }
+  return x;
+}
 // An 8 x 8 matrix of 16-bit values, lane (g, t) holding row g's columns 2 t, 2 t + 1, transposed.
 __device__ __forceinline__ uint32_t transpose8(uint32_t x) {
   uint32_t y;
@@ -463,15 +474,20 @@ serve_rows_kernel(ServeArgs a, Split sp) {
         ek = a.pg.k_exp[row];
         ev = a.pg.v_exp[row];
       }
+      // A lane takes one hash (or two) and finds which of the step's keys its block reaches: all, none, or those from its
+      // beginning on; where some block begins within the step, these words of keys are turned round into the keys' words of hashes.
+      // (Every hash compared with every key: 108 sequences of one to four tokens, 40/8 heads, 64 hashes, 346 us.)
+      const int top = p0 - kStep * (b + i), bottom = top - (kStep - 1);
+      auto reached = [&](int first) -> uint32_t {
+        const uint32_t whole = __ballot_sync(0xffffffffu, first <= bottom);
+        if (!(__ballot_sync(0xffffffffu, first <= top) & ~whole)) return whole;
+        return transpose_bits(first <= bottom ? 0xffffffffu : first > top ? 0u : (2u << (top - first)) - 1u, lane);
+      };
       MaskT all = 0;
       for (int h = 0; h < nh; ++h) {
-        const int4* begin = reinterpret_cast<const int4*>(s_begin + h * PLSH_MAX_S);
-        MaskT v = 0;
-        for (int k = 0; k < (a.s + 3) / 4; ++k) {  // places past the last hash hold the largest position
-          const int4 b4 = begin[k];
-          const uint32_t n4 = (b4.x <= j ? 1u : 0u) | (b4.y <= j ? 2u : 0u) | (b4.z <= j ? 4u : 0u) | (b4.w <= j ? 8u : 0u);
-          v |= static_cast<MaskT>(n4) << (4 * k);
-        }
+        const int* const begin = s_begin + h * PLSH_MAX_S;  // places past the last hash hold the largest position
+        MaskT v = reached(begin[lane]);
+        if constexpr (sizeof(MaskT) == 8) v |= static_cast<MaskT>(reached(begin[32 + lane])) << 32;
         keep[h * kStep + lane] = v;
         all |= v;
       }
