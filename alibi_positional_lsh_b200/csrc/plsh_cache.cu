@@ -8,6 +8,7 @@
 // heads: it finds their sequences and pages once, then moves rows 16 bytes a lane on the packed side (16 lanes
 // a row of 128 bf16), K and V of two rows in flight per lane; a row's largest magnitude is a butterfly over its lanes.
 #include "plsh_serve.cuh"
+#include "plsh_tile_common.cuh"
 
 namespace plsh {
 namespace {
@@ -15,7 +16,7 @@ namespace {
 using namespace serve;
 
 constexpr int kThreads = 256;
-constexpr int kTokens = 16;  // most tokens of a block
+constexpr int kTokens = 8;  // most tokens of a block
 
 // The rows of head 0 of a block's tokens, -1 where there is none.
 __device__ __forceinline__ void find_rows(const SeqArgs& sq, const PageArgs& pg, int t0, int n, long long* base, uint32_t* err) {
@@ -144,10 +145,12 @@ read_kernel(SeqArgs sq, PageArgs pg, int tokens, T* __restrict__ K, T* __restric
   }
 }
 
-// Tokens of a block: enough blocks to fill the machine twice, then up to 16, so that the rows' addresses are found once for many.
+// Tokens of a block: four blocks for every SM first, then up to 8 tokens, so that the rows' addresses are found once for many. With 1, 2, 4, 8
+// and 16 tokens (bf16 into e4m3 and back, 8 heads, d 128): 10.6, 10.5, 14.3, 16.4 and 22.6 us for 100 tokens, 26.6, 22.5, 21.2, 22.5
+// and 26.7 us for 4,000, 71.7, 51.2, 47.1, 45.1 and 48.3 us for 16,000.
 int tokens_per_block(int T) {
   int n = 1;
-  while (n < kTokens && T / (2 * n) >= 2 * 148) n *= 2;
+  while (n < kTokens && T / (2 * n) >= 4 * tiles::sm_count()) n *= 2;
   return n;
 }
 

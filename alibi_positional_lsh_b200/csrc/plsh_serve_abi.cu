@@ -51,6 +51,12 @@ int check_pages(const char* fn, const void* k, const void* v, const int8_t* ke, 
   return PLSH_OK;
 }
 
+// Whether the longer sequences of a paged bf16 call are the tile kernel's, or all the rows kernel's, which is quicker for few tokens
+// and rereads a window for every few of them. Rows and tiles, us, 16/8 heads, d 128, 4,000 tokens before the new ones, e4m3 (bf16)
+// pages: 64 sequences of 8 tokens 72 and 138 (92 and 97), of 16 tokens 111 and 109 (156 and 71), of 24 tokens 181 and 117 (153
+// and 78); 8 sequences of 16 tokens 40 and 47 (42 and 40); one of 16 tokens 23 and 42 (18 and 37).
+bool tiles_wanted(int T, int max_new) { return max_new > kFewTokens || (max_new > 8 && T > 128); }
+
 int lg2(int x) {
   int l = 0;
   while ((1 << l) < x) ++l;
@@ -145,7 +151,7 @@ extern "C" int plsh_cache_read(const void* k_pages, const void* v_pages, const i
 }
 
 extern "C" size_t plsh_paged_scratch_bytes(int T, int S, int max_new, int H_kv, int d, int max_window) {
-  if (T < 1 || S < 1 || H_kv < 1 || d < 1 || max_window < 1 || max_new <= plsh::kFewTokens) return 0;
+  if (T < 1 || S < 1 || H_kv < 1 || d < 1 || max_window < 1 || !plsh::tiles_wanted(T, max_new)) return 0;
   return plsh::serve_scratch_bytes(T, S, H_kv, d, max_window);
 }
 
@@ -171,7 +177,7 @@ extern "C" int plsh_paged_fwd(const void* Q, int64_t q_token, int64_t q_head, in
       return fail(PLSH_ERR_INVALID_ARG, "%s: need 1 <= windows_host[h] <= max_len (%d for head %d)", fn, windows_host[h], h);
     if (windows_host[h] > max_window) max_window = windows_host[h];
   }
-  const bool tiles = dtype == PLSH_BF16 && max_new > plsh::kFewTokens;
+  const bool tiles = dtype == PLSH_BF16 && plsh::tiles_wanted(T, max_new);
   if (!near_dev || !plsh::aligned16(near_dev)) return fail(PLSH_ERR_INVALID_ARG, "%s: near_dev must be given, 16-byte aligned", fn);
   if (tiles && k_exp) {
     const size_t need = plsh_paged_scratch_bytes(T, S, max_new, H_kv, d, max_window);

@@ -12,7 +12,8 @@
 // The partial rows (m, the sums, O) meet at the end, the warps' in shared memory and the blocks' across it (distributed shared
 // memory): one launch, no scratch, and always joined in the same order, so results do not depend on timing. Teams are
 // sized so that the launch fits the machine at once: narrow windows with a block each left a second wave of blocks whose
-// time is all trips to memory (64 sequences, 16/8 heads, d 128, e4m3: 39 us).
+// time is all trips to memory. 64 sequences of 600 to 16,000 tokens, 16/8 heads, d 128, e4m3: 36.9 us; one of 4,096 tokens, 32/8
+// heads: 20 us (16 us with a warm L2).
 //
 // The rows are the products' narrow side: with them on the wide one (16), half of the products, of O's registers and of
 // the exponentials were padding. K and V go from the pages to registers, 16 bytes at a time, and are not staged: a dot product may
@@ -30,7 +31,8 @@
 // counted from the masks.
 //
 // What bounds it: a few tokens read so little that the time is the chain of trips to memory (lengths and table; pages;
-// exponents, K and V; the cluster's exchange); a batch reads each window once, 16 keys a step with the next step's rows on their way.
+// exponents, K and V; the cluster's exchange); a batch reads each window once, 16 keys a step with the next step's rows on their way
+// (32 MB in 32 us, a quarter of the issue slots: what the warps wait for is the first keys and each other).
 #include <cooperative_groups.h>
 
 #include "plsh_binid.cuh"
@@ -476,7 +478,7 @@ serve_rows_kernel(ServeArgs a, Split sp) {
       }
       // A lane takes one hash (or two) and finds which of the step's keys its block reaches: all, none, or those from its
       // beginning on; where some block begins within the step, these words of keys are turned round into the keys' words of hashes.
-      // (Every hash compared with every key: 108 sequences of one to four tokens, 40/8 heads, 64 hashes, 346 us.)
+      // (Every hash compared with every key: 108 sequences of one to four tokens, 40/8 heads, 64 hashes, 346 us; so 238 us.)
       const int top = p0 - kStep * (b + i), bottom = top - (kStep - 1);
       auto reached = [&](int first) -> uint32_t {
         const uint32_t whole = __ballot_sync(0xffffffffu, first <= bottom);
@@ -680,7 +682,7 @@ int launch_src(const ServeArgs& a, cudaStream_t st) {
 }  // namespace
 
 // Tokens of one block of rows. In a call whose longest sequence is the tile kernel's, this kernel takes the sequences that fit one:
-// room for 16 tokens a sequence would leave most of the launch without rows (chunks of 1 and of more tokens mixed: 98 us, so 84).
+// room for 16 tokens a sequence would leave most of the launch without rows (ten chunks of 1 to 2,048 tokens: 98 us, so 84).
 int rows_block_tokens(int group) { return group < kRowsMax ? kRowsMax / group : 1; }
 
 int launch_serve_rows(const ServeArgs& a, cudaStream_t st) {

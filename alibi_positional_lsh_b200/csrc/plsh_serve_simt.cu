@@ -4,16 +4,16 @@
 //   O_i = sum_{j <= i} c_ij e^{S_ij} V_j / sum_{j <= i} c_ij e^{S_ij},  row_sum_i = ln sum_{j <= i} (c_ij / s) e^{S_ij},
 // with c_ij = s - popcount(OR of the boundary masks over (j, i]) (blocks are contiguous).
 //
-// A cluster of one to four blocks takes a tile of 32 positions of one query head, each block a run of the window's 64-key tiles,
-// from the diagonal down, with a running maximum and sum; the blocks' rows then meet across their shared memory, each
-// block joining a share of the elements, always in the same order. Tiles lie on the grid of absolute positions, so that the counts need
-// one word per row (the OR from the key tile's end to the row) and one suffix OR per key; those of the row's own key
-// tile are the plan's near counts (scanned here, they were a chain of up to 64 dependent steps a block). A thread holds 2 rows x 4 keys of S and 2 rows x d/16 columns of O (4 rows and half
-// as many warps: a key tile took twice as long, for want of warps to hide its trips to shared memory).
+// A cluster of one to four blocks takes a tile of 32 positions of one query head, each block a run of the window's
+// 64-key tiles, from the diagonal down, with a running maximum and sum; the blocks' rows then meet across their shared
+// memory, each block joining a share of the elements, always in the same order. Tiles lie on the grid of absolute
+// positions, so that the counts need one word per row (the OR from the key tile's end to the row) and one suffix OR per
+// key; those of the row's own key tile are the plan's near counts (scanned here, they were a chain of up to 64 dependent
+// steps a block). A thread holds 2 rows x 4 keys of S and 2 rows x d/16 columns of O.
 //
-// What bounds it: 4 d multiply-adds a weighted pair at 128 a clock and SM, and for short prompts the length of the longest
-// window, which is why blocks share one (one block a tile of 64 rows: 110 us for three prompts of 1,024, 301 and 699 tokens, 4/2
-// heads, d 64).
+// What bounds it: operands come from shared memory 16 bytes a lane, 6 loads for 32 multiply-adds, and key tiles follow one
+// another in a block, with the loads of one exposed. Three prompts of 1,024, 301 and 699 tokens, 4/2 heads, d 64: 51 us
+// (one block a tile of 64 rows 110 us; 64 rows, 4 x 4 a thread: 55 us in clusters of four, 100 us in clusters of eight).
 #include <cooperative_groups.h>
 
 #include "plsh_serve.cuh"
@@ -296,7 +296,9 @@ int launch(const ServeArgs& a, cudaStream_t st) {
   cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
   if (e != cudaSuccess) return cuda_fail(e, "cudaFuncSetAttribute(serve_simt_kernel)");
   const long long slots = a.sq.T / kRows + static_cast<long long>(a.sq.start ? 2 : 1) * a.sq.S;
-  // blocks of a row tile: up to four while the launch has fewer than four an SM, and no more than the longest window has key tiles
+  // Blocks of a row tile: up to four while the launch has fewer than four an SM, and no more than the longest window can have key
+  // tiles. With one, two and four: 84, 59 and 53 us in the case above, 100, 77 and 88 us for two prompts of 1,000 tokens with 8/8
+  // heads, 371, 441 and 589 us for four of 2,000 with 16/8.
   int C = 1;
   while (C < kCluster && slots * a.H * C < 4 * tiles::sm_count() && C * kKeys < a.sq.max_len) C *= 2;
   if (slots * C > 0x7fffffffLL) return fail(PLSH_ERR_RANGE, "too many row tiles");

@@ -35,6 +35,11 @@
 // Rows past a sequence's end hold another sequence's data: their K and V rows are cleared in shared memory before the
 // products, so that nothing there, not even a NaN, meets a zero weight: a sequence's result has the same bits whatever it is packed with.
 //
+// What bounds it: the chain of one tile (S read, exponentials, P written, P V) with two blocks an SM to overlap it, and the size
+// of its code; 24 prompts of 1 to 3,001 tokens, 32/8 heads, d 128: 158 us, the tensor pipe busy 26%, issue slots 32%, the special
+// function unit 16%. Every fourth pair's exponentials as a polynomial on the FMA pipe: 184 us. Items fetched by cancelling
+// unstarted blocks instead of the list dealt out in a snake: 170 us (every block reserves the widest items ahead of their use).
+//
 // Every barrier wait is bounded in time (PLSH_DEVERR_TIMEOUT), as in the fused kernel.
 #include <cmath>
 

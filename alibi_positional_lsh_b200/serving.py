@@ -25,7 +25,7 @@ _CODES = {torch.bfloat16: PLSH_BF16, torch.float32: PLSH_F32}
 
 
 _EMPTY = (0, 0, 0)
-_FEW = 16  # plsh_paged_fwd needs scratch for more new tokens than this
+_FEW = 8  # plsh_paged_fwd may need scratch for more new tokens than this
 
 
 def _stream(stream: Optional[torch.cuda.Stream], device: torch.device) -> int:

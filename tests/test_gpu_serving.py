@@ -690,6 +690,29 @@ def test_sequences_on_either_side_of_the_kernels_limits(lens):
             t, at = t + L, at + ends[n]
 
 
+@pytest.mark.parametrize("most", [8, 9, 16])
+@pytest.mark.parametrize("S", [8, 20])
+@pytest.mark.parametrize("kind", [E4M3, BF16])
+def test_chunks_of_several_tokens_in_large_and_small_calls(kind, S, most):
+    H, H_kv, d, page = 2, 1, 64, 32
+    g, rng = _gen(67), np.random.default_rng(most)
+    lens = [most] + [int(x) for x in rng.integers(1, most + 1, S - 1)]
+    starts = [int(x) for x in rng.integers(0, 150, S)]
+    ends = [a + b for a, b in zip(lens, starts)]
+    plan = _plan(H, H_kv, max(ends), d, 20, BF16)
+    pt, num = _table_of(ends, page)
+    cache = _cache(num, H_kv, page, d, kind)
+    K, V = _fill(cache, ends, pt, g, H_kv, d, BF16)
+    q, st = _randn(g, sum(lens), H, d), torch.tensor(starts, dtype=torch.int32, device="cuda:0")
+    O, R = plan.attend_paged(q, cache, pt, _cu(lens), st, max_new=most)
+    plan.check()
+    t = at = 0
+    for n, (L, a) in enumerate(zip(lens, starts)):
+        want = plain.sequence(q[t:t + L].double(), K[at:at + a + L], V[at:at + a + L], plan.table_host, a)
+        plain.check(O[t:t + L], R[t:t + L], want, BF16, f"sequence {n}")
+        t, at = t + L, at + ends[n]
+
+
 @pytest.mark.parametrize("kind", [E4M3, BF16])
 def test_a_pool_past_32_bit_offsets(kind):
     """Pages whose first element lies past 2^32 elements of the pool."""

@@ -66,6 +66,8 @@ def test_bad_arguments_are_refused_before_any_launch(plsh, name, args, bad):
 
 def test_scratch_is_needed_by_tiles_of_e4m3_only(plsh):
     assert plsh.plsh_paged_scratch_bytes(100, 2, 16, 2, 128, 50) == 0
+    assert plsh.plsh_paged_scratch_bytes(128, 8, 16, 2, 128, 50) == 0 and plsh.plsh_paged_scratch_bytes(4000, 500, 8, 2, 128, 50) == 0
+    assert plsh.plsh_paged_scratch_bytes(129, 9, 16, 2, 128, 50) == 2 * (129 + 9 * 320) * 2 * 128 * 2
     assert plsh.plsh_paged_scratch_bytes(100, 2, 17, 2, 128, 50) == 2 * (100 + 2 * 320) * 2 * 128 * 2
     assert plsh.plsh_paged_scratch_bytes(0, 2, 17, 2, 128, 50) == 0
 
