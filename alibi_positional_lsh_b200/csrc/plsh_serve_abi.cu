@@ -2,6 +2,7 @@
 #include <cstring>
 
 #include "plsh_internal.h"
+#include "plsh_tile_common.cuh"
 
 namespace plsh {
 namespace {
@@ -56,6 +57,14 @@ int check_pages(const char* fn, const void* k, const void* v, const int8_t* ke, 
 // pages: 64 sequences of 8 tokens 72 and 138 (92 and 97), of 16 tokens 111 and 109 (156 and 71), of 24 tokens 181 and 117 (153
 // and 78); 8 sequences of 16 tokens 40 and 47 (42 and 40); one of 16 tokens 23 and 42 (18 and 37).
 bool tiles_wanted(int T, int max_new) { return max_new > kFewTokens || (max_new > 8 && T > 128); }
+
+// Where the longer sequences are the tile kernel's, whether the others are worth a launch of the rows kernel, or a tile a head each. Rows and
+// tiles, us, a chunk of 600 tokens and single ones, 4,000 tokens before each, d 128, e4m3 (bf16) pages: 12 of them, 16/8 heads, 64
+// and 55 (57 and 43); 48, 16/8 heads, 91 and 101 (73 and 68); 24, 32/8 heads, 85 and 84 (79 and 69); 48, 32/8 heads, 81 and 121
+// (72 and 101). The lengths are on the device: few tokens besides the longest sequence's stand for short sequences.
+bool rows_wanted(int T, int S, int max_new, int H) {
+  return static_cast<long long>(S) * H > 5LL * tiles::sm_count() && T - max_new <= 8LL * S;
+}
 
 int lg2(int x) {
   int l = 0;
@@ -200,8 +209,9 @@ extern "C" int plsh_paged_fwd(const void* Q, int64_t q_token, int64_t q_head, in
   a.O = O; a.row_sum = row_sum; a.err = err_dev;
   const cudaStream_t st = static_cast<cudaStream_t>(stream);
   if (dtype == PLSH_BF16) {
-    a.few = tiles ? plsh::rows_block_tokens(H / H_kv) : plsh::kFewTokens;
-    if (int rc = plsh::launch_serve_rows(a, st)) return rc;
+    a.few = !tiles ? plsh::kFewTokens : plsh::rows_wanted(T, S, max_new, H) ? plsh::rows_block_tokens(H / H_kv) : 0;
+    if (a.few > 0)
+      if (int rc = plsh::launch_serve_rows(a, st)) return rc;
     return tiles ? plsh::launch_serve_tc(a, st) : PLSH_OK;
   }
   return plsh::launch_serve_simt(a, st);

@@ -681,8 +681,8 @@ int launch_src(const ServeArgs& a, cudaStream_t st) {
 
 }  // namespace
 
-// Tokens of one block of rows. In a call whose longest sequence is the tile kernel's, this kernel takes the sequences that fit one:
-// room for 16 tokens a sequence would leave most of the launch without rows (ten chunks of 1 to 2,048 tokens: 98 us, so 84).
+// Tokens of one block of rows. Where this kernel shares a call with the tile kernel, it takes the sequences that fit one: room
+// for 16 tokens a sequence would leave most of the launch without rows (ten chunks of 1 to 2,048 tokens: 98 us, so 84).
 int rows_block_tokens(int group) { return group < kRowsMax ? kRowsMax / group : 1; }
 
 int launch_serve_rows(const ServeArgs& a, cudaStream_t st) {

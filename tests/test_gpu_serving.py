@@ -670,6 +670,29 @@ def test_paged_many_heads(H, H_kv, lens, starts):
     _check_packed(plan, O, R, q, K.to(BF16), V.to(BF16), ends)
 
 
+@pytest.mark.parametrize("kind", [E4M3, BF16])
+def test_a_chunk_among_many_single_tokens(kind):
+    # many short sequences beside the tile kernel's: the rows kernel's, of up to 8 rows each
+    H, H_kv, d, page, lens = 16, 8, 64, 32, [1] * 24 + [70, 0, 4, 5] + [2] * 22
+    g, rng = _gen(68), np.random.default_rng(1)
+    starts = [int(x) for x in rng.integers(0, 150, len(lens))]
+    ends = [a + b for a, b in zip(lens, starts)]
+    plan = _plan(H, H_kv, max(ends), d, 20, BF16)
+    pt, num = _table_of(ends, page)
+    cache = _cache(num, H_kv, page, d, kind)
+    K, V = _fill(cache, ends, pt, g, H_kv, d, BF16)
+    q, st = _randn(g, sum(lens), H, d), torch.tensor(starts, dtype=torch.int32, device="cuda:0")
+    for most in (70, None):
+        O, R = plan.attend_paged(q, cache, pt, _cu(lens), st, max_new=most)
+        plan.check()
+        t = at = 0
+        for n, (L, a) in enumerate(zip(lens, starts)):
+            if L:
+                want = plain.sequence(q[t:t + L].double(), K[at:at + a + L], V[at:at + a + L], plan.table_host, a)
+                plain.check(O[t:t + L], R[t:t + L], want, BF16, f"sequence {n}")
+            t, at = t + L, at + ends[n]
+
+
 @pytest.mark.parametrize("lens", [[1, 4, 5, 16, 17], [16, 1, 16], [3, 17, 2, 4]])
 def test_sequences_on_either_side_of_the_kernels_limits(lens):
     # 8 rows, here 4 tokens, of a block; 16 tokens of the rows kernel's longest call
