@@ -120,7 +120,7 @@ struct ServeArgs {
   SeqArgs sq;
   int dtype, H, H_kv, d, s;
   const int32_t* spans; const void* bmask;  // plsh_window's, causal, over max_len positions
-  const uint8_t* near;                      // launch_near's; the bf16 kernel's
+  const uint8_t* near;                      // launch_near's; the tile kernels'
   const double* table;                      // [H][s][2]; the row kernel's
   // paged bf16: sequences with at most this many new tokens are the row kernel's, the others the tile kernel's (0: all theirs)
   int few;

@@ -82,7 +82,7 @@ __device__ __forceinline__ float pow2(int e) { return __int_as_float((e + 127) <
 // The scale of a row with largest finite magnitude m: the least e >= -126 with m <= 448 * 2^e. With
 // m = f * 2^x, 1 <= f < 2, and 448 = 1.75 * 2^8 that is x - 8, and one more where f > 1.75. A power of two costs an
 // e4m3 value no bits (its own exponent absorbs the scale), makes x * 2^-e exact, so the result
-// depends on one rounding only, and makes every dequantised value exact in bf16.
+// depends on one rounding only, and makes every dequantised value exact in bf16 (down to its smallest subnormal).
 __device__ __forceinline__ int e4m3_exponent(float m) {
   const uint32_t b = __float_as_uint(m);
   const int e = static_cast<int>(b >> 23) - 127 - 8 + ((b & 0x7FFFFFu) > 0x600000u ? 1 : 0);

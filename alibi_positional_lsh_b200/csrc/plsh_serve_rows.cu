@@ -12,7 +12,7 @@
 // The partial rows (m, the sums, O) meet at the end, the warps' in shared memory and the blocks' across it (distributed shared
 // memory): one launch, no scratch, and always joined in the same order, so results do not depend on timing. Teams are
 // sized so that the launch fits the machine at once: narrow windows with a block each left a second wave of blocks whose
-// time is all trips to memory. 64 sequences of 600 to 16,000 tokens, 16/8 heads, d 128, e4m3: 36.9 us; one of 4,096 tokens, 32/8
+// time is all trips to memory. 64 sequences of 443 to 15,566 tokens, 16/8 heads, d 128, e4m3: 36.9 us; one of 4,096 tokens, 32/8
 // heads: 20 us (16 us with a warm L2).
 //
 // The rows are the products' narrow side: with them on the wide one (16), half of the products, of O's registers and of

@@ -160,10 +160,16 @@ class PagedCache(_Errors):
                 raise ValueError(f"{nm} must be a contiguous CUDA tensor on {self.device}")
             if nm.endswith("exp") and (t.dtype != torch.int8 or t.shape != k_pages.shape[:3]):
                 raise ValueError(f"{nm} must be int8 [num_pages][H_kv][page_size]")
-        self.k_pages, self.v_pages, self.k_exp, self.v_exp = k_pages, v_pages, k_exp, v_exp
+        self._tensors = k_pages, v_pages, k_exp, v_exp
         self.err = torch.zeros((4,), dtype=torch.int32, device=self.device)
         self._like = {t: torch.empty((0,), dtype=t, device=self.device) for t in _CODES}  # what new tensors are made from
-        self._pages = tuple(0 if x is None else x.data_ptr() for x in (k_pages, v_pages, k_exp, v_exp))
+        self._pages = tuple(0 if x is None else x.data_ptr() for x in self._tensors)
+
+    # the cache's own tensors, which cannot be exchanged: the calls keep their addresses
+    k_pages = property(lambda self: self._tensors[0])
+    v_pages = property(lambda self: self._tensors[1])
+    k_exp = property(lambda self: self._tensors[2])
+    v_exp = property(lambda self: self._tensors[3])
 
     @classmethod
     def empty(cls, num_pages: int, H_kv: int, page_size: int, d: int, dtype: torch.dtype = torch.float8_e4m3fn,

@@ -1,3 +1,4 @@
+import gc
 import os
 import sys
 
@@ -27,3 +28,10 @@ def pytest_collection_modifyitems(config, items):
     for it in items:
         if "gpu" in it.keywords:
             it.add_marker(skip)
+
+
+def pytest_runtest_setup(item):
+    # test_zz_no_alloc compares allocated bytes before and after calls: tensors that earlier tests left in reference cycles (a caught
+    # exception's frames) go first, or a garbage collection between the two counts frees them
+    if item.path.name == "test_zz_no_alloc.py":
+        gc.collect()

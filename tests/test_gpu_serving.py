@@ -670,6 +670,34 @@ def test_paged_many_heads(H, H_kv, lens, starts):
     _check_packed(plan, O, R, q, K.to(BF16), V.to(BF16), ends)
 
 
+@pytest.mark.parametrize("kind,d,dtype", [(E4M3, 128, BF16), (F32, 64, F32)])
+def test_thousands_of_sequences(kind, d, dtype):
+    # more than 32 x 32: three steps of the search for a tile's sequence; empty ones in between
+    H, H_kv, page, S = 4, 2, 16, 2500
+    g, rng = _gen(69), np.random.default_rng(2)
+    lens = [int(x) for x in rng.choice([0, 1, 1, 2, 5], S)]
+    starts = [int(x) for x in rng.integers(0, 60, S)]
+    ends = [a + b if a else 0 for a, b in zip(lens, starts)]
+    plan = _plan(H, H_kv, 80, d, 20, dtype)
+    pt, num = _table_of(ends, page)
+    cache = _cache(num, H_kv, page, d, kind)
+    K, V = _fill(cache, ends, pt, g, H_kv, d, dtype)
+    q, st = _randn(g, sum(lens), H, d, dtype=dtype), torch.tensor(starts, dtype=torch.int32, device="cuda:0")
+    kp, vp = K.to(dtype), V.to(dtype)
+    qp = _randn(g, sum(ends), H, d, dtype=dtype)
+    OP, RP = plan.attend_packed(qp, kp, vp, _cu(ends))
+    for most in (5, None):
+        O, R = plan.attend_paged(q, cache, pt, _cu(lens), st, max_new=most)
+        plan.check()
+        t, at = np.concatenate([[0], np.cumsum(lens)]), np.concatenate([[0], np.cumsum(ends)])
+        for n in list(range(0, S, 97)) + [S - 2, S - 1]:
+            if not lens[n]:
+                continue
+            a, b = slice(t[n], t[n + 1]), slice(at[n], at[n + 1])
+            plain.check(O[a], R[a], plain.sequence(q[a].double(), K[b], V[b], plan.table_host, starts[n]), dtype, f"sequence {n}")
+            plain.check(OP[b], RP[b], plain.sequence(qp[b].double(), kp[b].double(), vp[b].double(), plan.table_host, 0), dtype, f"prompt {n}")
+
+
 @pytest.mark.parametrize("kind", [E4M3, BF16])
 def test_a_chunk_among_many_single_tokens(kind):
     # many short sequences beside the tile kernel's: the rows kernel's, of up to 8 rows each
