@@ -100,6 +100,8 @@ def _load() -> ctypes.CDLL:
     lib.plsh_paged_fwd.restype = i32
     lib.plsh_paged_fwd.argtypes = [vp, i64, i64, i32, i32, i32, vp, vp, i32, i32, i32, i32, vp, vp, vp, vp, vp, i32, i32,
                                    i32, i32, i32, vp, vp, vp, vp, vp, vp, ctypes.c_size_t, vp, vp, vp, vp]
+    for f in (lib.plsh_packed_fwd_args, lib.plsh_cache_append_args, lib.plsh_cache_read_args, lib.plsh_paged_fwd_args):
+        f.restype, f.argtypes = i32, [ctypes.c_char_p, ctypes.c_size_t]
     lib.plsh_paged_scratch_bytes.restype = ctypes.c_size_t
     lib.plsh_paged_scratch_bytes.argtypes = [i32, i32, i32, i32, i32, i32]
     return lib

@@ -1,5 +1,6 @@
 // Entry points of the serving operators (declared in include/plsh.h): argument checks, then the launch.
-#include <cstring>
+#include <type_traits>
+#include <utility>
 
 #include "plsh_internal.h"
 #include "plsh_tile_common.cuh"
@@ -216,3 +217,33 @@ extern "C" int plsh_paged_fwd(const void* Q, int64_t q_token, int64_t q_head, in
   }
   return plsh::launch_serve_simt(a, st);
 }
+
+// The same calls with their arguments in an array.
+namespace {
+template <typename T>
+T arg(int64_t x) {
+  if constexpr (std::is_pointer_v<T>) return reinterpret_cast<T>(static_cast<uintptr_t>(x));
+  else return static_cast<T>(x);
+}
+template <typename T>
+bool fits(int64_t x) {
+  if constexpr (std::is_same_v<T, int>) return x == static_cast<int>(x);
+  else return true;
+}
+template <typename... P, size_t... I>
+int spread(const char* fn, int (*f)(P...), const int64_t* args, std::index_sequence<I...>) {
+  if (!(fits<P>(args[I]) && ...)) return fail(PLSH_ERR_RANGE, "%s: an argument does not fit its type", fn);
+  return f(arg<P>(args[I])...);
+}
+template <typename... P>
+int spread(const char* fn, int (*f)(P...), const int64_t* args, size_t bytes) {
+  if (!args || bytes != sizeof...(P) * sizeof(int64_t))
+    return fail(PLSH_ERR_INVALID_ARG, "%s: %zu bytes of arguments needed, %zu given", fn, sizeof...(P) * sizeof(int64_t), args ? bytes : 0);
+  return spread(fn, f, args, std::make_index_sequence<sizeof...(P)>());
+}
+}  // namespace
+
+extern "C" int plsh_packed_fwd_args(const int64_t* args, size_t bytes) { return spread("plsh_packed_fwd_args", plsh_packed_fwd, args, bytes); }
+extern "C" int plsh_cache_append_args(const int64_t* args, size_t bytes) { return spread("plsh_cache_append_args", plsh_cache_append, args, bytes); }
+extern "C" int plsh_cache_read_args(const int64_t* args, size_t bytes) { return spread("plsh_cache_read_args", plsh_cache_read, args, bytes); }
+extern "C" int plsh_paged_fwd_args(const int64_t* args, size_t bytes) { return spread("plsh_paged_fwd_args", plsh_paged_fwd, args, bytes); }

@@ -13,6 +13,7 @@ outside the pool) are reported by check().
 """
 from __future__ import annotations
 
+from struct import Struct
 from typing import Optional, Sequence, Tuple
 
 import numpy as np
@@ -24,6 +25,9 @@ from . import (PLSH_BF16, PLSH_F32, PLSH_MAX_S, PLSH_TILE, PlshError, _check, _l
 _CODES = {torch.bfloat16: PLSH_BF16, torch.float32: PLSH_F32}
 
 
+# the calls' arguments as arrays: ctypes takes longer to pass them one by one than the library to check and launch
+_PACKED, _APPEND, _READ, _PAGED = (Struct(f"={len(f.argtypes)}q") for f in (_lib.plsh_packed_fwd, _lib.plsh_cache_append, _lib.plsh_cache_read,
+                                                                          _lib.plsh_paged_fwd))
 _EMPTY = (0, 0, 0)
 _FEW = 8  # plsh_paged_fwd may need scratch for more new tokens than this
 
@@ -193,8 +197,8 @@ class PagedCache(_Errors):
         if S == 0 or T == 0:
             return
         with _On(dev.index):
-            _check(_lib.plsh_cache_append(*kr, *vr, _CODES[dtype], T, S, cu, st, self.H_kv, self.d, *self._pages, pt, width,
-                                          self.num_pages, self.page_size, self.err.data_ptr(), _stream(stream, dev)))
+            _check(_lib.plsh_cache_append_args(_APPEND.pack(*kr, *vr, _CODES[dtype], T, S, cu, st, self.H_kv, self.d, *self._pages, pt, width,
+                                                            self.num_pages, self.page_size, self.err.data_ptr(), _stream(stream, dev)), _APPEND.size))
 
     def read(self, page_table: torch.Tensor, cu_seqlens: torch.Tensor, start: torch.Tensor, total: int,
              dtype: Optional[torch.dtype] = None, out: Optional[Tuple[torch.Tensor, torch.Tensor]] = None,
@@ -222,8 +226,8 @@ class PagedCache(_Errors):
                     if not x.is_contiguous():
                         raise ValueError(f"{nm} must be contiguous")
             if S and total:
-                _check(_lib.plsh_cache_read(*self._pages, pt, width, self.num_pages, self.page_size, total, S, cu, st, self.H_kv,
-                                            self.d, _CODES[dtype], K.data_ptr(), V.data_ptr(), self.err.data_ptr(), _stream(stream, dev)))
+                _check(_lib.plsh_cache_read_args(_READ.pack(*self._pages, pt, width, self.num_pages, self.page_size, total, S, cu, st, self.H_kv,
+                                            self.d, _CODES[dtype], K.data_ptr(), V.data_ptr(), self.err.data_ptr(), _stream(stream, dev)), _READ.size))
         return K, V
 
 
@@ -299,8 +303,8 @@ class PlshServing(_Errors):
         with _On(dev.index):
             O, row_sum = self._outputs(T, out, stream)
             if S and T:
-                _check(_lib.plsh_packed_fwd(*qr, *kr, *vr, self._code, T, S, cu, self.H, self.H_kv, self.d, self.s, self.max_len,
-                                            *self._plan, O.data_ptr(), row_sum.data_ptr(), self._err, _stream(stream, dev)))
+                _check(_lib.plsh_packed_fwd_args(_PACKED.pack(*qr, *kr, *vr, self._code, T, S, cu, self.H, self.H_kv, self.d, self.s, self.max_len,
+                                            *self._plan, O.data_ptr(), row_sum.data_ptr(), self._err, _stream(stream, dev)), _PACKED.size))
         return O, row_sum
 
     def attend_paged(self, q: torch.Tensor, cache: PagedCache, page_table: torch.Tensor, cu_seqlens: torch.Tensor,
@@ -329,8 +333,8 @@ class PlshServing(_Errors):
                     need = _lib.plsh_paged_scratch_bytes(T, S, most, self.H_kv, self.d, self.max_window)
                     if need:
                         scratch = _empty(self._like[2], stream, need)
-                _check(_lib.plsh_paged_fwd(*qr, self._code, T, S, cu, st, most, self.H, self.H_kv, self.d, *cache._pages, pt, width,
+                _check(_lib.plsh_paged_fwd_args(_PAGED.pack(*qr, self._code, T, S, cu, st, most, self.H, self.H_kv, self.d, *cache._pages, pt, width,
                                            cache.num_pages, cache.page_size, self.s, self.max_len, self._table, *self._plan, self._windows,
                                            scratch.data_ptr() if need else 0, need, O.data_ptr(), row_sum.data_ptr(), self._err,
-                                           _stream(stream, dev)))
+                                           _stream(stream, dev)), _PAGED.size))
         return O, row_sum

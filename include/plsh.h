@@ -587,6 +587,18 @@ PLSH_API int plsh_paged_fwd(const void* Q, int64_t q_token, int64_t q_head, int 
                             const uint8_t* near_dev, const int32_t* windows_host, void* scratch_dev,
                             size_t scratch_bytes, void* O, float* row_sum, uint32_t* err_dev, void* stream);
 
+/*
+ * plsh_*_args -- the serving calls with their arguments, in the order above,
+ * as an array of 64-bit integers (pointers as addresses) of `bytes` bytes:
+ * for bindings in which every argument of a call costs time. A size that is
+ * not the call's returns PLSH_ERR_INVALID_ARG, a number that does not fit its
+ * argument's type PLSH_ERR_RANGE.
+ */
+PLSH_API int plsh_packed_fwd_args(const int64_t* args, size_t bytes);
+PLSH_API int plsh_cache_append_args(const int64_t* args, size_t bytes);
+PLSH_API int plsh_cache_read_args(const int64_t* args, size_t bytes);
+PLSH_API int plsh_paged_fwd_args(const int64_t* args, size_t bytes);
+
 #ifdef __cplusplus
 }
 #endif

@@ -1,6 +1,7 @@
 """The serving entry points without a GPU: the host-side checks refuse bad arguments before any device work, and the
 plain implementation that the GPU tests compare with agrees with the oracle."""
 import ctypes
+import struct
 
 import numpy as np
 import pytest
@@ -62,6 +63,22 @@ def test_bad_arguments_are_refused_before_any_launch(plsh, name, args, bad):
     for change, code in bad:
         assert getattr(plsh._lib, name)(*args(**change)) == code, change
         assert plsh.plsh_last_error().startswith(name + ":")
+
+
+@pytest.mark.parametrize("name,args,bad", REFUSED[1:], ids=[r[0] for r in REFUSED[1:]])
+def test_the_same_refusals_through_an_array(plsh, name, args, bad):
+    def call(values, cut=0):
+        a = [ctypes.cast(x, ctypes.c_void_p).value if isinstance(x, ctypes.Array) else x.value if hasattr(x, "value") else x for x in values]
+        raw = struct.pack(f"={len(a)}q", *[x or 0 for x in a])
+        return getattr(plsh._lib, name + "_args")(raw, len(raw) - cut)
+    for change, code in bad:
+        values = args(**change)  # kept: the array holds addresses
+        assert call(values) == code, change
+    values = args(**bad[0][0])
+    for cut in (8, -8):
+        assert call(values, cut) == 1 and "bytes of arguments" in plsh.plsh_last_error()
+    assert call(args(T=(1 << 32) + 10)) == 3 and "does not fit" in plsh.plsh_last_error()
+    assert getattr(plsh._lib, name + "_args")(None, 8 * len(values)) == 1
 
 
 def test_scratch_is_needed_by_tiles_of_e4m3_only(plsh):
