@@ -26,7 +26,7 @@ namespace cg = cooperative_groups;
 using namespace serve;
 
 constexpr int kRows = 32, kKeys = 64, kThreads = 256, kCluster = 4;
-constexpr int kR = kRows / (kThreads / 16);  // rows of a thread
+constexpr int kR = kRows / (kThreads / 32);  // rows of a warp
 
 template <int D, typename MaskT>
 struct SimtSmem {
@@ -47,7 +47,7 @@ __global__ void __launch_bounds__(kThreads) serve_simt_kernel(ServeArgs a, int C
   auto& sm = *reinterpret_cast<SimtSmem<D, MaskT>*>(smem_raw);
   cg::cluster_group cluster = cg::this_cluster();  // heads from the last: with the usual slopes, the widest windows first
   if (blockIdx.x == 0 && blockIdx.y == 0) check_seqs(a.sq, a.err);
-  const int tid = threadIdx.x, tx = tid & 15, ty = tid >> 4, warp = tid >> 5, lane = tid & 31;
+  const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
   const int mult = a.sq.start ? 2 : 1, slot = blockIdx.x / C, rank = blockIdx.x % C;
   if (warp == 0) {
     const int s = warp_find(a.sq.cu, a.sq.S, kRows == 64 ? 6 : 5, mult, slot);
@@ -111,13 +111,14 @@ __global__ void __launch_bounds__(kThreads) serve_simt_kernel(ServeArgs a, int C
   gap = 0;
 #pragma unroll
   for (int w = 0; w < kThreads / 32; ++w) gap |= sm.gap[w];
-  float m[kR], l[kR], acc[kR][D / 16];
+  constexpr int kCols = D / 32;  // columns of O of a lane, kCols * lane ..
+  float m[kR], l[kR], acc[kR][kCols];
 #pragma unroll
   for (int r = 0; r < kR; ++r) {
     m[r] = -INFINITY;
     l[r] = 0.0f;
 #pragma unroll
-    for (int e = 0; e < D / 16; ++e) acc[r][e] = 0.0f;
+    for (int e = 0; e < kCols; ++e) acc[r][e] = 0.0f;
   }
 
   for (int t = t0; t < t1; ++t) {
@@ -169,74 +170,70 @@ __global__ void __launch_bounds__(kThreads) serve_simt_kernel(ServeArgs a, int C
     }
     __syncthreads();
 
-    float x[kR][4];
+    float x[kR][2];
 #pragma unroll
-    for (int r = 0; r < kR; ++r)
-#pragma unroll
-      for (int e = 0; e < 4; ++e) x[r][e] = 0.0f;
+    for (int r = 0; r < kR; ++r) x[r][0] = x[r][1] = 0.0f;
 #pragma unroll 4
     for (int c = 0; c < D; c += 4) {
-      float4 qa[kR], ka[4];
+      float4 qa[kR], ka[2];
 #pragma unroll
-      for (int r = 0; r < kR; ++r) qa[r] = *reinterpret_cast<const float4*>(&sm.q[kR * ty + r][c]);
+      for (int r = 0; r < kR; ++r) qa[r] = *reinterpret_cast<const float4*>(&sm.q[kR * warp + r][c]);
 #pragma unroll
-      for (int e = 0; e < 4; ++e) ka[e] = *reinterpret_cast<const float4*>(&sm.k[tx + 16 * e][c]);
+      for (int e = 0; e < 2; ++e) ka[e] = *reinterpret_cast<const float4*>(&sm.k[lane + 32 * e][c]);
 #pragma unroll
       for (int r = 0; r < kR; ++r)
 #pragma unroll
-        for (int e = 0; e < 4; ++e)
+        for (int e = 0; e < 2; ++e)
           x[r][e] = fmaf(qa[r].x, ka[e].x, fmaf(qa[r].y, ka[e].y, fmaf(qa[r].z, ka[e].z, fmaf(qa[r].w, ka[e].w, x[r][e]))));
     }
-    float alpha[kR];
 #pragma unroll
     for (int r = 0; r < kR; ++r) {
-      const int row = kR * ty + r;
-      int cn[4];
+      const int row = kR * warp + r;
+      int cn[2];
       float top = m[r];
 #pragma unroll
-      for (int e = 0; e < 4; ++e) {
-        const int key = tx + 16 * e;
+      for (int e = 0; e < 2; ++e) {
+        const int key = lane + 32 * e;
         cn[e] = t == 0 ? sm.c[row][key] : a.s - popc_mask<MaskT>(static_cast<MaskT>(sm.own[row] | sm.suf[key]));
         x[r][e] *= sc;
         if (cn[e] > 0) top = fmaxf(top, x[r][e]);
       }
 #pragma unroll
-      for (int o = 8; o >= 1; o >>= 1) top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, o));
-      alpha[r] = top == -INFINITY ? 1.0f : exp2f(m[r] - top);
+      for (int o = 16; o >= 1; o >>= 1) top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, o));
+      const float alpha = top == -INFINITY ? 1.0f : exp2f(m[r] - top);
       float sum = 0.0f;
 #pragma unroll
-      for (int e = 0; e < 4; ++e) {
+      for (int e = 0; e < 2; ++e) {
         const float p = cn[e] > 0 ? static_cast<float>(cn[e]) * exp2f(x[r][e] - top) : 0.0f;
         sum += p;
-        sm.p[row][tx + 16 * e] = p;
+        sm.p[row][lane + 32 * e] = p;
       }
-      l[r] = l[r] * alpha[r] + sum;
+      l[r] = l[r] * alpha + sum;
       m[r] = top;
+#pragma unroll
+      for (int e = 0; e < kCols; ++e) acc[r][e] *= alpha;
     }
-#pragma unroll
-    for (int r = 0; r < kR; ++r)
-#pragma unroll
-      for (int e = 0; e < D / 16; ++e) acc[r][e] *= alpha[r];
     __syncwarp();  // a warp's rows of P are its own
     gap = static_cast<MaskT>(gap | all);
 #pragma unroll 4
     for (int k = 0; k < kKeys; k += 4) {
       float4 pr[kR];
 #pragma unroll
-      for (int r = 0; r < kR; ++r) pr[r] = *reinterpret_cast<const float4*>(&sm.p[kR * ty + r][k]);
+      for (int r = 0; r < kR; ++r) pr[r] = *reinterpret_cast<const float4*>(&sm.p[kR * warp + r][k]);
 #pragma unroll
       for (int kk = 0; kk < 4; ++kk) {
+        float vv[kCols];
+        if constexpr (kCols == 4) {
+          load4f(&sm.v[k + kk][4 * lane], vv);
+        } else {
+          const float2 v2 = *reinterpret_cast<const float2*>(&sm.v[k + kk][2 * lane]);
+          vv[0] = v2.x; vv[1] = v2.y;
+        }
 #pragma unroll
-        for (int e = 0; e < D / 64; ++e) {
-          const float4 vv = *reinterpret_cast<const float4*>(&sm.v[k + kk][64 * e + 4 * tx]);
+        for (int r = 0; r < kR; ++r) {
+          const float p = kk == 0 ? pr[r].x : kk == 1 ? pr[r].y : kk == 2 ? pr[r].z : pr[r].w;
 #pragma unroll
-          for (int r = 0; r < kR; ++r) {
-            const float p = kk == 0 ? pr[r].x : kk == 1 ? pr[r].y : kk == 2 ? pr[r].z : pr[r].w;
-            acc[r][4 * e + 0] = fmaf(p, vv.x, acc[r][4 * e + 0]);
-            acc[r][4 * e + 1] = fmaf(p, vv.y, acc[r][4 * e + 1]);
-            acc[r][4 * e + 2] = fmaf(p, vv.z, acc[r][4 * e + 2]);
-            acc[r][4 * e + 3] = fmaf(p, vv.w, acc[r][4 * e + 3]);
-          }
+          for (int e = 0; e < kCols; ++e) acc[r][e] = fmaf(p, vv[e], acc[r][e]);
         }
       }
     }
@@ -249,25 +246,20 @@ __global__ void __launch_bounds__(kThreads) serve_simt_kernel(ServeArgs a, int C
     if (col == 0)
       a.row_sum[static_cast<size_t>(t) * a.H + h] = (log2f(total) + top) * 0.6931471805599453f - logf(static_cast<float>(a.s));
   };
-  if (C > 1) __syncthreads();  // K has been read
+  __syncthreads();  // K has been read
 #pragma unroll
   for (int r = 0; r < kR; ++r) {
     float total = l[r];
 #pragma unroll
-    for (int o = 8; o >= 1; o >>= 1) total += __shfl_xor_sync(0xffffffffu, total, o);
-    const int row = kR * ty + r, t = token(i0 + row);
-#pragma unroll
-    for (int e = 0; e < D / 64; ++e) {
-      const float o[4] = {acc[r][4 * e], acc[r][4 * e + 1], acc[r][4 * e + 2], acc[r][4 * e + 3]};
-      if (C > 1) store4f(&sm.k[row][64 * e + 4 * tx], o);
-      else if (t >= 0) finish(t, 64 * e + 4 * tx, m[r], total, o);
-    }
-    if (C > 1 && tx == 0) {
+    for (int o = 16; o >= 1; o >>= 1) total += __shfl_xor_sync(0xffffffffu, total, o);
+    const int row = kR * warp + r;
+    if constexpr (kCols == 4) store4f(&sm.k[row][4 * lane], acc[r]);
+    else *reinterpret_cast<float2*>(&sm.k[row][2 * lane]) = make_float2(acc[r][0], acc[r][1]);
+    if (lane == 0) {
       sm.k[row][D] = m[r];
       sm.k[row][D + 1] = total;
     }
   }
-  if (C == 1) return;
   cluster.sync();
   for (int e = rank + C * tid; e < kRows * (D / 4); e += C * kThreads) {
     const int row = e / (D / 4), col = e % (D / 4) * 4, t = token(i0 + row);
