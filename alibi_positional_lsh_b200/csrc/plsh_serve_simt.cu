@@ -9,11 +9,13 @@
 // memory, each block joining a share of the elements, always in the same order. Tiles lie on the grid of absolute
 // positions, so that the counts need one word per row (the OR from the key tile's end to the row) and one suffix OR per
 // key; those of the row's own key tile are the plan's near counts (scanned here, they were a chain of up to 64 dependent
-// steps a block). A thread holds 2 rows x 4 keys of S and 2 rows x d/16 columns of O.
+// steps a block). A warp has 4 rows, each lane 2 keys of S and d/32 columns of O: rows are then
+// broadcast, and the lanes' own loads all differ (2 rows x 4 keys a lane, two lanes sharing each key: 51 us in the case below).
 //
-// What bounds it: operands come from shared memory 16 bytes a lane, 6 loads for 32 multiply-adds, and key tiles follow one
-// another in a block, with the loads of one exposed. Three prompts of 1,024, 301 and 699 tokens, 4/2 heads, d 64: 51 us
-// (one block a tile of 64 rows 110 us; 64 rows, 4 x 4 a thread: 55 us in clusters of four, 100 us in clusters of eight).
+// What bounds it: operands come from shared memory, 12 passes of it for 32 multiply-adds of a warp, key tiles follow one
+// another in a block (four for the widest windows), and some 5 us go before the first and after the last. Three prompts of
+// 1,024, 301 and 699 tokens, 4/2 heads, d 64: 48 us (one block a tile of 64 rows 110 us; 64 rows, 4 x 4 a thread: 55 us in
+// clusters of four, 100 us in clusters of eight; K and V loaded before their tile's arithmetic: 49 us).
 #include <cooperative_groups.h>
 
 #include "plsh_serve.cuh"
@@ -121,41 +123,41 @@ __global__ void __launch_bounds__(kThreads) serve_simt_kernel(ServeArgs a, int C
     for (int e = 0; e < kCols; ++e) acc[r][e] = 0.0f;
   }
 
+  // K or V of a key tile into shared memory, rows past the end as zeros. fp32 rows are copied behind the arithmetic: V under S, the
+  // next tile's K under P V; e4m3 rows go through registers.
+  auto load_tile = [&](bool value, int j0) {
+#pragma unroll (D == 64 ? 4 : 2)
+    for (int e = tid; e < kKeys * (D / 4); e += kThreads) {
+      const int r = e / (D / 4), c = e % (D / 4) * 4, p = j0 + r;
+      float* const dst = value ? &sm.v[r][c] : &sm.k[r][c];
+      long long row = -1;
+      if (p < end) row = kPaged ? page_row(a.pg, sq.s, p, kvh, a.err) : sq.c0 + p;
+      if constexpr (kQuant) {
+        float x[4] = {0.0f, 0.0f, 0.0f, 0.0f};
+        if (row >= 0) {
+          e4m3_to_float4(*reinterpret_cast<const uint32_t*>(static_cast<const uint8_t*>(value ? a.pg.v : a.pg.k) + row * D + c), x);
+          const float s = pow2((value ? a.pg.v_exp : a.pg.k_exp)[row]);
+#pragma unroll
+          for (int u = 0; u < 4; ++u) x[u] *= s;
+        }
+        store4f(dst, x);
+      } else {
+        const float* src = static_cast<const float*>(a.Q);  // any address: nothing is read where there is no row
+        if (row >= 0) {
+          if constexpr (kPaged) src = static_cast<const float*>(value ? a.pg.v : a.pg.k) + row * D + c;
+          else src = static_cast<const float*>(value ? a.V : a.K) + row * (value ? a.vs.token : a.ks.token) + kvh * (value ? a.vs.head : a.ks.head) + c;
+        }
+        asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(static_cast<uint32_t>(__cvta_generic_to_shared(dst))), "l"(src), "r"(row >= 0 ? 16 : 0)
+                     : "memory");
+      }
+    }
+    asm volatile("cp.async.commit_group;" ::: "memory");
+  };
+  if (t0 < t1) load_tile(false, kKeys * (diag - t0));
   for (int t = t0; t < t1; ++t) {
     const int j0 = kKeys * (diag - t);
-    __syncthreads();  // the tile before has been read
-#pragma unroll (D == 64 ? 8 : 4)
-    for (int e = tid; e < kKeys * (D / 4); e += kThreads) {
-      const int r = e / (D / 4), c = e % (D / 4) * 4;
-      const int p = j0 + r;
-      float x[4] = {0.0f, 0.0f, 0.0f, 0.0f}, y[4] = {0.0f, 0.0f, 0.0f, 0.0f};
-      if (p < end) {
-        if constexpr (kPaged) {
-          const long long row = page_row(a.pg, sq.s, p, kvh, a.err);
-          if (row >= 0) {
-            if constexpr (kQuant) {
-              e4m3_to_float4(*reinterpret_cast<const uint32_t*>(static_cast<const uint8_t*>(a.pg.k) + row * D + c), x);
-              e4m3_to_float4(*reinterpret_cast<const uint32_t*>(static_cast<const uint8_t*>(a.pg.v) + row * D + c), y);
-              const float sk = pow2(a.pg.k_exp[row]), sv = pow2(a.pg.v_exp[row]);
-#pragma unroll
-              for (int u = 0; u < 4; ++u) {
-                x[u] *= sk;
-                y[u] *= sv;
-              }
-            } else {
-              load4f(static_cast<const float*>(a.pg.k) + row * D + c, x);
-              load4f(static_cast<const float*>(a.pg.v) + row * D + c, y);
-            }
-          }
-        } else {
-          const long long tk = sq.c0 + p;
-          load4f(static_cast<const float*>(a.K) + tk * a.ks.token + kvh * a.ks.head + c, x);
-          load4f(static_cast<const float*>(a.V) + tk * a.vs.token + kvh * a.vs.head + c, y);
-        }
-      }
-      store4f(&sm.k[r][c], x);
-      store4f(&sm.v[r][c], y);
-    }
+    __syncthreads();  // V of the tile before has been read
+    load_tile(true, j0);
     MaskT all = 0;  // every mask of the tile (a later tile's gap)
     if (t > 0) {    // suffix ORs over the tile's keys, two a lane; every warp for itself, the first one for all
       const MaskT b0 = bm[j0 + 2 * lane], b1 = bm[j0 + 2 * lane + 1];
@@ -168,6 +170,7 @@ __global__ void __launch_bounds__(kThreads) serve_simt_kernel(ServeArgs a, int C
         sm.suf[2 * lane + 1] = static_cast<MaskT>(after | gap);
       }
     }
+    asm volatile("cp.async.wait_group 1;" ::: "memory");  // K
     __syncthreads();
 
     float x[kR][2];
@@ -213,7 +216,9 @@ __global__ void __launch_bounds__(kThreads) serve_simt_kernel(ServeArgs a, int C
 #pragma unroll
       for (int e = 0; e < kCols; ++e) acc[r][e] *= alpha;
     }
-    __syncwarp();  // a warp's rows of P are its own
+    asm volatile("cp.async.wait_group 0;" ::: "memory");
+    __syncthreads();  // V is there, K has been read (a warp's rows of P are its own)
+    if (t + 1 < t1) load_tile(false, j0 - kKeys);
     gap = static_cast<MaskT>(gap | all);
 #pragma unroll 4
     for (int k = 0; k < kKeys; k += 4) {
@@ -289,8 +294,8 @@ int launch(const ServeArgs& a, cudaStream_t st) {
   if (e != cudaSuccess) return cuda_fail(e, "cudaFuncSetAttribute(serve_simt_kernel)");
   const long long slots = a.sq.T / kRows + static_cast<long long>(a.sq.start ? 2 : 1) * a.sq.S;
   // Blocks of a row tile: up to four while the launch has fewer than four an SM, and no more than the longest window can have key
-  // tiles. With one, two and four: 84, 59 and 53 us in the case above, 100, 77 and 88 us for two prompts of 1,000 tokens with 8/8
-  // heads, 371, 441 and 589 us for four of 2,000 with 16/8.
+  // tiles. With one, two and four (before the last two steps): 84, 59 and 53 us in the case above, 100, 77 and 88 us for two prompts of 1,000
+  // tokens with 8/8 heads, 371, 441 and 589 us for four of 2,000 with 16/8.
   int C = 1;
   while (C < kCluster && slots * a.H * C < 4 * tiles::sm_count() && C * kKeys < a.sq.max_len) C *= 2;
   if (slots * C > 0x7fffffffLL) return fail(PLSH_ERR_RANGE, "too many row tiles");
