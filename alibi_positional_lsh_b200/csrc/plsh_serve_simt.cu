@@ -294,8 +294,8 @@ int launch(const ServeArgs& a, cudaStream_t st) {
   if (e != cudaSuccess) return cuda_fail(e, "cudaFuncSetAttribute(serve_simt_kernel)");
   const long long slots = a.sq.T / kRows + static_cast<long long>(a.sq.start ? 2 : 1) * a.sq.S;
   // Blocks of a row tile: up to four while the launch has fewer than four an SM, and no more than the longest window can have key
-  // tiles. With one, two and four (before the last two steps): 84, 59 and 53 us in the case above, 100, 77 and 88 us for two prompts of 1,000
-  // tokens with 8/8 heads, 371, 441 and 589 us for four of 2,000 with 16/8.
+  // tiles. With one, two and four: 82, 55 and 49 us in the case above, 94, 69 and 80 us for two prompts of 1,000 tokens with 8/8 heads,
+  // 342, 400 and 543 us for four of 2,000 with 16/8.
   int C = 1;
   while (C < kCluster && slots * a.H * C < 4 * tiles::sm_count() && C * kKeys < a.sq.max_len) C *= 2;
   if (slots * C > 0x7fffffffLL) return fail(PLSH_ERR_RANGE, "too many row tiles");
