@@ -23,10 +23,12 @@
 // Per key tile g:
 //   MMA      S(g) = Q K^T once S(g - 1) has been read,  O += P(g - 1) V,  C(g) = A B^T
 //   softmax  P = 4c 2^(S log2e/sqrt(d) - m);  l += sum P
-// The reference m starts at 0 and changes only where a row leaves the range it is good for: a tile's sum above 2^64,
-// or a sum below 2^-30 in the tile of the row's own key (which has the largest weight). fp32 and bf16 hold such P with
-// full relative precision, so no maximum is taken otherwise; the tile is then done again
-// with m = the maximum over its keys with c > 0. No score of a key without weight can push a row's weights out of range.
+// The reference m starts at 0 and changes only where a row leaves the range it is good for: 32 keys' sum above 2^64, or, in
+// the tile of the row's own key (which has the largest count), a sum below 2^-30 as soon as a key with weight is in it. fp32 and bf16
+// hold P between these limits with full relative precision, so no maximum is taken otherwise; these 32 keys are then done
+// again with m = the maximum over those with c > 0, and what was summed before follows by the same power of two. Keys that
+// come before the own one in its tile may hold all of the row's weight: below 2^-126 their P would be zero, and nothing
+// could bring it back. No score of a key without weight can push a row's weights out of range.
 //
 // P is rounded to bf16 for the second product. O is divided by the sum of the rounded P over the row's own 32 keys (a block of the warp's) and of P
 // before them, which takes back most of that rounding where few keys carry the weight (a row's only key then gives its V exactly) and
@@ -342,6 +344,7 @@ serve_tc_kernel(const __grid_constant__ CUtensorMap tmap_q, const __grid_constan
           // which 32-key halves hold weight for some row of the warp, and where the counts come from
           const bool own = rel == (rg >> 1);
           uint32_t nc[16];  // its counts
+          bool early = false;  // own tile of an odd block: keys with weight in the half before the row's own
           if (own) {
 #pragma unroll
             for (int i = 0; i < 4; ++i)
@@ -380,6 +383,7 @@ serve_tc_kernel(const __grid_constant__ CUtensorMap tmap_q, const __grid_constan
           __syncwarp();
           if (lane == 0) mbar_arrive(&sm.s_free);
           if (own) {
+            early = (rg & 1) && ((nc[0] | nc[1] | nc[2] | nc[3]) | (nc[4] | nc[5] | nc[6] | nc[7])) != 0;
 #pragma unroll
             for (int i = 0; i < 32; ++i) {  // byte b as the float 2^23 + b, exactly; then 4 (f - 2^23)
               c0v[i] = __float_as_uint(fmaf(4.0f, __uint_as_float(__byte_perm(nc[i >> 2], 0x4B000000u, 0x7540u | (i & 3))), -33554432.0f));
@@ -413,9 +417,9 @@ serve_tc_kernel(const __grid_constant__ CUtensorMap tmap_q, const __grid_constan
                 f2_unpack(ls2[1], b0, b1);
                 hsum = (a0 + a1) + (b0 + b1);
               }
-              // out of range: a sum too large (or NaN: an infinite exponential of a key without weight), or too small once the
-              // row's own key is in it
-              const bool redo = at >= 0 && (!(hsum <= kSumMax) || (own && hf == (rg & 1) && l + lsum + hsum < kSumMin));
+              // out of range: a sum too large (or NaN: an infinite exponential of a key without weight), or too small though keys
+              // with weight are in it, the own tile's being the first of the row's
+              const bool redo = at >= 0 && (!(hsum <= kSumMax) || (own && (hf == (rg & 1) || early) && l + lsum + hsum < kSumMin));
               if (__any_sync(0xffffffffu, redo)) {
                 // these rows' reference becomes the maximum so far over keys with weight, rounded up to a whole number, so that
                 // everything before follows by an exact power of two (PV(g - 1) has completed: C(g) came after it); the warp's other rows keep their bits
