@@ -165,12 +165,20 @@ __device__ __forceinline__ bool elect_one() {
 // A value that all lanes hold alike, known as such to the compiler.
 __device__ __forceinline__ int uniform(int x) { return __shfl_sync(0xffffffffu, x, 0); }
 
-// 32 bytes of a row in one store.
-__device__ __forceinline__ void store32(void* p, const uint32_t* w) {
-  asm volatile("st.global.v8.b32 [%0], {%1, %2, %3, %4, %5, %6, %7, %8};" ::"l"(p), "r"(w[0]), "r"(w[1]), "r"(w[2]), "r"(w[3]),
-               "r"(w[4]), "r"(w[5]), "r"(w[6]), "r"(w[7])
-               : "memory");
+// 32 bytes of a row, 16-byte aligned; in one store where `whole` says that the address is a multiple of 32 (two stores everywhere:
+// 24 prompts of 1 to 3,001 tokens 176 us instead of 159).
+__device__ __forceinline__ void store32(void* p, const uint32_t* w, bool whole) {
+  if (whole) {
+    asm volatile("st.global.v8.b32 [%0], {%1, %2, %3, %4, %5, %6, %7, %8};" ::"l"(p), "r"(w[0]), "r"(w[1]), "r"(w[2]), "r"(w[3]),
+                 "r"(w[4]), "r"(w[5]), "r"(w[6]), "r"(w[7])
+                 : "memory");
+  } else {
+    uint4* const dst = static_cast<uint4*>(p);
+    dst[0] = make_uint4(w[0], w[1], w[2], w[3]);
+    dst[1] = make_uint4(w[4], w[5], w[6], w[7]);
+  }
 }
+__device__ __forceinline__ bool aligned32(const void* p) { return (reinterpret_cast<uintptr_t>(p) & 31u) == 0; }
 
 // Row r of a 0/1 operand: byte k is 0x40 (e4m3 2.0) where bit k is set. Four bits spread to four bytes by one multiply.
 __device__ __forceinline__ uint32_t spread4(uint32_t bits) { return ((bits & 0xFu) * (0x00204081u << 6)) & 0x40404040u; }
@@ -508,8 +516,9 @@ serve_tc_kernel(const __grid_constant__ CUtensorMap tmap_q, const __grid_constan
           }
           if (!done) p_written();
           if (d_at >= 0) {
+            const bool whole = aligned32(O);
 #pragma unroll
-            for (int c = 0; c < D; c += 16) store32(O + static_cast<size_t>(d_at) * D + c, o + c / 2);
+            for (int c = 0; c < D; c += 16) store32(O + static_cast<size_t>(d_at) * D + c, o + c / 2, whole);
             row_sum[d_at] = (__log2f(d_l) + d_m - 2.0f) * 0.6931471805599453f - prm.log_s;
           }
         }
@@ -916,7 +925,7 @@ __global__ void __launch_bounds__(256) gather_kernel(SeqArgs sq, PageArgs pg, co
         o[2 * i] = pack_bf16x2(f[0] * sc, f[1] * sc);
         o[2 * i + 1] = pack_bf16x2(f[2] * sc, f[3] * sc);
       }
-      store32(out[kv], o);
+      store32(out[kv], o, aligned32(out[kv]));
     }
   }
 }

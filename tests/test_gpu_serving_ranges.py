@@ -54,3 +54,52 @@ def test_rows_whose_scores_all_lie_far_below_zero(d, kind, score):
     cache.append(k, v, pt, _cu(lens), _at(*[0] * len(lens)))
     _check_chunks(plan, cache, pt, q, lens, [33, 40, 70, 100, 150])
     _check_chunks(plan, cache, pt, q, lens, [1] * 5, max_new=1)
+
+
+def _shifted(x):
+    """A copy of x 16 bytes into a larger buffer: aligned to 16 bytes and to no more."""
+    n = 16 // x.element_size()
+    y = torch.empty(x.numel() + n, dtype=x.dtype, device=x.device)[n:].view(x.shape)
+    assert y.data_ptr() % 32 == 16
+    return y.copy_(x)
+
+
+@pytest.mark.parametrize("d,dtype", [(128, BF16), (64, BF16), (64, F32)])
+def test_tensors_aligned_to_16_bytes(d, dtype):
+    import alibi_positional_lsh_b200 as m
+    H, H_kv, s, page, lens = 4, 2, 20, 32, [200, 1, 77, 130]
+    T, g, n = sum(lens), _gen(71), len(lens)
+    plan = _plan(H, H_kv, 210, d, s, dtype)
+    q, k, v = (_randn(g, T, h, d, dtype=dtype) for h in (H, H_kv, H_kv))
+    cu, zero = _cu(lens), _at(*[0] * n)
+    sq, sk, sv = _shifted(q), _shifted(k), _shifted(v)
+    out = _shifted(torch.zeros_like(q)), _shifted(torch.zeros((T, H), device="cuda:0"))
+    want = plan.attend_packed(q, k, v, cu)
+    got = plan.attend_packed(sq, sk, sv, cu, out=out)
+    assert all(torch.equal(a, b) for a, b in zip(want, got))
+    pt, num = _table_of(lens, page)
+    for kind in (E4M3, dtype):
+        a = _cache(num, H_kv, page, d, kind)
+        b = m.PagedCache(*(None if x is None else _shifted(x) for x in (a.k_pages, a.v_pages, a.k_exp, a.v_exp)))
+        a.append(k, v, pt, cu, zero)
+        b.append(sk, sv, pt, cu, zero)
+        rows = a.read(pt, cu, zero, T, dtype=dtype)
+        back = b.read(pt, cu, zero, T, out=(_shifted(torch.zeros_like(k)), _shifted(torch.zeros_like(v))))
+        assert all(torch.equal(x, y) for x, y in zip(rows, back))
+        for most in (None, 200):
+            want = plan.attend_paged(q, a, pt, cu, zero, max_new=most)
+            got = plan.attend_paged(sq, b, pt, cu, zero, max_new=most, out=out)
+            assert all(torch.equal(x, y) for x, y in zip(want, got))
+        tok, one = _at(*[L - 1 for L in lens]), _cu([1] * n)
+        want = plan.attend_paged(q[:n], a, pt, one, tok, max_new=1)
+        got = plan.attend_paged(sq[:n], b, pt, one, tok, max_new=1, out=(out[0][:n], out[1][:n]))
+        assert all(torch.equal(x, y) for x, y in zip(want, got))
+        if kind == E4M3 and dtype == BF16:
+            scratch = _shifted(torch.zeros(m.plsh_paged_scratch_bytes(T, n, T, H_kv, d, plan.max_window), dtype=torch.uint8, device="cuda:0"))
+            want = plan.attend_paged(q, a, pt, cu, zero)
+            err = torch.zeros(4, dtype=torch.int32, device="cuda:0")
+            m.plsh_paged_fwd(q, m.PLSH_BF16, cu, zero, T, H, H_kv, d, b.k_pages, b.v_pages, b.k_exp, b.v_exp, pt, s, 210, plan.table_dev,
+                             plan.spans, plan.bmask, plan.near, plan.windows_host, scratch, out[0], out[1], err)
+            assert all(torch.equal(x, y) for x, y in zip(want, out)) and int(err.abs().max()) == 0
+        b.check()
+    plan.check()
