@@ -18,7 +18,7 @@ using namespace serve;
 constexpr int kThreads = 256;
 constexpr int kTokens = 8;  // most tokens of a block
 
-// The rows of head 0 of a block's tokens, -1 where there is none.
+// The rows of head 0 of a block's tokens: -1 where the token is of no sequence, -2 where its page is not there.
 __device__ __forceinline__ void find_rows(const SeqArgs& sq, const PageArgs& pg, int t0, int n, long long* base, uint32_t* err) {
   if (blockIdx.x == 0) check_seqs(sq, err);
   const int tid = threadIdx.x;
@@ -31,7 +31,12 @@ __device__ __forceinline__ void find_rows(const SeqArgs& sq, const PageArgs& pg,
       else hi = mid;
     }
     const Seq q = load_seq(sq, lo);
-    base[tid] = t >= q.c0 && t < q.c0 + q.len ? page_row(pg, q.s, q.pos0 + t - q.c0, 0, err) : -1;
+    long long row = -1;
+    if (t >= q.c0 && t < q.c0 + q.len) {
+      row = page_row(pg, q.s, q.pos0 + t - q.c0, 0, err);
+      if (row < 0) row = -2;
+    }
+    base[tid] = row;
   }
   __syncthreads();
 }
@@ -114,9 +119,15 @@ read_kernel(SeqArgs sq, PageArgs pg, int tokens, T* __restrict__ K, T* __restric
 #pragma unroll 2
   for (int i = threadIdx.x / kLanes; i < rows; i += kThreads / kLanes) {
     const int k = i / pg.H_kv, h = i % pg.H_kv;
-    if (base[k] < 0) continue;
-    const long long row = base[k] + (static_cast<long long>(h) << pg.lg_page);
     const long long out = (static_cast<long long>(t0 + k) * pg.H_kv + h) * D;
+    if (base[k] < 0) {
+      if (base[k] == -2) {
+        __stcs(reinterpret_cast<uint4*>(K + out) + l, make_uint4(0, 0, 0, 0));
+        __stcs(reinterpret_cast<uint4*>(V + out) + l, make_uint4(0, 0, 0, 0));
+      }
+      continue;
+    }
+    const long long row = base[k] + (static_cast<long long>(h) << pg.lg_page);
 #pragma unroll
     for (int kv = 0; kv < 2; ++kv) {
       const void* pages = kv == 0 ? pg.k : pg.v;

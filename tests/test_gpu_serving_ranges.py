@@ -122,3 +122,27 @@ def test_values_up_to_2_to_the_80_under_high_scores(d, kind, dtype, score):
     cache.append(k, v, pt, _cu(lens), _at(*[0] * len(lens)))
     _check_chunks(plan, cache, pt, q, lens, [33, 40, 100, 150])
     _check_chunks(plan, cache, pt, q, lens, [1] * 4, max_new=1)
+
+
+@pytest.mark.parametrize("kind,d,dtype", [(E4M3, 128, BF16), (E4M3, 64, F32), (BF16, 64, BF16), (F32, 128, F32)])
+def test_rows_whose_page_is_not_there_read_as_zeros(kind, d, dtype):
+    H_kv, page, lens, starts = 3, 16, [40, 1, 30], [3, 0, 20]
+    T, g = sum(lens), _gen(73)
+    pt, num = _table_of([a + b for a, b in zip(lens, starts)], page)
+    cache = _cache(num, H_kv, page, d, kind)
+    cu, st = _cu(lens), _at(*starts)
+    cache.append(_randn(g, T, H_kv, d, dtype=dtype), _randn(g, T, H_kv, d, dtype=dtype), pt, cu, st)
+    whole = cache.read(pt, cu, st, T, dtype=dtype)
+    cache.check()
+    for bad in (-1, num, 2 ** 31 - 1, -2 ** 31):
+        cut = pt.clone()
+        cut[0, 1], cut[2, 2] = bad, bad
+        lost = torch.zeros(T + 2, dtype=torch.bool, device="cuda:0")
+        for t, p, s in [(i, 3 + i, 0) for i in range(40)] + [(41 + i, 20 + i, 2) for i in range(30)]:
+            lost[t] = p // page == (1 if s == 0 else 2)
+        out = tuple(torch.full((T + 2, H_kv, d), 7.0, dtype=dtype, device="cuda:0") for _ in range(2))
+        cache.read(cut, cu, st, T + 2, out=out)
+        assert cache.device_errors() == ["PAGE"]
+        cache.reset_errors()
+        for x, w in zip(out, whole):
+            assert (x[lost] == 0).all() and torch.equal(x[:T][~lost[:T]], w[~lost[:T]]) and (x[T:] == 7.0).all()
