@@ -117,10 +117,30 @@ def _empty(like: torch.Tensor, stream: Optional[torch.cuda.Stream], *shape: int)
         return like.new_empty(*shape)
 
 
-class _Errors:
-    """The device error word of an object's calls."""
+class _Kept:
+    """An object whose calls pass addresses and sizes that were looked up once: its attributes cannot be exchanged (memory that a
+    call still reads would be freed), and a copy looks its own up. Also the device error word of the calls."""
 
     err: torch.Tensor
+
+    def _keep(self) -> dict:
+        """What the calls need of the object's tensors, by attribute."""
+        raise NotImplementedError
+
+    def _fix(self) -> None:
+        self.__dict__.update(self._keep(), _fixed=True)
+
+    def __setattr__(self, name: str, value) -> None:
+        if "_fixed" in self.__dict__ and name in self.__dict__:
+            raise AttributeError(f"{name} cannot be exchanged: the calls go on with what the object was made of")
+        super().__setattr__(name, value)
+
+    def __delattr__(self, name: str) -> None:
+        raise AttributeError(f"{name} cannot be taken out")
+
+    def __setstate__(self, state: dict) -> None:  # copies and pickles: other tensors, other addresses
+        self.__dict__.update(state)
+        self._fix()
 
     def reset_errors(self) -> None:
         self.err.zero_()
@@ -136,7 +156,7 @@ class _Errors:
             raise PlshError(-1, "device reported " + ",".join(errs))
 
 
-class PagedCache(_Errors):
+class PagedCache(_Kept):
     """K and V of many sequences in pages [num_pages][H_kv][page_size][d].
 
     dtype torch.float8_e4m3fn: each row is held as e4m3 values times a power of two, whose exponent is in
@@ -167,9 +187,12 @@ class PagedCache(_Errors):
         self._tensors = k_pages, v_pages, k_exp, v_exp
         self.err = torch.zeros((4,), dtype=torch.int32, device=self.device)
         self._like = {t: torch.empty((0,), dtype=t, device=self.device) for t in _CODES}  # what new tensors are made from
-        self._pages = tuple(0 if x is None else x.data_ptr() for x in self._tensors)
+        self._fix()
 
-    # the cache's own tensors, which cannot be exchanged: the calls keep their addresses
+    def _keep(self) -> dict:
+        return {"_pages": tuple(0 if x is None else x.data_ptr() for x in self._tensors)}
+
+    # the cache's own tensors
     k_pages = property(lambda self: self._tensors[0])
     v_pages = property(lambda self: self._tensors[1])
     k_exp = property(lambda self: self._tensors[2])
@@ -231,7 +254,7 @@ class PagedCache(_Errors):
         return K, V
 
 
-class PlshServing(_Errors):
+class PlshServing(_Kept):
     """T~ (causal) for sequences of up to max_len positions, all with one table."""
 
     def __init__(self, H: int, H_kv: int, max_len: int, d: int, s: int, sigma: Sequence[float], seed: int = 0,
@@ -272,11 +295,14 @@ class PlshServing(_Errors):
             self.check()  # waits for the plan, so that any stream may use it from here on
             self.windows_host = self.bmax.cpu().numpy()  # the heads' longest blocks
         self.max_window = int(self.windows_host.max())
-        self._windows = self.windows_host.ctypes.data
         self._like = tuple(torch.empty((0,), dtype=t, device=self.device) for t in (dtype, torch.float32, torch.uint8))
-        self._code, self._err = _CODES[dtype], self.err.data_ptr()
-        self._table = self.table_dev.data_ptr()
-        self._plan = self.spans.data_ptr(), self.bmask.data_ptr(), self.near.data_ptr()
+        self._code = _CODES[dtype]
+        self._fix()
+
+    def _keep(self) -> dict:
+        self.windows_host.flags.writeable = False
+        return {"_windows": self.windows_host.ctypes.data, "_err": self.err.data_ptr(), "_table": self.table_dev.data_ptr(),
+                "_plan": (self.spans.data_ptr(), self.bmask.data_ptr(), self.near.data_ptr())}
 
     def _outputs(self, T: int, out, stream) -> Tuple[torch.Tensor, torch.Tensor]:
         if out is None:

@@ -146,3 +146,32 @@ def test_rows_whose_page_is_not_there_read_as_zeros(kind, d, dtype):
         cache.reset_errors()
         for x, w in zip(out, whole):
             assert (x[lost] == 0).all() and torch.equal(x[:T][~lost[:T]], w[~lost[:T]]) and (x[T:] == 7.0).all()
+
+
+@pytest.mark.parametrize("dtype,d", [(BF16, 128), (F32, 64)])
+def test_plans_and_caches_keep_what_they_were_made_of(dtype, d):
+    """Neither tensors nor sizes can be exchanged under the calls; deep copies have tensors of their own."""
+    import copy
+    H, H_kv, page, lens = 4, 2, 16, [50, 1, 70]
+    T, g, zero = sum(lens), _gen(74), _at(0, 0, 0)
+    plan = _plan(H, H_kv, 80, d, 20, dtype)
+    pt, num = _table_of(lens, page)
+    cache = _cache(num, H_kv, page, d, E4M3)
+    for x, names in ((plan, "spans bmask near table_dev err windows_host max_window H H_kv d s max_len dtype device"),
+                     (cache, "k_pages v_pages k_exp v_exp err num_pages H_kv page_size d dtype device quantised")):
+        for name in names.split():
+            with pytest.raises(AttributeError):
+                setattr(x, name, getattr(x, name))
+    with pytest.raises(ValueError):
+        plan.windows_host[0] = 1 << 20
+    q, k, v = (_randn(g, T, h, d, dtype=dtype) for h in (H, H_kv, H_kv))
+    cache.append(k, v, pt, _cu(lens), zero)
+    want = plan.attend_paged(q, cache, pt, _cu(lens), zero) + plan.attend_packed(q, k, v, _cu(lens))
+    plan2, cache2 = copy.deepcopy(plan), copy.deepcopy(cache)
+    for t in (cache.k_pages, cache.v_pages):  # the first cache's rows go, the copy's stay
+        t.view(torch.uint8).zero_()
+    plan.spans.zero_()
+    plan.near.zero_()
+    got = plan2.attend_paged(q, cache2, pt, _cu(lens), zero) + plan2.attend_packed(q, k, v, _cu(lens))
+    plan2.check()
+    assert all(torch.equal(a, b) for a, b in zip(want, got))

@@ -111,3 +111,30 @@ def test_plain_quantiser_agrees_with_torch_and_keeps_its_definition():
     scaled = x.double() * torch.exp2(-torch.tensor(exp).double())[..., None]
     assert np.array_equal(scaled.float().to(torch.float8_e4m3fn).view(torch.uint8).numpy(), byte)
     assert np.array_equal(plain.values(byte, exp), scaled.float().to(torch.float8_e4m3fn).double().numpy() * (2.0 ** exp.astype(float))[..., None])
+
+
+def test_what_the_calls_keep_addresses_of_cannot_be_exchanged(plsh):
+    import copy
+    from alibi_positional_lsh_b200.serving import _Kept
+
+    class Kept(_Kept):
+        def __init__(self):
+            self.t, self.size = torch.arange(4), 4
+            self._fix()
+
+        def _keep(self):
+            return {"_at": self.t.data_ptr()}
+
+    x = Kept()
+    for name in ("t", "size", "_at"):
+        with pytest.raises(AttributeError):
+            setattr(x, name, 1)
+        with pytest.raises(AttributeError):
+            delattr(x, name)
+    x.note = "the caller's own"
+    for y in (copy.copy(x), copy.deepcopy(x)):
+        assert y._at == y.t.data_ptr() and torch.equal(y.t, x.t) and y.note == x.note
+        with pytest.raises(AttributeError):
+            y.t = x.t
+    assert copy.deepcopy(x)._at != x._at
+    assert issubclass(plsh.PagedCache, _Kept) and issubclass(plsh.PlshServing, _Kept)
