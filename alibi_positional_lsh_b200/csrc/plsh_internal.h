@@ -121,7 +121,7 @@ struct ServeArgs {
   int dtype, H, H_kv, d, s;
   const int32_t* spans; const void* bmask;  // plsh_window's, causal, over max_len positions
   const uint8_t* near;                      // launch_near's; the tile kernels'
-  const double* table;                      // [H][s][2]; the row kernel's
+  const double* table;                      // [H][s][2]; the row kernel's and the gather's
   // paged bf16: sequences with at most this many new tokens are the row kernel's, the others the tile kernel's (0: all theirs)
   int few;
   const int32_t* windows_host;              // [H], host: the heads' longest blocks

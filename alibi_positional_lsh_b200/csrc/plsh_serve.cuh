@@ -12,6 +12,7 @@
 #include <cuda_bf16.h>
 #include <cuda_fp16.h>
 
+#include "plsh_binid.cuh"
 #include "plsh_internal.h"
 
 namespace plsh {
@@ -65,15 +66,41 @@ __device__ __forceinline__ int warp_find(const int32_t* cu, int S, int lg_tile, 
 
 // ---------------------------------------------------------------- pages
 
-// The row (page, head, place in the page) of position p, or -1 (and PLSH_DEVERR_PAGE) where the page table has none.
-__device__ __forceinline__ long long page_row(const PageArgs& g, int s, int p, int kvh, uint32_t* err) {
+// The page of position p, or -1 where the page table has none.
+__device__ __forceinline__ int find_page(const PageArgs& g, int s, int p) {
   const int slot = p >> g.lg_page;
   const int page = slot < g.width ? g.table[static_cast<long long>(s) * g.width + slot] : -1;
-  if (page < 0 || page >= g.num_pages) {
-    atomicOr(err, PLSH_DEVERR_PAGE);
-    return -1;
-  }
+  return page >= 0 && page < g.num_pages ? page : -1;
+}
+
+// The row (page, head, place in the page) of position p, or -1.
+__device__ __forceinline__ long long find_row(const PageArgs& g, int s, int p, int kvh) {
+  const int page = find_page(g, s, p);
+  if (page < 0) return -1;
   return ((static_cast<long long>(page) * g.H_kv + kvh) << g.lg_page) + (p & ((1 << g.lg_page) - 1));
+}
+
+// The same of a position that the call needs: PLSH_DEVERR_PAGE where there is none.
+__device__ __forceinline__ long long page_row(const PageArgs& g, int s, int p, int kvh, uint32_t* err) {
+  const long long row = find_row(g, s, p, kvh);
+  if (row < 0) atomicOr(err, PLSH_DEVERR_PAGE);
+  return row;
+}
+
+// The first position of the block of hash `b` that holds p.
+__device__ __forceinline__ int block_begin(const Binning& b, int p) {
+  if (!b.ok) return 0;
+  const int32_t id = b.at(p);
+  const double x = ceil((static_cast<double>(id) + b.base) * b.delta - b.u);  // at most a rounding away
+  const int guess = x <= 0.0 ? 0 : x >= static_cast<double>(p) ? p : static_cast<int>(x);
+  if (b.at(guess) == id && (guess == 0 || b.at(guess - 1) != id)) return guess;
+  int good = p, bad = -1;  // ids do not decrease
+  while (good - bad > 1) {
+    const int mid = bad + (good - bad) / 2;
+    if (b.at(mid) == id) good = mid;
+    else bad = mid;
+  }
+  return good;
 }
 
 // 2^e as a float, -126 <= e <= 127.

@@ -35,7 +35,6 @@
 // (32 MB in 32 us, a quarter of the issue slots: what the warps wait for is the first keys and each other).
 #include <cooperative_groups.h>
 
-#include "plsh_binid.cuh"
 #include "plsh_serve.cuh"
 #include "plsh_tile_common.cuh"
 
@@ -87,22 +86,6 @@ struct Layout {
     total = at;
   }
 };
-
-// The first position of the block of hash `b` that holds p.
-__device__ __forceinline__ int block_begin(const Binning& b, int p) {
-  if (!b.ok) return 0;
-  const int32_t id = b.at(p);
-  const double x = ceil((static_cast<double>(id) + b.base) * b.delta - b.u);  // at most a rounding away
-  const int guess = x <= 0.0 ? 0 : x >= static_cast<double>(p) ? p : static_cast<int>(x);
-  if (b.at(guess) == id && (guess == 0 || b.at(guess - 1) != id)) return guess;
-  int good = p, bad = -1;  // ids do not decrease
-  while (good - bad > 1) {
-    const int mid = bad + (good - bad) / 2;
-    if (b.at(mid) == id) good = mid;
-    else bad = mid;
-  }
-  return good;
-}
 
 __device__ __forceinline__ void mma_f16(float (&c)[4], uint32_t a0, uint32_t a1, uint32_t a2, uint32_t a3, uint32_t b0, uint32_t b1) {
   asm volatile("mma.sync.aligned.m16n8k16.row.col.f32.f16.f16.f32 {%0, %1, %2, %3}, {%4, %5, %6, %7}, {%8, %9}, {%0, %1, %2, %3};"

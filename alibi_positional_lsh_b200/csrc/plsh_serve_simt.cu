@@ -123,15 +123,17 @@ __global__ void __launch_bounds__(kThreads) serve_simt_kernel(ServeArgs a, int C
     for (int e = 0; e < kCols; ++e) acc[r][e] = 0.0f;
   }
 
-  // K or V of a key tile into shared memory, rows past the end as zeros. fp32 rows are copied behind the arithmetic: V under S, the
-  // next tile's K under P V; e4m3 rows go through registers.
+  // K or V of a key tile into shared memory, rows past the end or without a page as zeros. fp32 rows are copied behind the arithmetic: V
+  // under S, the next tile's K under P V; e4m3 rows go through registers. Returns the last of this thread's rows without a page.
   auto load_tile = [&](bool value, int j0) {
+    int missing = -1;
 #pragma unroll (D == 64 ? 4 : 2)
     for (int e = tid; e < kKeys * (D / 4); e += kThreads) {
       const int r = e / (D / 4), c = e % (D / 4) * 4, p = j0 + r;
       float* const dst = value ? &sm.v[r][c] : &sm.k[r][c];
       long long row = -1;
-      if (p < end) row = kPaged ? page_row(a.pg, sq.s, p, kvh, a.err) : sq.c0 + p;
+      if (p < end) row = kPaged ? find_row(a.pg, sq.s, p, kvh) : sq.c0 + p;
+      if (kPaged && p < end && row < 0) missing = r;
       if constexpr (kQuant) {
         float x[4] = {0.0f, 0.0f, 0.0f, 0.0f};
         if (row >= 0) {
@@ -152,12 +154,25 @@ __global__ void __launch_bounds__(kThreads) serve_simt_kernel(ServeArgs a, int C
       }
     }
     asm volatile("cp.async.commit_group;" ::: "memory");
+    return missing;
+  };
+  // A tile's first key that the call's first row reaches (kKeys: none): in pages, what lies before it is no longer the sequence's own
+  // and may be anything, not finite or not there.
+  const int r0 = max(0, sq.pos0 - i0);
+  auto lowest = [](uint32_t even, uint32_t odd) {  // of keys 2 i and 2 i + 1
+    return min(even ? 2 * (__ffs(even) - 1) : kKeys, odd ? 2 * (__ffs(odd) - 1) + 1 : kKeys);
   };
   if (t0 < t1) load_tile(false, kKeys * (diag - t0));
   for (int t = t0; t < t1; ++t) {
     const int j0 = kKeys * (diag - t);
     __syncthreads();  // V of the tile before has been read
-    load_tile(true, j0);
+    const int missing = load_tile(true, j0);
+    int reach = 0;
+    if (kPaged && t == 0) {
+      auto reached = [&](int key) { return __ballot_sync(0xffffffffu, j0 + key >= i0 + r0 || sm.c[r0][key] > 0); };
+      const uint32_t even = reached(2 * lane), odd = reached(2 * lane + 1);
+      reach = lowest(even, odd);
+    }
     MaskT all = 0;  // every mask of the tile (a later tile's gap)
     if (t > 0) {    // suffix ORs over the tile's keys, two a lane; every warp for itself, the first one for all
       const MaskT b0 = bm[j0 + 2 * lane], b1 = bm[j0 + 2 * lane + 1];
@@ -165,6 +180,11 @@ __global__ void __launch_bounds__(kThreads) serve_simt_kernel(ServeArgs a, int C
       MaskT after = __shfl_down_sync(0xffffffffu, inc, 1);
       if (lane == 31) after = 0;
       all = __shfl_sync(0xffffffffu, inc, 0);
+      if (kPaged) {
+        auto reached = [&](MaskT between) { return __ballot_sync(0xffffffffu, popc_mask<MaskT>(static_cast<MaskT>(sm.own[r0] | between | gap)) < a.s); };
+        const uint32_t even = reached(static_cast<MaskT>(after | b1)), odd = reached(after);
+        reach = lowest(even, odd);
+      }
       if (warp == 0) {
         sm.suf[2 * lane] = static_cast<MaskT>(after | b1 | gap);
         sm.suf[2 * lane + 1] = static_cast<MaskT>(after | gap);
@@ -217,6 +237,11 @@ __global__ void __launch_bounds__(kThreads) serve_simt_kernel(ServeArgs a, int C
       for (int e = 0; e < kCols; ++e) acc[r][e] *= alpha;
     }
     asm volatile("cp.async.wait_group 0;" ::: "memory");
+    if (kPaged) {
+      if (missing >= reach) atomicOr(a.err, PLSH_DEVERR_PAGE);
+      // V there meets weights of zero, which a NaN would not leave: the thread that copied it clears it (K's scores are not taken)
+      for (int e = tid; e < reach * (D / 4); e += kThreads) *reinterpret_cast<float4*>(&sm.v[e / (D / 4)][e % (D / 4) * 4]) = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
+    }
     __syncthreads();  // V is there, K has been read (a warp's rows of P are its own)
     if (t + 1 < t1) load_tile(false, j0 - kKeys);
     gap = static_cast<MaskT>(gap | all);

@@ -77,6 +77,9 @@ constexpr uint32_t kRegsSoftmax = 216, kRegsRest = 40;
 struct Item {
   int valid, h, i0, c0, pos0, end, s, top, low;
   int kv0;  // row of K and V that holds position 0
+  // K and V from pages: the first row reaches every key from `sure` on, and the lowest it reaches is `reach` (looked for on the way
+  // down below `sure`; known already where that is 0)
+  int reach, sure;
 };
 
 // The sum of 32 bf16, in fp32.
@@ -106,6 +109,7 @@ struct __align__(1024) TcSmem {
   MaskT rows[2][kRows + kRows / 2];
   MaskT gap[2], upper[2];   // [stage]: OR between the key tile and the row tile; OR of the key tile's keys 32..63
   Item item[kItems];
+  int missing[2 * kItems], reach[2 * kItems];  // of an item, by its number (see the loads)
   int16_t order[kMaxSortedHeads];
   int32_t width[kMaxSortedHeads];
   uint64_t item_full[kItems], item_empty[kItems];
@@ -522,6 +526,10 @@ serve_tc_kernel(const __grid_constant__ CUtensorMap tmap_q, const __grid_constan
             for (int c = 0; c < D; c += 16) store32(O + static_cast<size_t>(d_at) * D + c, o + c / 2, whole);
             row_sum[d_at] = (__log2f(d_l) + d_m - 2.0f) * 0.6931471805599453f - prm.log_s;
           }
+          if (kPaged && threadIdx.x == 0) {
+            const int x = (items - 1) % (2 * kItems);
+            if (sm.missing[x] >= sm.reach[x]) atomicOr(err, PLSH_DEVERR_PAGE);
+          }
         }
         if (done) break;
       }
@@ -558,11 +566,17 @@ serve_tc_kernel(const __grid_constant__ CUtensorMap tmap_q, const __grid_constan
         if (lane == 0) atomicOr(err, PLSH_DEVERR_WINDOW);
         lo = i0;
       }
+      // a tile that begins before the new tokens: its first row's window begins between this tile's own and the next one's
+      int reach = lo, sure = 0;
+      if (kPaged && i0 < sq.pos0) {
+        sure = tile + 1 < T128 ? prm.spans[(static_cast<size_t>(h) * T128 + tile + 1) * 2] : end;
+        reach = min(sure, sq.pos0);
+      }
       const int at = k % kItems;
       if (k >= kItems && !wait_all(&sm.item_empty[at], k / kItems + 1)) { ok = false; break; }
       if (lane == 0) {
         sm.item[at] = Item{1, h, i0, sq.c0, sq.pos0, end, si, min((i0 + kRows - 1) >> 6, (end - 1) >> 6), lo >> 6,
-                           sq.c0 - sq.pos0 + (prm.kv_pad ? (si + 1) * prm.kv_pad - kKeys : 0)};
+                           sq.c0 - sq.pos0 + (prm.kv_pad ? (si + 1) * prm.kv_pad - kKeys : 0), reach, sure};
         mbar_arrive(&sm.item_full[at]);
       }
       ++k;
@@ -591,25 +605,21 @@ serve_tc_kernel(const __grid_constant__ CUtensorMap tmap_q, const __grid_constan
         mbar_arrive(&sm.item_empty[k % kItems]);
         if (!it.valid) break;
         const int kvh = it.h / (H / prm.H_kv);
-        // a tile of K or V: one box, or one for each page that it touches. Pages behind the sequence's end are not looked up (their rows
-        // are cleared), and one outside the pool is replaced by page 0: the call reports it, and reads nothing else's memory.
+        // A tile of K or V: one box, or one for each page that it touches. Behind the sequence's end, and where the table names no page of
+        // the pool, a box outside the tensor: zeros. The item's last position without a page is noted, and is an error if the item's rows
+        // reach it, which the warp of the counts' operands finds out as it goes down the tiles (the epilogue compares).
+        int missing = -1;
         auto load_tile = [&](uint8_t* dst, const CUtensorMap* map, int swap, int u, uint64_t* bar) {
           if constexpr (kPaged) {
             const int rows = min(kKeys, 1 << prm.pg.lg_page);
 #pragma unroll 1
             for (int r = 0; r < kKeys; r += rows) {
-              const int p = kKeys * u + r, slot = p >> prm.pg.lg_page;
-              int page = 0;
-              if (p < it.end) {
-                page = slot < prm.pg.width ? prm.pg.table[static_cast<long long>(it.s) * prm.pg.width + slot] : -1;
-                if (page < 0 || page >= prm.pg.num_pages) {
-                  atomicOr(err, PLSH_DEVERR_PAGE);
-                  page = 0;
-                }
-              }
+              const int p = kKeys * u + r, page = p < it.end ? find_page(prm.pg, it.s, p) : -1;
+              if (page < 0 && p < it.end) missing = max(missing, min(p + rows, it.end) - 1);
+              const int plane = page < 0 ? -1 : page * prm.H_kv + kvh;
 #pragma unroll 1
               for (int c = 0; c < D / 64; ++c)
-                tma_load_3d(dst + c * (kKeys * 128) + r * 128, map, 64 * c, p & ((1 << prm.pg.lg_page) - 1), page * prm.H_kv + kvh, bar);
+                tma_load_3d(dst + c * (kKeys * 128) + r * 128, map, 64 * c, p & ((1 << prm.pg.lg_page) - 1), plane, bar);
             }
           } else {
             const int t = it.kv0 + kKeys * u;
@@ -623,6 +633,7 @@ serve_tc_kernel(const __grid_constant__ CUtensorMap tmap_q, const __grid_constan
           if (n >= kStages && !wait(&sm.k_empty[st], n / kStages + 1)) { ok = false; break; }
           mbar_arrive_expect_tx(&sm.k_full[st], Smem::kKBytes);
           load_tile(sm.k[st], &tmap_k, prm.k_swap, u, &sm.k_full[st]);
+          if (kPaged) sm.missing[k % (2 * kItems)] = missing;  // read once the item's last V has been used
           if (u == it.top) {
             if (loads && !wait(&sm.q_empty, loads + 1)) { ok = false; ++n; break; }
             const int tq = it.c0 - it.pos0 + it.i0;
@@ -748,6 +759,8 @@ serve_tc_kernel(const __grid_constant__ CUtensorMap tmap_q, const __grid_constan
       if (!wait_all(&sm.item_full[k % kItems], k / kItems)) break;
       const Item& item = sm.item[k % kItems];
       const int valid = item.valid, first = item.top, low = item.low, end = item.end, i0 = item.i0, h = item.h;
+      const int p0 = max(i0, item.pos0), sure = item.sure;  // p0: the first row
+      int reach = item.reach;
       const MaskT* bm = bmask + static_cast<size_t>(h) * max_len;
       __syncwarp();
       if (lane == 0) mbar_arrive(&sm.item_empty[k % kItems]);
@@ -814,15 +827,41 @@ serve_tc_kernel(const __grid_constant__ CUtensorMap tmap_q, const __grid_constan
           sm.gap[fs] = gap;
           sm.upper[fs] = t1;
         }
+        // rows past the end: another sequence's, or nothing at all. From pages, also rows of pages before the one of the lowest key
+        // that the first row reaches (no later row reaches further): they are no longer the sequence's own.
+        int own = 0;
+        if constexpr (kPaged) {
+          const int up = p0 - kKeys * u;  // the first row's place, if it lies in this tile
+          if (kKeys * u < sure && up >= 0) {
+            __syncwarp();
+            // OR after the key up to the tile's end, and from there to the first row
+            MaskT b0 = static_cast<MaskT>(a0 | t1), b1 = a1, between = 0;
+            if (up >= kKeys) {
+              between = rel < 0 ? static_cast<MaskT>(gap | rows[p0 - i0]) : rows[64 + p0 - i0];
+            } else {  // only boundaries up to the first row
+              b1 = tiles::warp_suffix_or<MaskT>(32 + lane <= up ? kv[1] : static_cast<MaskT>(0), lane);
+              b0 = tiles::warp_suffix_or<MaskT>(lane <= up ? kv[0] : static_cast<MaskT>(0), lane);
+              const MaskT u1 = __shfl_sync(0xffffffffu, b1, 0);
+              b1 = __shfl_down_sync(0xffffffffu, b1, 1);
+              b0 = __shfl_down_sync(0xffffffffu, b0, 1);
+              if (lane == 31) b1 = b0 = 0;
+              b0 = static_cast<MaskT>(b0 | u1);
+            }
+            const uint32_t n0 = __ballot_sync(0xffffffffu, static_cast<MaskT>(FULL & ~(b0 | between)) != 0);
+            const uint32_t n1 = __ballot_sync(0xffffffffu, static_cast<MaskT>(FULL & ~(b1 | between)) != 0);
+            if (n0 | n1) reach = min(reach, kKeys * u + (n0 ? __ffs(n0) - 1 : 31 + __ffs(n1)));
+          }
+          own = min(kKeys, max(0, (reach >> prm.pg.lg_page << prm.pg.lg_page) - kKeys * u));
+          if (lane == 0) sm.reach[k % (2 * kItems)] = reach;
+        }
         if (rel < 0) gap = static_cast<MaskT>(gap | t0 | t1);
-        // rows past the end: another sequence's, or nothing at all
-        if (kKeys * (u + 1) > end) {
+        if (own > 0 || kKeys * (u + 1) > end) {
           const int st = g % kStages, sv = g % kVStages;
           if (!wait_all(&sm.k_full[st], g / kStages) || !wait_all(&sm.v_full[sv], g / kVStages)) { ok = false; break; }
-          const int r0 = end - kKeys * u;
+          const int past = min(kKeys, end - kKeys * u);
 #pragma unroll 1
-          for (int e = lane; e < (kKeys - r0) * (D / 8); e += 32) {
-            const int r = r0 + e / (D / 8), c = e % (D / 8);
+          for (int e = lane; e < (own + kKeys - past) * (D / 8); e += 32) {
+            const int r_ = e / (D / 8), r = r_ < own ? r_ : r_ - own + past, c = e % (D / 8);
             const int at = (c >> 3) * (kKeys * 128) + r * 128 + (c & 7) * 16;
             *reinterpret_cast<uint4*>(sm.k[st] + at) = make_uint4(0, 0, 0, 0);
             *reinterpret_cast<uint4*>(sm.v[sv] + at) = make_uint4(0, 0, 0, 0);
@@ -887,9 +926,11 @@ int make_pages_map(CUtensorMap* map, const void* p, int rows, long long planes, 
 // The e4m3 rows that the tile kernel's sequences need, as bf16 (exact), in front of their new tokens: row
 // c0 + (s + 1) kv_pad - 64 + p - pos0 of [rows][H_kv][D] holds position p of sequence s. A block takes 64 positions of one
 // KV head, from the window of its widest head on.
+// What no head of the group reaches is none of the sequence's any more, whatever the table says: its pages' rows are zeros.
 template <int D>
-__global__ void __launch_bounds__(256) gather_kernel(SeqArgs sq, PageArgs pg, const int32_t* __restrict__ spans, int H, int few,
-                                                     int kv_pad, __nv_bfloat16* __restrict__ K, __nv_bfloat16* __restrict__ V,
+__global__ void __launch_bounds__(256) gather_kernel(SeqArgs sq, PageArgs pg, const int32_t* __restrict__ spans,
+                                                     const double* __restrict__ table, int H, int s, int few, int kv_pad,
+                                                     __nv_bfloat16* __restrict__ K, __nv_bfloat16* __restrict__ V,
                                                      uint32_t* __restrict__ err) {
   const int kvh = blockIdx.y, G = H / pg.H_kv, k = kv_pad / kKeys + 2;
   const int si = warp_find(sq.cu, sq.S, 6, k, blockIdx.x);
@@ -897,17 +938,34 @@ __global__ void __launch_bounds__(256) gather_kernel(SeqArgs sq, PageArgs pg, co
   if (q.len <= few) return;
   const int u = (q.pos0 >> 6) - kv_pad / kKeys + static_cast<int>(blockIdx.x) - ((sq.cu[si] >> 6) + k * si);
   const int end = q.pos0 + q.len;
-  const int T128 = (sq.max_len + PLSH_TILE - 1) / PLSH_TILE;
-  int lo = q.pos0;
-  for (int h = 0; h < G; ++h) lo = min(lo, spans[(static_cast<size_t>(kvh * G + h) * T128 + (q.pos0 >> 7)) * 2]);
+  const int T128 = (sq.max_len + PLSH_TILE - 1) / PLSH_TILE, tile = q.pos0 >> 7, next = min(tile + 1, T128 - 1);
+  int lo = q.pos0, sure = q.pos0;  // the group's window begins between these, and at lo where a row tile begins with pos0
+  for (int h = 0; h < G; ++h) {
+    const int32_t* span = spans + static_cast<size_t>(kvh * G + h) * T128 * 2;
+    lo = min(lo, span[2 * tile]);
+    sure = min(sure, span[2 * next]);
+  }
   lo = max(lo, max(0, q.pos0 - (kv_pad - kKeys)));
   if (u < (lo >> 6) || kKeys * u >= end) return;
+  // Rows from the page of the window's first key on are the sequence's. The last blocks of a window look for that key (1.4 us of
+  // the launch's 14.6 for 8 chunks of 512 tokens after 0 to 15,000, 32/8 heads, d 128).
+  int own = lo;
+  if (q.pos0 % PLSH_TILE != 0 && (kKeys * u < sure || next == tile)) {
+    __shared__ int first;
+    if (threadIdx.x == 0) first = q.pos0;
+    __syncthreads();
+    for (int e = threadIdx.x; e < G * s; e += 256)
+      atomicMin(&first, block_begin(Binning::from_table(table + (static_cast<size_t>(kvh) * G * s + e) * 2), q.pos0));
+    __syncthreads();
+    own = first;
+  }
+  own = own >> pg.lg_page << pg.lg_page;
   constexpr int kPer = D / 16;  // 16-byte pieces of a row
   const long long out0 = q.c0 + static_cast<long long>(si + 1) * kv_pad - kKeys - q.pos0;
   for (int e = threadIdx.x; e < kKeys * kPer; e += 256) {
     const int p = kKeys * u + e / kPer, c = e % kPer;
     if (p >= end) break;
-    const long long row = page_row(pg, si, p, kvh, err);
+    const long long row = p >= own ? page_row(pg, si, p, kvh, err) : -1;
     __nv_bfloat16* out[2] = {K + ((out0 + p) * pg.H_kv + kvh) * D + 16 * c, V + ((out0 + p) * pg.H_kv + kvh) * D + 16 * c};
 #pragma unroll
     for (int kv = 0; kv < 2; ++kv) {
@@ -1019,8 +1077,8 @@ int launch_serve_tc(const ServeArgs& a, cudaStream_t st) {
   b.V = v;
   b.ks = b.vs = {static_cast<long long>(a.H_kv) * a.d, a.d};
   const dim3 grid(static_cast<unsigned>(slots), a.H_kv);
-  if (a.d == 128) gather_kernel<128><<<grid, 256, 0, st>>>(a.sq, a.pg, a.spans, a.H, a.few, b.kv_pad, k, v, a.err);
-  else gather_kernel<64><<<grid, 256, 0, st>>>(a.sq, a.pg, a.spans, a.H, a.few, b.kv_pad, k, v, a.err);
+  if (a.d == 128) gather_kernel<128><<<grid, 256, 0, st>>>(a.sq, a.pg, a.spans, a.table, a.H, a.s, a.few, b.kv_pad, k, v, a.err);
+  else gather_kernel<64><<<grid, 256, 0, st>>>(a.sq, a.pg, a.spans, a.table, a.H, a.s, a.few, b.kv_pad, k, v, a.err);
   const cudaError_t e = cudaGetLastError();
   if (e != cudaSuccess) return cuda_fail(e, "gather_kernel launch");
   return launch_types<false>(b, st);

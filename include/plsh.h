@@ -501,12 +501,18 @@ PLSH_API int plsh_attention_bwd_tc(const void* Q, const void* K, const void* V, 
  *     place p % page_size. With k_exp and v_exp, int8
  *     [num_pages][H_kv][page_size], the pages hold e4m3 bytes and a row's
  *     values are byte * 2^exp; with both NULL they hold the call's dtype.
- *     Entries of the table that no position of the call needs are not read.
+ *     Of the table, only entries of positions that the call needs have to be
+ *     valid: those written or read back, and for plsh_paged_fwd the new tokens'
+ *     and those that share a bin with the sequence's first new token, for some
+ *     head and hash. Pages behind that window may be in another's use, and
+ *     their entries may be anything.
  *   - err_dev: PLSH_DEVERR_SEQUENCE for a malformed sequence (it is skipped),
  *     PLSH_DEVERR_PAGE for a needed page outside the table or the pool (a
- *     row is then not written, or read as zeros).
- *   - K and V must be finite: a NaN or an infinity may reach any row of
- *     its own sequence near it, weighted or not, but no other sequence. |V| may
+ *     row is then not written, or read back as zeros; nothing outside the
+ *     pool is read).
+ *   - K and V must be finite, in pages in every place below the sequence's
+ *     end: a NaN or an infinity may reach any row of its own
+ *     sequence near it, weighted or not, but no other sequence. |V| may
  *     be up to 2^80 (weights are summed before they are normalised). Scores
  *     of any finite size are taken, whatever those of keys without weight.
  *   - Two sequences that share pages may read them in one call; a call in

@@ -175,3 +175,64 @@ def test_plans_and_caches_keep_what_they_were_made_of(dtype, d):
     got = plan2.attend_paged(q, cache2, pt, _cu(lens), zero) + plan2.attend_packed(q, k, v, _cu(lens))
     plan2.check()
     assert all(torch.equal(a, b) for a, b in zip(want, got))
+
+
+def _window_start(plan, p):
+    """The lowest position that shares a bin with p, of any head's hashes."""
+    delta, u = (torch.tensor(plan.table_host[..., i]) for i in range(2))
+    j = torch.arange(p + 1, dtype=torch.float64)
+    same = torch.floor((j[:, None, None] + u) / delta) == torch.floor((p + u) / delta)
+    return int(same.flatten(1).any(1).nonzero()[0])
+
+
+BEHIND = [
+    # kind, d, dtype, s, H, H_kv, page, sigma, lens, starts
+    (E4M3, 128, BF16, 20, 4, 2, 16, [0.5, 2.0, 6.0, 15.0], [130, 40, 200, 17], [700, 641, 64, 1005]),
+    (BF16, 128, BF16, 20, 4, 2, 16, [0.5, 2.0, 6.0, 15.0], [130, 40, 200, 17], [700, 641, 64, 1005]),
+    (BF16, 64, BF16, 20, 4, 2, 32, [0.5, 1.0, 1.5, 2.0], [100, 64, 20, 300], [703, 704, 767, 768]),
+    (BF16, 128, BF16, 40, 4, 1, 16, [0.5, 1.0, 9.0, 30.0], [33, 18, 129], [415, 831, 640]),
+    (E4M3, 64, BF16, 33, 6, 2, 64, [1.0, 1.0, 2.0, 20.0, 30.0, 30.0], [18, 140, 64], [900, 640, 1023]),
+    (BF16, 64, BF16, 20, 2, 2, 256, [1.0, 20.0], [30, 260], [900, 600]),
+    (E4M3, 128, BF16, 20, 8, 2, 16, [0.5, 1.0, 2.0, 2.0, 3.0, 3.0, 9.0, 30.0], [1, 3, 8, 1, 2], [900, 641, 64, 63, 400]),
+    (BF16, 64, BF16, 20, 4, 2, 32, [0.5, 1.0, 2.0, 15.0], [1, 3, 8, 1, 16], [900, 641, 64, 63, 400]),
+    (F32, 64, F32, 20, 4, 2, 16, [0.5, 2.0, 6.0, 15.0], [1, 100, 33, 64], [700, 641, 96, 1005]),
+    (E4M3, 128, F32, 40, 2, 1, 32, [1.0, 3.0], [1, 70, 5], [703, 704, 767]),
+    (F32, 64, F32, 20, 16, 4, 16, [0.5 + 0.5 * h for h in range(16)], [600, 500, 700, 550, 640], [701, 640, 96, 1005, 32]),
+]
+
+
+@pytest.mark.parametrize("kind,d,dtype,s,H,H_kv,page,sigma,lens,starts", BEHIND, ids=[str(n) for n in range(len(BEHIND))])
+def test_pages_behind_the_window_may_be_anything(kind, d, dtype, s, H, H_kv, page, sigma, lens, starts):
+    """A server hands on pages that no later token reaches: entries then name nothing, or another sequence's page."""
+    ends = [a + b for a, b in zip(lens, starts)]
+    plan, g = _plan(H, H_kv, max(ends) + 5, d, s, dtype, sigma=sigma), _gen(75)
+    pt, num = _table_of(ends, page, spare=3)
+    cache = _cache(num, H_kv, page, d, kind)   # pages without an owner hold NaN
+    T = sum(ends)
+    cache.append(_randn(g, T, H_kv, d, dtype=dtype), _randn(g, T, H_kv, d, dtype=dtype), pt, _cu(ends), _at(*[0] * len(ends)))
+    K, V = (x.double() for x in cache.read(pt, _cu(ends), _at(*[0] * len(ends)), T, dtype=F32 if cache.quantised else dtype))
+    unowned = [n for n in range(num) if not (pt == n).any()]
+    lost = [_window_start(plan, a) // page for a in starts]
+    assert sum(lost) >= 4
+    q, cu, st = _randn(g, sum(lens), H, d, dtype=dtype), _cu(lens), _at(*starts)
+    for most in (max(lens), None):
+        want = plan.attend_paged(q, cache, pt, cu, st, max_new=most)
+        plan.check()
+        t = at = 0
+        for n, (L, a) in enumerate(zip(lens, starts)):
+            full = plain.sequence(q[t:t + L].double(), K[at:at + a + L], V[at:at + a + L], plan.table_host, a)
+            plain.check(want[0][t:t + L], want[1][t:t + L], full, dtype, f"sequence {n}")
+            t, at = t + L, at + ends[n]
+        for entry in (-1, num, -2 ** 31, unowned[0]):
+            cut = pt.clone()
+            for n, c in enumerate(lost):
+                cut[n, :c] = entry
+            got = plan.attend_paged(q, cache, cut, cu, st, max_new=most)
+            plan.check()
+            assert all(torch.equal(a, b) for a, b in zip(want, got)), entry
+        for n, c in enumerate(lost):  # one page more is needed
+            cut = pt.clone()
+            cut[n, c] = -1
+            plan.attend_paged(q, cache, cut, cu, st, max_new=most)
+            assert plan.device_errors() == ["PAGE"], n
+            plan.reset_errors()
