@@ -1053,8 +1053,17 @@ int launch_types(const ServeArgs& a, cudaStream_t st) {
 // further down than a row's own), and a tile's slack at either end.
 int serve_kv_pad(int max_window) { return ceil_div(max_window + 2 * PLSH_TILE, kKeys) * kKeys; }
 
+// Sequences whose rows the scratch holds at a time. Their lengths are on the device, so each has room for the longest window; a call with
+// more sequences than fit kScratchBytes runs in groups, one after another in the same scratch.
+constexpr size_t kScratchBytes = size_t{2} << 30;
+int serve_group(int S, int H_kv, int d, int kv_pad) {
+  const size_t fit = kScratchBytes / (static_cast<size_t>(kv_pad) * H_kv * d * 4);
+  return fit < 1 ? 1 : fit < static_cast<size_t>(S) ? static_cast<int>(fit) : S;
+}
+
 size_t serve_scratch_bytes(int T, int S, int H_kv, int d, int max_window) {
-  return 2 * (static_cast<size_t>(T) + static_cast<size_t>(S) * serve_kv_pad(max_window)) * H_kv * d * 2;
+  const int kv_pad = serve_kv_pad(max_window);
+  return 2 * (static_cast<size_t>(T) + static_cast<size_t>(serve_group(S, H_kv, d, kv_pad)) * kv_pad) * H_kv * d * 2;
 }
 
 int launch_serve_tc(const ServeArgs& a, cudaStream_t st) {
@@ -1067,8 +1076,9 @@ int launch_serve_tc(const ServeArgs& a, cudaStream_t st) {
   // e4m3 pages: the rows in reach as bf16 in the caller's scratch, then as if they were packed
   ServeArgs b = a;
   b.kv_pad = serve_kv_pad(a.max_window);
-  const long long rows = static_cast<long long>(a.sq.T) + static_cast<long long>(a.sq.S) * b.kv_pad;
-  const long long slots = (a.sq.T >> 6) + static_cast<long long>(a.sq.S) * (b.kv_pad / kKeys + 2);
+  const int group = serve_group(a.sq.S, a.H_kv, a.d, b.kv_pad);
+  const long long rows = static_cast<long long>(a.sq.T) + static_cast<long long>(group) * b.kv_pad;
+  const long long slots = (a.sq.T >> 6) + static_cast<long long>(group) * (b.kv_pad / kKeys + 2);
   if (rows > 0x7fffffffLL || slots > 0x7fffffffLL) return fail(PLSH_ERR_RANGE, "plsh_paged_fwd: too many cached rows in reach");
   b.kv_rows = static_cast<int>(rows);
   __nv_bfloat16* k = static_cast<__nv_bfloat16*>(a.scratch);
@@ -1077,11 +1087,18 @@ int launch_serve_tc(const ServeArgs& a, cudaStream_t st) {
   b.V = v;
   b.ks = b.vs = {static_cast<long long>(a.H_kv) * a.d, a.d};
   const dim3 grid(static_cast<unsigned>(slots), a.H_kv);
-  if (a.d == 128) gather_kernel<128><<<grid, 256, 0, st>>>(a.sq, a.pg, a.spans, a.table, a.H, a.s, a.few, b.kv_pad, k, v, a.err);
-  else gather_kernel<64><<<grid, 256, 0, st>>>(a.sq, a.pg, a.spans, a.table, a.H, a.s, a.few, b.kv_pad, k, v, a.err);
-  const cudaError_t e = cudaGetLastError();
-  if (e != cudaSuccess) return cuda_fail(e, "gather_kernel launch");
-  return launch_types<false>(b, st);
+  for (int s = 0; s < a.sq.S; s += group) {
+    b.sq.cu = a.sq.cu + s;
+    b.sq.start = a.sq.start + s;
+    b.sq.S = a.sq.S - s < group ? a.sq.S - s : group;
+    b.pg.table = a.pg.table + static_cast<long long>(s) * a.pg.width;
+    if (a.d == 128) gather_kernel<128><<<grid, 256, 0, st>>>(b.sq, b.pg, a.spans, a.table, a.H, a.s, a.few, b.kv_pad, k, v, a.err);
+    else gather_kernel<64><<<grid, 256, 0, st>>>(b.sq, b.pg, a.spans, a.table, a.H, a.s, a.few, b.kv_pad, k, v, a.err);
+    const cudaError_t e = cudaGetLastError();
+    if (e != cudaSuccess) return cuda_fail(e, "gather_kernel launch");
+    if (int rc = launch_types<false>(b, st)) return rc;
+  }
+  return PLSH_OK;
 }
 
 }  // namespace plsh

@@ -584,7 +584,11 @@ PLSH_API int plsh_cache_read(const void* k_pages, const void* v_pages, const int
  *             plsh_paged_scratch_bytes(.., the largest of
  *             windows_host) bytes, 16-byte aligned (NULL where that is 0, with
  *             pages of the call's dtype, and for fp32): bf16 copies of the
- *             e4m3 rows that the longer sequences reach. Nothing in it needs clearing.
+ *             e4m3 rows that the longer sequences reach: 4 T H_kv d bytes, and
+ *             room for the longest window of every sequence, up to 2 GiB of it
+ *             (what does not fit runs in groups of sequences, one after
+ *             another; one sequence's window always fits). Nothing in
+ *             it needs clearing.
  */
 PLSH_API size_t plsh_paged_scratch_bytes(int T, int S, int max_new, int H_kv, int d, int max_window);
 PLSH_API int plsh_paged_fwd(const void* Q, int64_t q_token, int64_t q_head, int dtype, int T, int S,

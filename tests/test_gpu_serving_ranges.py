@@ -236,3 +236,42 @@ def test_pages_behind_the_window_may_be_anything(kind, d, dtype, s, H, H_kv, pag
             plan.attend_paged(q, cache, cut, cu, st, max_new=most)
             assert plan.device_errors() == ["PAGE"], n
             plan.reset_errors()
+
+
+def test_many_sequences_under_heads_that_reach_far():
+    """More windows than the scratch holds at a time: three groups of sequences, empty and single-token ones among them."""
+    import alibi_positional_lsh_b200 as m
+    H, H_kv, d, page, S = 8, 8, 128, 64, 40
+    lens = [(17 + 3 * n) % 45 + 1 if n % 4 else n % 8 for n in range(S)]
+    lens[16] = lens[31] = 140
+    starts = [(37 * n) % 300 for n in range(S)]
+    ends = [a + b if b else 0 for a, b in zip(starts, lens)]
+    plan, g = _plan(H, H_kv, 32768, d, 20, BF16, sigma=[20000.0 + 1000 * h for h in range(H)]), _gen(76)
+    assert m.plsh_paged_scratch_bytes(sum(lens), S, 140, H_kv, d, plan.max_window) < S / 2 * 4 * H_kv * d * plan.max_window
+    pt, num = _table_of(ends, page)
+    cache = _cache(num, H_kv, page, d, E4M3)
+    T = sum(ends)
+    cache.append(_randn(g, T, H_kv, d), _randn(g, T, H_kv, d), pt, _cu(ends), _at(*[0] * S))
+    K, V = (x.double() for x in cache.read(pt, _cu(ends), _at(*[0] * S), T, dtype=F32))
+    q = _randn(g, sum(lens), H, d)
+    O, R = plan.attend_paged(q, cache, pt, _cu(lens), _at(*starts), max_new=140)
+    plan.check()
+    cache.check()
+    t = at = 0
+    for n, (L, a) in enumerate(zip(lens, starts)):
+        if L:
+            want = plain.sequence(q[t:t + L].double(), K[at:at + a + L], V[at:at + a + L], plan.table_host, a)
+            plain.check(O[t:t + L], R[t:t + L], want, BF16, f"sequence {n}")
+        t, at = t + L, at + ends[n]
+    # a page missing, and a sequence too long, in the last group
+    cut = pt.clone()
+    last = max(n for n in range(S) if lens[n] > 17)
+    cut[last, 0] = -1
+    plan.attend_paged(q, cache, cut, _cu(lens), _at(*starts), max_new=140)
+    assert plan.device_errors() == ["PAGE"]
+    plan.reset_errors()
+    late = list(starts)
+    late[S - 1] = 32768
+    plan.attend_paged(q, cache, pt, _cu(lens), _at(*late), max_new=140)
+    assert plan.device_errors() == ["SEQUENCE"]
+    plan.reset_errors()

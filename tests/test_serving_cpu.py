@@ -138,3 +138,13 @@ def test_what_the_calls_keep_addresses_of_cannot_be_exchanged(plsh):
             y.t = x.t
     assert copy.deepcopy(x)._at != x._at
     assert issubclass(plsh.PagedCache, _Kept) and issubclass(plsh.PlshServing, _Kept)
+
+
+def test_scratch_does_not_grow_with_all_sequences(plsh):
+    # 64 and 1,024 sequences, one of them perhaps a chunk, with heads that reach back 100,000 tokens; one window is (100,000 + 256) rows up to whole 64
+    one = 4 * 8 * 128 * 100288
+    assert plsh.plsh_paged_scratch_bytes(600, 1, 512, 8, 128, 100_000) == 4 * 600 * 8 * 128 + one
+    for S in (64, 1024):
+        assert one <= plsh.plsh_paged_scratch_bytes(600, S, 512, 8, 128, 100_000) - 4 * 600 * 8 * 128 <= 2 << 30
+    # a window that alone takes more than that
+    assert plsh.plsh_paged_scratch_bytes(600, 64, 512, 64, 128, 100_000) == 8 * (4 * 600 * 8 * 128 + one)
