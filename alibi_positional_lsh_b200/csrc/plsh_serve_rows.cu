@@ -27,7 +27,7 @@
 // block's first token, the beginning b_k of p0's own block follows from the table in closed form (no mask is read for the window, whose
 // load would be one more trip to memory before K and V), the lowest of them is the window's exact end, and
 //   c_ij = popcount({k : b_k <= j} without the hashes that open a block in (p0, i]),
-// one word per key and head and one word per row. The up to 15 keys above p0 are a step of their own,
+// one word per key and head and one word per row. The up to 7 keys above p0 are a step of their own,
 // counted from the masks.
 //
 // What bounds it: a few tokens read so little that the time is the chain of trips to memory (lengths and table; pages;
@@ -46,7 +46,7 @@ using namespace serve;
 
 constexpr int kThreads = 256, kWarps = 8, kRowsMax = 8, kStep = 32;
 constexpr int kCluster = 8;
-constexpr int kTail = 16;        // places above p0 (a block has at most 8 tokens)
+constexpr int kTail = kRowsMax - 1;  // positions above p0, at most (a block has up to 8 tokens)
 constexpr int kChunkSteps = 32;  // steps of 32 keys whose pages a block holds at a time
 constexpr int kMaxSplitHeads = 64;
 constexpr int kMaxGroup = 8;     // query heads of a block (a larger group takes several blocks)
@@ -398,7 +398,7 @@ serve_rows_kernel(ServeArgs a, Split sp) {
   // ---- the keys above p0, one step of the first block's first warp
   if (rank == 0 && warp == w0 && nt > 1) {
     const int at = place(0);
-    if (lane < kTail) {
+    if (lane < 16) {
       const long long row = lane + 1 < nt ? page_row(a.pg, sid, p0 + 1 + lane, kvh, a.err) : -1;
       s_row[at + lane] = row;
       if (kQuant) {

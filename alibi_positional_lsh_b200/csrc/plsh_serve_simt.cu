@@ -52,7 +52,7 @@ __global__ void __launch_bounds__(kThreads) serve_simt_kernel(ServeArgs a, int C
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
   const int mult = a.sq.start ? 2 : 1, slot = blockIdx.x / C, rank = blockIdx.x % C;
   if (warp == 0) {
-    const int s = warp_find(a.sq.cu, a.sq.S, kRows == 64 ? 6 : 5, mult, slot);
+    const int s = warp_find(a.sq.cu, a.sq.S, 5, mult, slot);
     if (lane == 0) sm.sid = s;
   }
   __syncthreads();
@@ -95,12 +95,7 @@ __global__ void __launch_bounds__(kThreads) serve_simt_kernel(ServeArgs a, int C
     const MaskT b1 = kKeys * diag + 32 + lane < end ? bm[kKeys * diag + 32 + lane] : static_cast<MaskT>(0);
     const MaskT u = tiles::warp_prefix_or<MaskT>(b0, lane), v = tiles::warp_prefix_or<MaskT>(b1, lane);
     const MaskT w = static_cast<MaskT>(__shfl_sync(0xffffffffu, u, 31) | v);
-    if (kRows == 64) {
-      sm.own[lane] = u;
-      sm.own[kRows - 32 + lane] = w;
-    } else {
-      sm.own[lane] = i0 & 32 ? w : u;
-    }
+    sm.own[lane] = i0 & 32 ? w : u;
   }
   if (t0 == 0)  // the counts in the diagonal tile are the plan's
     for (int e = tid; e < kRows * (kKeys / 16); e += kThreads) {

@@ -196,6 +196,7 @@ BEHIND = [
     (E4M3, 128, BF16, 20, 8, 2, 16, [0.5, 1.0, 2.0, 2.0, 3.0, 3.0, 9.0, 30.0], [1, 3, 8, 1, 2], [900, 641, 64, 63, 400]),
     (BF16, 64, BF16, 20, 4, 2, 32, [0.5, 1.0, 2.0, 15.0], [1, 3, 8, 1, 16], [900, 641, 64, 63, 400]),
     (F32, 64, F32, 20, 4, 2, 16, [0.5, 2.0, 6.0, 15.0], [1, 100, 33, 64], [700, 641, 96, 1005]),
+    (E4M3, 128, BF16, 20, 2, 1, 16, [1.0, 9.0], [20, 33], [800, 927]),   # in the plan's last row tile
     (E4M3, 128, F32, 40, 2, 1, 32, [1.0, 3.0], [1, 70, 5], [703, 704, 767]),
     (F32, 64, F32, 20, 16, 4, 16, [0.5 + 0.5 * h for h in range(16)], [600, 500, 700, 550, 640], [701, 640, 96, 1005, 32]),
 ]
