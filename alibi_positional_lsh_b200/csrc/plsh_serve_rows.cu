@@ -46,7 +46,7 @@ using namespace serve;
 
 constexpr int kThreads = 256, kWarps = 8, kRowsMax = 8, kStep = 32;
 constexpr int kCluster = 8;
-constexpr int kTail = kRowsMax - 1;  // positions above p0, at most (a block has up to 8 tokens)
+constexpr int kTail = kRowsMax;  // places above p0 (of which a block's up to 8 tokens use 7)
 constexpr int kChunkSteps = 32;  // steps of 32 keys whose pages a block holds at a time
 constexpr int kMaxSplitHeads = 64;
 constexpr int kMaxGroup = 8;     // query heads of a block (a larger group takes several blocks)

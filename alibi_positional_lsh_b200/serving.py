@@ -128,15 +128,18 @@ class _Kept:
         raise NotImplementedError
 
     def _fix(self) -> None:
-        self.__dict__.update(self._keep(), _fixed=True)
+        self.__dict__.update(self._keep())
+        self.__dict__.setdefault("_fixed", frozenset(self.__dict__) | {"_fixed"})  # not what a caller adds later
 
     def __setattr__(self, name: str, value) -> None:
-        if "_fixed" in self.__dict__ and name in self.__dict__:
+        if name in self.__dict__.get("_fixed", ()):
             raise AttributeError(f"{name} cannot be exchanged: the calls go on with what the object was made of")
         super().__setattr__(name, value)
 
     def __delattr__(self, name: str) -> None:
-        raise AttributeError(f"{name} cannot be taken out")
+        if name in self.__dict__.get("_fixed", ()):
+            raise AttributeError(f"{name} cannot be taken out: the calls go on with what the object was made of")
+        super().__delattr__(name)
 
     def __setstate__(self, state: dict) -> None:  # copies and pickles: other tensors, other addresses
         self.__dict__.update(state)

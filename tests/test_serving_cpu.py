@@ -132,10 +132,14 @@ def test_what_the_calls_keep_addresses_of_cannot_be_exchanged(plsh):
         with pytest.raises(AttributeError):
             delattr(x, name)
     x.note = "the caller's own"
+    x.note = "which may change"
+    x.other = 1
+    del x.other
     for y in (copy.copy(x), copy.deepcopy(x)):
         assert y._at == y.t.data_ptr() and torch.equal(y.t, x.t) and y.note == x.note
         with pytest.raises(AttributeError):
             y.t = x.t
+        y.note = "again"
     assert copy.deepcopy(x)._at != x._at
     assert issubclass(plsh.PagedCache, _Kept) and issubclass(plsh.PlshServing, _Kept)
 
