@@ -23,10 +23,11 @@
 // Per key tile g:
 //   MMA      S(g) = Q K^T once S(g - 1) has been read,  O += P(g - 1) V,  C(g) = A B^T
 //   softmax  P = 4c 2^(S log2e/sqrt(d) - m);  l += sum P
-// The reference m starts at 0 and changes only where a row leaves the range it is good for: its sum above 2^40, or, in
+// The reference m starts at 0 and changes only where a row leaves the range it is good for: its sum above 2^62, or, in
 // the tile of the row's own key (which has the largest count), below 2^-30 as soon as a key with weight is in it. fp32 and bf16
-// hold P between these limits with full relative precision, and 2^40 leaves P V room in fp32 for any |V| up to 2^80, so no
-// maximum is taken otherwise; these 32 keys are then done
+// hold P between these limits with full relative precision, and 2^62 leaves P V room in fp32 for any |V| up to 2^64, so no
+// maximum is taken otherwise (a limit of 2^40, with room up to 2^80: scores around 15 +- 3, 24 prompts as below, 292 us instead of
+// 154); these 32 keys are then done
 // again with m = the maximum over those with c > 0, and what was summed before follows by the same power of two. Keys that
 // come before the own one in its tile may hold all of the row's weight: below 2^-126 their P would be zero, and nothing
 // could bring it back. No score of a key without weight can push a row's weights out of range.
@@ -67,7 +68,7 @@ constexpr int kRows = 128, kKeys = 64;
 constexpr int kItems = 4;                     // item descriptors in flight
 constexpr uint32_t kTmemCols = 256;           // half of Tensor Memory: two blocks share an SM
 constexpr uint32_t kColS = 0, kColC = 64, kColO = 128;
-constexpr float kSumMax = 1.0995116e12f, kSumMin = 9.3132257e-10f;  // 2^40, 2^-30
+constexpr float kSumMax = 4.6116860e18f, kSumMin = 9.3132257e-10f;  // 2^62, 2^-30
 constexpr int kMaxSortedHeads = 256;
 constexpr uint64_t kDrainNs = 100000000ull;
 // Registers per thread: 256 x 128 at launch; the softmax warpgroup takes 216, the other one keeps 40 (192 and 64: 7% slower, by spills).
@@ -377,7 +378,7 @@ serve_tc_kernel(const __grid_constant__ CUtensorMap tmap_q, const __grid_constan
           if (!wait_all(&sm.c_full, g)) { ok = false; break; }
           tc_fence_after();
           // P = 4c 2^(S sc - m) against the reference m, whatever S's maximum is: fp32 and bf16 hold P far beyond what the
-          // softmax needs, so m has to be near the maximum only within some 2^30
+          // softmax needs, so m has to be near the maximum only within some 2^60
           float lsum = 0.0f;
           // S and C of both halves into registers at once; S is then free for the next tile's
           uint32_t s0[32], s1[32], c0v[32], c1v[32];

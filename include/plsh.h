@@ -513,7 +513,7 @@ PLSH_API int plsh_attention_bwd_tc(const void* Q, const void* K, const void* V, 
  *   - K and V must be finite, in pages in every place below the sequence's
  *     end: a NaN or an infinity may reach any row of its own
  *     sequence near it, weighted or not, but no other sequence. |V| may
- *     be up to 2^80 (weights are summed before they are normalised). Scores
+ *     be up to 2^64 (weights are summed before they are normalised). Scores
  *     of any finite size are taken, whatever those of keys without weight.
  *   - Two sequences that share pages may read them in one call; a call in
  *     which two tokens are written to one place leaves that row undefined.
