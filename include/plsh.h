@@ -489,7 +489,8 @@ PLSH_API int plsh_attention_bwd_tc(const void* Q, const void* K, const void* V, 
  *     token to the next and X_head from one head to the next, each a
  *     multiple of 16 bytes and at least d (the views that a fused QKV
  *     projection gives, or head-major storage, need no copy). Outputs are
- *     dense [T][H][d] and [T][H].
+ *     dense [T][H][d] and [T][H] and overlap no input. Tensors, pages and
+ *     scratch are 16-byte aligned.
  *   - max_len: positions of the plan: bmask_dev [H][max_len] and
  *     tile_span_dev [H][ceil(max_len/128)][2] come from plsh_window (or
  *     plsh_window_from_table) with n = max_len and causal = 1, once for all
@@ -510,8 +511,8 @@ PLSH_API int plsh_attention_bwd_tc(const void* Q, const void* K, const void* V, 
  *     PLSH_DEVERR_PAGE for a needed page outside the table or the pool (a
  *     row is then not written, or read back as zeros; nothing outside the
  *     pool is read).
- *   - K and V must be finite, in pages in every place below the sequence's
- *     end: a NaN or an infinity may reach any row of its own
+ *   - K and V must be finite, in needed pages in every place below the
+ *     sequence's end: a NaN or an infinity may reach any row of its own
  *     sequence near it, weighted or not, but no other sequence. |V| may
  *     be up to 2^64 (weights are summed before they are normalised). Scores
  *     of any finite size are taken, whatever those of keys without weight.
@@ -572,7 +573,9 @@ PLSH_API int plsh_cache_read(const void* k_pages, const void* v_pages, const int
  * plsh_paged_fwd -- T~ of a chunk of new tokens of every sequence (one token
  * when decoding) against the pages, which hold the sequence's positions up to
  * and including the chunk's own (append first). Results as plsh_packed_fwd,
- * with the pages' K and V.
+ * with the pages' K and V. Against e4m3 pages, bf16 queries of few tokens are
+ * held in f16, scaled by a power of two to a largest magnitude in [1, 2): an
+ * element moves by at most 2^-25 of its row's largest.
  *   max_new   no sequence has more new tokens than this (else
  *             PLSH_DEVERR_SEQUENCE, and it is skipped). The call chooses its kernels by it,
  *             so give the largest length where it is known, or T.
